@@ -165,7 +165,8 @@ int wal_noalloc_status(wal_stream_t stream);
 /* Read and clear the device status word in a workspace header (synchronises
  * `stream`).  Every product call clears the word when it starts, so it reports
  * on the last call that used this workspace.  WAL_OK, WAL_ERR_TIMEOUT, or
- * WAL_ERR_ARG for a token id outside the table (wal_int3_embed). */
+ * WAL_ERR_ARG for a token id outside the table (wal_int3_embed) or an index
+ * value out of range (the cache and attention calls). */
 int wal_device_status(void* ws, wal_stream_t stream);
 
 /* Whole body pass: n_mats products, matrix i reading xs[i] (bf16 [M][K_i]) and
@@ -371,6 +372,146 @@ int wal_int4_gemm(const wal_int4_matrix* m, const uint16_t* X, int M, int ldx, f
  * 512 bytes.  Asynchronous. */
 int wal_int3_embed(const wal_int3_table* t, const int32_t* ids, int M, float* out, void* ws, size_t ws_bytes,
                    wal_stream_t stream);
+
+/* ---- between the q, k, v products and the o product ------------------------
+ * Rotary positions, a paged KV cache and attention.  The model cards describe
+ * a whole-model decode with a KV cache (WAL-Ternary-8B card, Kazakh README:
+ * KV 2048 and 256; WAL2-Ternary-27B card: 25 slots, context 32768) and give no
+ * layout; everything below is this library's.
+ *
+ * Row-major activations as elsewhere: row t of a [T][ld] array is token t,
+ * head h lies in columns h * head_dim .. (h + 1) * head_dim - 1, columns past
+ * the heads are neither read nor written.  Rows are 16-byte aligned: the base
+ * pointer is, and ld is a multiple of 8 (bf16) or 4 (fp32) elements.  q heads
+ * are grouped: n_heads is a multiple of n_kv_heads, and q head h reads K/V
+ * head h / (n_heads / n_kv_heads).  Index arrays (positions, slots, starts,
+ * lengths, tables) are int32 device memory, 4-byte aligned; the library reads
+ * them on the device only, so a captured graph sees their values at replay.
+ *
+ * Index values are checked on the device: one that is out of range never
+ * causes an access outside the caller's buffers.  It records WAL_ERR_ARG in
+ * the workspace status word (wal_device_status), as wal_int3_embed does, and
+ * each entry point says what happens to the rows concerned. */
+enum { WAL_F32 = 0, WAL_BF16 = 1 };                       /* element types of activations */
+enum { WAL_ROPE_HALF = 0, WAL_ROPE_INTERLEAVED = 1 };     /* which columns make a pair */
+enum { WAL_SCALING_NONE = 0, WAL_SCALING_LINEAR = 1, WAL_SCALING_PARTS = 2 };
+enum { WAL_KV_BF16 = 0, WAL_KV_INT8 = 1, WAL_KV_E4M3 = 2 };
+
+/* Rotary positions.  Pair i of a head (i < rot_dim / 2) is columns
+ * (i, i + rot_dim / 2) in the half layout and (2i, 2i + 1) in the interleaved
+ * one; at position p it is turned by p * f_i radians and multiplied by mscale.
+ * Columns from rot_dim on pass through unchanged.  freq holds f_i / 2 pi, the
+ * turns of pair i per position, as 64-bit fixed-point fractions
+ * (round(2^64 f_i / 2 pi)): p * freq modulo 2^64 is then the angle of any
+ * int32 position, negative ones too, with no loss for far ones. */
+typedef struct wal_rope_plan {
+  int32_t head_dim;      /* a multiple of 16 up to 256 */
+  int32_t rot_dim;       /* a multiple of 16, 16 .. head_dim */
+  int32_t layout;        /* WAL_ROPE_HALF or WAL_ROPE_INTERLEAVED */
+  float mscale;
+  const uint64_t* freq;  /* device [rot_dim / 2] */
+} wal_rope_plan;
+
+/* Frequencies for wal_rope_plan (host memory, rot_dim / 2 values) and the
+ * factor on the result.  f_i = base^(-2i / rot_dim), then
+ *   WAL_SCALING_NONE    f_i, mscale 1;
+ *   WAL_SCALING_LINEAR  f_i / factor, mscale 1;
+ *   WAL_SCALING_PARTS   the by-parts interpolation of the YaRN paper (Peng et
+ *     al., 2023): with t = original_len f_i / 2 pi turns over the original
+ *     length and g = clamp((t - slow) / (fast - slow), 0, 1), the frequency is
+ *     (1 - g) f_i / factor + g f_i, and mscale = 0.1 ln(factor) + 1.
+ * base > 1, factor >= 1, original_len > 0, fast > slow >= 0 (those a scaling
+ * does not use are ignored).  Host only. */
+int wal_rope_freqs(int rot_dim, double base, int scaling, double factor, double original_len, double slow,
+                   double fast, uint64_t* freq, float* mscale);
+
+/* Y[t][h] = rotate(X[t][h], positions[t]) for T >= 0 rows of n_heads heads.
+ * X is fp32 or bf16 (x_type), Y bf16, rounded once.  Y may be X itself when
+ * X is bf16 and ldy == ldx (each pair is read before it is written); any other
+ * overlap is not allowed.  Asynchronous. */
+int wal_rope(const wal_rope_plan* rope, const void* X, int x_type, int T, int n_heads, int ldx,
+             const int32_t* positions, uint16_t* Y, int ldy, wal_stream_t stream);
+
+/* A paged KV cache.  Page p holds page_size token slots of every K/V head:
+ *   k, v               [n_pages][n_heads][page_size][head_dim] of `type`;
+ *   k_scale, v_scale   fp32 [n_pages][n_heads][page_size], NULL for bf16.
+ * A value is its code, times the scale of its (slot, head) row in the 8-bit
+ * types: int8 codes in [-127, 127], or e4m3 codes (finite ones; the two NaN
+ * codes are never written and not read as NaN).  Buffers are 16-byte aligned.
+ * head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; n_pages * page_size
+ * below 2^31.  K and V are the caller's; slots nobody wrote may hold anything,
+ * and no entry point reads past a sequence's length. */
+typedef struct wal_kv_cache {
+  int32_t n_pages, page_size, n_heads, head_dim, type;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} wal_kv_cache;
+
+/* Bytes of k, v, k_scale and v_scale (the last two 0 for bf16).  Host only;
+ * fails as described above for a shape or type that is not supported. */
+int wal_kv_cache_sizes(int n_pages, int page_size, int n_heads, int head_dim, int type, size_t out_bytes[4]);
+
+/* Write T new tokens: row t of K and V (fp32 or bf16, in_type) goes to slot
+ * slots[t] = page * page_size + offset, K rotated by `rope` at positions[t]
+ * first (rope NULL: as it is, positions ignored).  bf16 caches round once;
+ * the 8-bit types keep, per (token, head) row of K or V,
+ *   scale = max(amax / qmax, 2^-126), code = round(x / scale) to nearest even,
+ * qmax = 127 (int8) or 448 (e4m3), all from the fp32 values.  A row with a NaN
+ * or an infinity gets codes 0 and the scale NaN: it reads back as NaN.
+ * slots[t] = -1 skips the row (a padded batch); any other value outside
+ * [0, n_pages * page_size) is skipped and records WAL_ERR_ARG.  Two rows of a
+ * call must not name the same slot.  ws: at least 512 bytes.  Asynchronous. */
+int wal_kv_append(const wal_kv_cache* cache, const void* K, const void* V, int in_type, int T, int ldk, int ldv,
+                  const int32_t* slots, const int32_t* positions, const wal_rope_plan* rope, void* ws,
+                  size_t ws_bytes, wal_stream_t stream);
+
+/* Read B sequences back: token j of sequence b, for j < start[b + 1] - start[b],
+ * lies in page table[b * ld_table + j / page_size] at j % page_size and goes
+ * to row start[b] + j of K and V (fp32 or bf16, out_type; one rounding to
+ * bf16).  K or V may be NULL to skip it.  max_len bounds the lengths and
+ * ceil(max_len / page_size) <= ld_table; T is the number of rows in K and V.
+ * A sequence whose start values do not increase, leave [0, T] or span more than
+ * max_len tokens writes nothing, a page id outside [0, n_pages) gives zero
+ * rows; both record WAL_ERR_ARG.  ws: at least 512 bytes.  Asynchronous. */
+int wal_kv_read(const wal_kv_cache* cache, const int32_t* table, int ld_table, const int32_t* start, int B,
+                int max_len, void* K, void* V, int out_type, int T, int ldk, int ldv, void* ws, size_t ws_bytes,
+                wal_stream_t stream);
+
+/* Scratch bytes of wal_attn_paged: the 256-byte header, and partial results
+ * where the keys of a sequence are split over CTAs.  0 on a bad argument. */
+size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q, int max_kv);
+
+/* Attention of new tokens over the cache that holds them already.  Rows
+ * q_start[b] .. q_start[b + 1] - 1 of Q (bf16 [T][ldq]) are the last tokens of
+ * sequence b, whose kv_len[b] tokens lie in the pages of its table row: new
+ * token i sees the keys j <= kv_len[b] - (q_start[b + 1] - q_start[b]) + i.
+ *   O[t][h] = sum_j softmax_j(scale * Q[t][h] . K[j]) V[j]       (bf16 [T][ldo])
+ * with the maximum, the sum and the accumulators in fp32, and each softmax
+ * weight rounded to bf16 for its product with V.  A row that sees no key gets
+ * zeros.  Keys a row does not see never reach it, whatever they hold.
+ * 1 <= B <= 65535; max_q >= 1 and max_kv >= 1 bound the lengths (they size the grid and
+ * the workspace), ceil(max_kv / page_size) <= ld_table.  Rows of no sequence
+ * (before q_start[0] or from q_start[B] on) are left as they are.
+ * A sequence whose starts decrease or leave [0, T], with more than max_q new
+ * tokens, or with kv_len outside [0, max_kv] is left out, its rows unwritten;
+ * a page id outside [0, n_pages) makes its sequence's rows unspecified; both
+ * record WAL_ERR_ARG.  n_heads / n_kv_heads <= 128.  O must not overlap Q.
+ * Results do not depend on timing (no atomics on values).  Asynchronous. */
+int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
+                   const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,
+                   int max_q, int max_kv, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
+                   wal_stream_t stream);
+
+/* Causal attention over whole prompts, packed one after another: rows
+ * start[b] .. start[b + 1] - 1 of Q, K, V and O (bf16) are sequence b, and its
+ * token i sees its tokens 0 .. i.  Formula, types, bounds and reports as in
+ * wal_attn_paged with max_len in the place of max_q.  head_dim 64 or 128.
+ * ws: at least 512 bytes.  Asynchronous. */
+int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
+                    int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B, int max_len,
+                    float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes, wal_stream_t stream);
 
 const char* wal_status_string(int status);
 const char* wal_last_error(void);

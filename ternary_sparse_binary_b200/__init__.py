@@ -19,5 +19,11 @@ from ._abi import (  # noqa: F401
     wal_rc1_body_workspace_bytes, wal_rc1_body_pass,
     wal_int4_matrix, wal_int3_table, wal_int4_sizes, wal_int3_sizes, wal_int4_pack, wal_int3_pack,
     wal_int4_workspace_bytes, wal_int4_gemm, wal_int3_embed,
+    WAL_F32, WAL_BF16, WAL_ROPE_HALF, WAL_ROPE_INTERLEAVED, WAL_SCALING_NONE, WAL_SCALING_LINEAR, WAL_SCALING_PARTS,
+    WAL_KV_BF16, WAL_KV_INT8, WAL_KV_E4M3, wal_rope_plan, wal_kv_cache,
+    wal_rope_freqs, wal_rope, wal_kv_cache_sizes, wal_kv_append, wal_kv_read,
+    wal_attn_paged_workspace_bytes, wal_attn_paged, wal_attn_prompt,
 )
 from .packed import PackedMatrix, Pq2Matrix, Rc1Matrix, pack_host, pack_pq2_host, to_device, BodyPass  # noqa: F401
+from . import attention  # noqa: F401
+from .attention import Rope, KvCache, attn_prompt  # noqa: F401

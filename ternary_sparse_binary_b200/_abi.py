@@ -20,6 +20,10 @@ WAL_ERR_TIMEOUT = -7
 WAL_MAX_RANK = 32
 WAL_MAX_SMALL_M = 16
 WAL_NOALLOC_SCRATCH_BYTES = 16 << 20
+WAL_F32, WAL_BF16 = 0, 1
+WAL_ROPE_HALF, WAL_ROPE_INTERLEAVED = 0, 1
+WAL_SCALING_NONE, WAL_SCALING_LINEAR, WAL_SCALING_PARTS = 0, 1, 2
+WAL_KV_BF16, WAL_KV_INT8, WAL_KV_E4M3 = 0, 1, 2
 
 EXPORTED_SYMBOLS = [
     "wal_packed_sizes", "wal_pack_matrix", "wal_validate", "wal_unpack_matrix",
@@ -32,6 +36,8 @@ EXPORTED_SYMBOLS = [
     "wal_rc1_body_workspace_bytes", "wal_rc1_body_pass",
     "wal_int4_sizes", "wal_int3_sizes", "wal_int4_pack", "wal_int3_pack", "wal_int4_workspace_bytes",
     "wal_int4_gemm", "wal_int3_embed",
+    "wal_rope_freqs", "wal_rope", "wal_kv_cache_sizes", "wal_kv_append", "wal_kv_read",
+    "wal_attn_paged_workspace_bytes", "wal_attn_paged", "wal_attn_prompt",
     "wal_status_string", "wal_last_error",
 ]
 
@@ -64,6 +70,17 @@ class wal_int3_table(ctypes.Structure):
 
 class wal_pq2_matrix(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("blocks", ctypes.c_void_p)]
+
+
+class wal_rope_plan(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("freq", ctypes.c_void_p)]
+
+
+class wal_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 def _load():
@@ -129,6 +146,17 @@ lib.wal_int4_workspace_bytes.argtypes = [ctypes.POINTER(wal_int4_matrix), _i]
 lib.wal_int4_workspace_bytes.restype = _sz
 lib.wal_int4_gemm.argtypes = [ctypes.POINTER(wal_int4_matrix), _vp, _i, _i, _vp, _i, _vp, _sz, _vp]
 lib.wal_int3_embed.argtypes = [ctypes.POINTER(wal_int3_table), _vp, _i, _vp, _vp, _sz, _vp]
+_dbl, _f = ctypes.c_double, ctypes.c_float
+_CP, _OP = ctypes.POINTER(wal_kv_cache), ctypes.POINTER(wal_rope_plan)
+lib.wal_rope_freqs.argtypes = [_i, _dbl, _i, _dbl, _dbl, _dbl, _dbl, _vp, ctypes.POINTER(_f)]
+lib.wal_rope.argtypes = [_OP, _vp, _i, _i, _i, _i, _vp, _vp, _i, _vp]
+lib.wal_kv_cache_sizes.argtypes = [_i, _i, _i, _i, _i, ctypes.POINTER(_sz)]
+lib.wal_kv_append.argtypes = [_CP, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _OP, _vp, _sz, _vp]
+lib.wal_kv_read.argtypes = [_CP, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp]
+lib.wal_attn_paged_workspace_bytes.argtypes = [_CP, _i, _i, _i, _i, _i]
+lib.wal_attn_paged_workspace_bytes.restype = _sz
+lib.wal_attn_paged.argtypes = [_CP, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
+lib.wal_attn_prompt.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
 lib.wal_status_string.argtypes = [_i]
 lib.wal_status_string.restype = ctypes.c_char_p
 lib.wal_last_error.argtypes = []
@@ -331,3 +359,49 @@ def wal_int4_gemm(m, X, M, ldx, Y, ldy, ws, ws_bytes, stream):
 
 def wal_int3_embed(t, ids, M, out, ws, ws_bytes, stream):
     return _check(lib.wal_int3_embed(ctypes.byref(t), ids, M, out, ws, ws_bytes, stream), "wal_int3_embed")
+
+
+def wal_rope_freqs(rot_dim, base, scaling, factor, original_len, slow, fast, freq):
+    """Fills freq (host pointer to rot_dim / 2 uint64); returns mscale."""
+    m = _f()
+    _check(lib.wal_rope_freqs(rot_dim, base, scaling, factor, original_len, slow, fast, freq, ctypes.byref(m)),
+           "wal_rope_freqs")
+    return m.value
+
+
+def wal_rope(rope, X, x_type, T, n_heads, ldx, positions, Y, ldy, stream):
+    return _check(lib.wal_rope(ctypes.byref(rope), X, x_type, T, n_heads, ldx, positions, Y, ldy, stream), "wal_rope")
+
+
+def wal_kv_cache_sizes(n_pages, page_size, n_heads, head_dim, type):
+    out = (_sz * 4)()
+    _check(lib.wal_kv_cache_sizes(n_pages, page_size, n_heads, head_dim, type, out), "wal_kv_cache_sizes")
+    return [int(v) for v in out]
+
+
+def wal_kv_append(cache, K, V, in_type, T, ldk, ldv, slots, positions, rope, ws, ws_bytes, stream):
+    """rope: a wal_rope_plan, or None to store K as it is."""
+    return _check(lib.wal_kv_append(ctypes.byref(cache), K, V, in_type, T, ldk, ldv, slots, positions,
+                                    ctypes.byref(rope) if rope is not None else None, ws, ws_bytes, stream),
+                  "wal_kv_append")
+
+
+def wal_kv_read(cache, table, ld_table, start, B, max_len, K, V, out_type, T, ldk, ldv, ws, ws_bytes, stream):
+    return _check(lib.wal_kv_read(ctypes.byref(cache), table, ld_table, start, B, max_len, K, V, out_type, T, ldk,
+                                  ldv, ws, ws_bytes, stream), "wal_kv_read")
+
+
+def wal_attn_paged_workspace_bytes(cache, n_heads, T, B, max_q, max_kv):
+    return int(lib.wal_attn_paged_workspace_bytes(ctypes.byref(cache), n_heads, T, B, max_q, max_kv))
+
+
+def wal_attn_paged(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo, ws,
+                   ws_bytes, stream):
+    return _check(lib.wal_attn_paged(ctypes.byref(cache), Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B,
+                                     max_q, max_kv, scale, O, ldo, ws, ws_bytes, stream), "wal_attn_paged")
+
+
+def wal_attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len, scale, O, ldo, ws,
+                    ws_bytes, stream):
+    return _check(lib.wal_attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len,
+                                      scale, O, ldo, ws, ws_bytes, stream), "wal_attn_prompt")
