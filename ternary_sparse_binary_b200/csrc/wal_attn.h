@@ -24,7 +24,16 @@ struct AttnParams {
   int T, B, max_q, max_kv;
   float scale_log2;          // scale * log2(e)
   int32_t* status;
+  // keys split over CTAs: split s holds keys [s * split_keys, (s + 1) * split_keys)
+  int n_split, split_keys;
+  float* part_o;             // n_split > 1: [n_split][T * n_heads][head_dim], sums of w v
+  float2* part_ml;           // [n_split][T * n_heads]: {m, l}, m in units of log2
 };
+
+// Whether the call goes to the tensor-core kernel (wal_attn_tc.cu), and its launch.
+bool attn_uses_tc(int max_q, int group);
+constexpr int kTcAttnRows = 256;  // query rows of one CTA there
+int launch_attn_tc(const AttnParams& p, cudaStream_t stream);
 
 // Sequence b as its index arrays give it; n_q = 0 where they are out of range.
 struct AttnSeq {
@@ -55,6 +64,94 @@ __device__ __forceinline__ int64_t attn_page_row(const AttnParams& p, int b, int
     page = 0;
   }
   return (((int64_t)page * p.n_kv_heads + h) << p.shift) + (j & ((1 << p.shift) - 1));
+}
+
+// Row of a query in the partial results.
+__device__ __forceinline__ int64_t attn_part_row(const AttnParams& p, const AttnSeq& s, int tok, int head) {
+  return (int64_t)(s.q0 + tok) * p.n_heads + head;
+}
+
+// One row by one warp, in fp32: lane i holds columns [i * VPL, (i + 1) * VPL).
+// Only visible keys are touched, and a non-finite one among them acts as in
+// the formula: a NaN score, a +inf score, scores that are all -inf, or a
+// non-finite value under any weight give NaN.  The kernels below come back to
+// it for a row that a key of its tile turned into NaN without being visible
+// (its weight is 0, but 0 * NaN is NaN).
+template <int D>
+__device__ __noinline__ void attend_row(const AttnParams& p, const AttnSeq& s, int b, int head, int tok) {
+  constexpr int VPL = D / 32;
+  const int lane = threadIdx.x & 31, h = head / p.group;
+  const int lim = attn_limit(s, tok);
+  float q[VPL], acc[VPL];
+  const uint16_t* qr = p.Q + (s.q0 + tok) * p.ldq + head * D + lane * VPL;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    q[i] = __uint_as_float((uint32_t)qr[i] << 16);
+    acc[i] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  for (int j = 0; j < lim; ++j) {
+    float k[VPL], v[VPL];
+    if (p.table && p.type != WAL_KV_BF16) {
+      const int64_t row = attn_page_row(p, b, h, j);
+      const uint8_t* kc = static_cast<const uint8_t*>(p.k) + row * D + lane * VPL;
+      const uint8_t* vc = static_cast<const uint8_t*>(p.v) + row * D + lane * VPL;
+      const float ks = p.ks[row], vs = p.vs[row];
+      uint32_t kw = 0, vw = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        kw |= (uint32_t)kc[i] << (8 * i);
+        vw |= (uint32_t)vc[i] << (8 * i);
+      }
+      float kf[4], vf[4];
+      if (p.type == WAL_KV_INT8) {
+        dev::codes4_to_float<WAL_KV_INT8>(kw, kf);
+        dev::codes4_to_float<WAL_KV_INT8>(vw, vf);
+      } else {
+        dev::codes4_to_float<WAL_KV_E4M3>(kw, kf);
+        dev::codes4_to_float<WAL_KV_E4M3>(vw, vf);
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        k[i] = kf[i] * ks;
+        v[i] = vf[i] * vs;
+      }
+    } else {
+      const uint16_t *kr, *vr;
+      if (p.table) {
+        const int64_t row = attn_page_row(p, b, h, j);
+        kr = static_cast<const uint16_t*>(p.k) + row * D;
+        vr = static_cast<const uint16_t*>(p.v) + row * D;
+      } else {
+        kr = static_cast<const uint16_t*>(p.k) + (int64_t)(s.q0 + j) * p.ldk + h * D;
+        vr = static_cast<const uint16_t*>(p.v) + (int64_t)(s.q0 + j) * p.ldv + h * D;
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        k[i] = __uint_as_float((uint32_t)kr[lane * VPL + i] << 16);
+        v[i] = __uint_as_float((uint32_t)vr[lane * VPL + i] << 16);
+      }
+    }
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x += q[i] * k[i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    x *= p.scale_log2;
+    const float mn = fmaxf(m, x);
+    const float c = m == -INFINITY ? 1.f : exp2f(m - mn);  // nothing summed yet, or only weights of zero
+    const float w = x == -INFINITY ? 0.f : exp2f(x - mn);
+    m = mn;
+    l = l * c + w;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = acc[i] * c + w * v[i];
+  }
+  uint16_t* o = p.O + (s.q0 + tok) * p.ldo + head * D + lane * VPL;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const float y = lim == 0 ? 0.f : acc[i] / l;
+    o[i] = (uint16_t)(dev::float2_to_bf16x2(y, 0.f) & 0xFFFFu);
+  }
 }
 
 }  // namespace wal

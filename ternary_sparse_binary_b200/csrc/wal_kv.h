@@ -48,5 +48,25 @@ __device__ __forceinline__ void codes4_to_float(uint32_t w, float (&v)[4]) {
   }
 }
 
+// The same as bf16 pairs: lo = codes 0 and 1, hi = codes 2 and 3.  Both types are
+// exact in bf16.
+template <int TYPE>
+__device__ __forceinline__ void codes4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (TYPE == WAL_KV_INT8) {
+    // byte b = 128 s + u stands for u - 128 s.  As the low byte of 0x43xx, u
+    // reads 128 + u and the sign bit alone 128 or 256: their difference.
+    const uint32_t t0 = __byte_perm(w, 0x43434343u, 0x4140), t1 = __byte_perm(w, 0x43434343u, 0x4342);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(t0 & 0xFF7FFF7Fu), "r"(t0 & 0xFF80FF80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(t1 & 0xFF7FFF7Fu), "r"(t1 & 0xFF80FF80u));
+  } else {
+    // s eeee mmm moved to the sign, the low exponent bits and the high mantissa
+    // bits reads 2^-120 times the value, subnormals too
+    const uint32_t t0 = __byte_perm(w, 0, 0x1404), t1 = __byte_perm(w, 0, 0x3424);
+    const uint32_t e = 0x7B807B80u;  // 2^120 as a bf16 pair
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"((t0 & 0x80008000u) | ((t0 >> 4) & 0x07F007F0u)), "r"(e));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"((t1 & 0x80008000u) | ((t1 >> 4) & 0x07F007F0u)), "r"(e));
+  }
+}
+
 }  // namespace dev
 }  // namespace wal
