@@ -1,4 +1,4 @@
-// Attention entry points and the kernels that run on CUDA cores.
+// Attention entry points, the single-token kernel and the sum over splits.
 //
 //   O[t][h] = sum_j softmax_j(scale * Q[t][h] . K[j]) V[j]
 //
@@ -353,18 +353,6 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
 
 // Add the splits of a row in order: one warp a row.
 template <int D>
-__global__ void __launch_bounds__(32 * kRowWarps) attn_rows_kernel(const __grid_constant__ AttnParams p) {
-  const int b = blockIdx.z;
-  const AttnSeq s = attn_seq(p, b);
-  if (s.bad) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
-    return;
-  }
-  const int head = blockIdx.y * kRowWarps + (threadIdx.x >> 5);
-  if ((int)blockIdx.x < s.n_q && head < p.n_heads) attend_row<D>(p, s, b, head, blockIdx.x);
-}
-
-template <int D>
 __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __grid_constant__ AttnParams p) {
   constexpr int VPL = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -464,13 +452,9 @@ int64_t attn_ctas(int B, int n_kv_heads, int64_t rows) {
 }
 
 int launch_attn(const AttnParams& p, cudaStream_t stream) {
-  if (!p.table || attn_uses_tc(p.max_q, p.group)) {
-    const dim3 grid((unsigned)p.max_q, (unsigned)((p.n_heads + kRowWarps - 1) / kRowWarps), (unsigned)p.B);
-    if (p.head_dim == 64)
-      attn_rows_kernel<64><<<grid, 32 * kRowWarps, 0, stream>>>(p);
-    else
-      attn_rows_kernel<128><<<grid, 32 * kRowWarps, 0, stream>>>(p);
-    return launched(cudaGetLastError(), "attn_rows_kernel");
+  if (!p.table || (int64_t)p.max_q * p.group > kDecMaxRows) {
+    const int st = launch_attn_tc(p, stream);
+    return st || p.n_split == 1 ? st : launch_combine(p, stream);
   }
   const dim3 grid((unsigned)p.n_split, (unsigned)p.n_kv_heads, (unsigned)p.B);
   const bool wide = p.head_dim == 128;
@@ -484,8 +468,6 @@ int launch_attn(const AttnParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
-
-bool attn_uses_tc(int max_q, int group) { return (int64_t)max_q * group > kDecMaxRows; }
 
 }  // namespace wal
 
@@ -566,6 +548,7 @@ extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint1
   p.n_heads = n_heads; p.n_kv_heads = n_kv_heads; p.group = n_heads / n_kv_heads;
   p.head_dim = head_dim; p.type = WAL_KV_BF16;
   p.T = T; p.B = B; p.max_q = p.max_kv = max_len < T ? max_len : T;
+  p.n_split = 1; p.split_keys = p.max_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
   return launch_attn(p, s);
 }

@@ -30,8 +30,7 @@ struct AttnParams {
   float2* part_ml;           // [n_split][T * n_heads]: {m, l}, m in units of log2
 };
 
-// Whether the call goes to the tensor-core kernel (wal_attn_tc.cu), and its launch.
-bool attn_uses_tc(int max_q, int group);
+// The tensor-core kernel (wal_attn_tc.cu).
 constexpr int kTcAttnRows = 256;  // query rows of one CTA there
 int launch_attn_tc(const AttnParams& p, cudaStream_t stream);
 
