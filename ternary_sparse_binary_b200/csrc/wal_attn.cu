@@ -94,10 +94,12 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const AttnSeq s = attn_seq(p, b);
-  if (s.bad) {
-    if (split == 0 && h == 0 && threadIdx.x == 0) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
-    return;
+  if (p.clear) {
+    if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
+  } else if (s.bad && h == 0 && threadIdx.x == 0) {
+    atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   }
+  if (s.bad) return;
   const int rows = s.n_q * p.group;
   const int k0 = split * p.split_keys, k1 = min(s.len, k0 + p.split_keys);
   if (rows == 0 || (k0 >= k1 && split > 0)) return;  // split 0 also answers for a sequence without keys
@@ -351,13 +353,20 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
   }
 }
 
-// Add the splits of a row in order: one warp a row.
+// Add the splits of a row in order, one warp a row, and report index values out
+// of range.
 template <int D>
 __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __grid_constant__ AttnParams p) {
   constexpr int VPL = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.z, lane = threadIdx.x & 31;
   const AttnSeq s = attn_seq(p, b);
+  if (blockIdx.x == 0) {  // the first kernel cleared the status word; what it skipped is reported here
+    bool bad = s.bad;
+    const int pages = (s.len + (1 << p.shift) - 1) >> p.shift;
+    for (int i = threadIdx.x; i < pages; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + b * p.ld_table + i) >= (uint32_t)p.n_pages;
+    if (bad) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+  }
   const int row = blockIdx.x * kRowWarps + (threadIdx.x >> 5);  // (token, head)
   if (s.bad || row >= s.n_q * p.n_heads) return;
   const int tok = row / p.n_heads, head = row - tok * p.n_heads;
@@ -503,7 +512,11 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   if ((st = current_device(&dev))) return st;
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
-  if ((st = clear_status(ws, s, &p.status))) return st;
+  const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
+  plan_split(attn_ctas(B, cache->n_heads, rows), max_kv, rows > kDecMaxRows, &p.n_split, &p.split_keys);
+  p.clear = T > 0 && p.n_split > 1;
+  p.status = status_word(ws);
+  if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
   if (T == 0) return WAL_OK;
   p.Q = Q; p.O = O;
   p.k = cache->k; p.v = cache->v;
@@ -515,8 +528,6 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   p.shift = log2_of(cache->page_size); p.n_pages = cache->n_pages;
   p.T = T; p.B = B; p.max_q = max_q < T ? max_q : T; p.max_kv = max_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int64_t rows = (int64_t)p.max_q * p.group;
-  plan_split(attn_ctas(B, p.n_kv_heads, rows), max_kv, rows > kDecMaxRows, &p.n_split, &p.split_keys);
   char* part = reinterpret_cast<char*>(p.status) + 256;
   p.part_ml = reinterpret_cast<float2*>(part);
   p.part_o = reinterpret_cast<float*>(part + align_up((size_t)p.n_split * T * n_heads * 8, 256));
@@ -539,8 +550,9 @@ extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint1
   if ((st = current_device(&dev))) return st;
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
-  if ((st = clear_status(ws, s, &p.status))) return st;
-  if (T == 0) return WAL_OK;
+  if (T == 0) return clear_status(ws, s, &p.status);
+  p.clear = true;
+  p.status = status_word(ws);
   p.Q = Q; p.O = O;
   p.k = K; p.v = V;
   p.q_start = start;

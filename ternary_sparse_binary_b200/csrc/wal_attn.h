@@ -24,6 +24,10 @@ struct AttnParams {
   int T, B, max_q, max_kv;
   float scale_log2;          // scale * log2(e)
   int32_t* status;
+  // A call that splits its keys clears the status word in its first kernel and
+  // reports index values in its second, a prompt does both in its one kernel,
+  // another call after a memset.
+  bool clear;
   // keys split over CTAs: split s holds keys [s * split_keys, (s + 1) * split_keys)
   int n_split, split_keys;
   float* part_o;             // n_split > 1: [n_split][T * n_heads][head_dim], sums of w v
@@ -54,15 +58,16 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
 // Keys that new token i sees: the first attn_limit(s, i) of the sequence.
 __device__ __forceinline__ int attn_limit(const AttnSeq& s, int i) { return max(0, s.len - s.n_q + i + 1); }
 
-// Row of key j (in units of head_dim elements) in the cache; a page id out of
-// range is recorded and page 0 read in its place.
+// Page of key j; an id out of range is recorded and page 0 read in its place.
+__device__ __forceinline__ int attn_page(const AttnParams& p, int b, int j) {
+  const int page = __ldg(p.table + b * p.ld_table + (j >> p.shift));
+  if ((uint32_t)page < (uint32_t)p.n_pages) return page;
+  if (!p.clear) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+  return 0;
+}
+// Row of key j in the cache (in units of head_dim elements).
 __device__ __forceinline__ int64_t attn_page_row(const AttnParams& p, int b, int h, int j) {
-  int page = __ldg(p.table + b * p.ld_table + (j >> p.shift));
-  if ((uint32_t)page >= (uint32_t)p.n_pages) {
-    atomicExch(p.status, (int32_t)WAL_ERR_ARG);
-    page = 0;
-  }
-  return (((int64_t)page * p.n_kv_heads + h) << p.shift) + (j & ((1 << p.shift) - 1));
+  return (((int64_t)attn_page(p, b, j) * p.n_kv_heads + h) << p.shift) + (j & ((1 << p.shift) - 1));
 }
 
 // Row of a query in the partial results.

@@ -1,21 +1,25 @@
 // Attention of many query rows: tcgen05, over packed prompts or the paged cache.
 //
-// A CTA owns 256 query rows of one K/V head (rows are (token, head of the
-// group), token-major, so the heads that share K and V share its tiles) as two
-// tiles of 128, and walks the keys in tiles of 128:
+// A piece of work is 256 query rows of one K/V head (rows are (token, head of
+// the group), token-major, so the heads that share K and V share its tiles) as
+// two tiles of 128, and a range of keys, in tiles of 128:
 //   S_t = Q_t K^T          128 x 128, K-major operands from shared memory
 //   P_t = 2^(S_t - m)      in registers, one row a thread, back to tensor
 //                          memory as bf16 over S_t's first half
 //   O_t += P_t V           A from tensor memory, V as it lies (MN-major)
 // While one tile's softmax runs on the CUDA cores, the tensor core works on the
-// other's products.  384 threads:
-//   warps 0-3, 4-7   softmax, rescaling and output of tile 0 and 1
+// other's products.  A piece with one tile of rows gives both halves of the CTA
+// that tile and every other key tile each.  CTAs are persistent: each role walks
+// the CTA's pieces by itself, so the loads and the first products of a piece run
+// under the end of the one before.
+//   warps 0-3, 4-7   softmax, rescaling and output of half 0 and 1
 //   warp 8           issues the MMAs (lane 0)
-//   warp 9           bf16 K/V: TMA boxes of whole pages (or packed rows) into a
-//                    ring of K and V tiles in the 128-byte swizzle
-//   warps 9-11       8-bit K/V: plain loads, codes widened to bf16 (exact) and
-//                    stored in the same layout; the key's scales go through a
-//                    small ring of their own and meet S and P in fp32
+//   warp 9           K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
+//                    into a ring in the 128-byte swizzle, 8-bit codes and their
+//                    scales into a ring as they lie
+//   warps 10, 11     Q
+//   warps 12-15      (8-bit) codes to bf16 tiles, exact; scales go to a ring of
+//                    their own and meet S and P in fp32
 // The MMAs of one thread run in order, so S_t of the next keys may overwrite
 // P_t once P_t V has been issued, and a softmax that sees its S_t finished knows
 // that its O_t is too.
@@ -47,19 +51,30 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kTile = 128;      // query rows of a tile, keys of a step
-constexpr int kConv = 96;       // converter threads of an 8-bit cache
-constexpr int kScaleRing = 4;
+constexpr int kScaleRing = 4;   // key tiles whose scales are held at once
+constexpr int kQThreads = 64;   // threads that load Q
 constexpr float kLazy = 8.f;    // growth of the maximum, in log2, that O is rescaled for
+constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobody, so any number is right
 
+// Shared memory and registers.  Launched registers are shared out again by
+// setmaxnreg: 384 threads of 168 as 2 x 128 x 208 + 128 x 88, 512 threads of 128
+// as 2 x 128 x 176 + 2 x 128 x 80.
 template <int D, int TYPE>
 struct Cfg {
-  static constexpr uint32_t tile_bytes = kTile * D * 2;
-  static constexpr int slots = D == 64 ? 8 : TYPE == WAL_KV_BF16 ? 5 : 4;
-  static constexpr uint32_t scale_off = (2 + slots) * tile_bytes;
-  static constexpr uint32_t bar_off = scale_off + (TYPE == WAL_KV_BF16 ? 0 : kScaleRing * 2 * kTile * 4);
-  static constexpr uint32_t smem = bar_off + 512 + 1024;  // barriers, slack for the alignment
+  static constexpr bool codes = TYPE != WAL_KV_BF16;
+  static constexpr int threads = codes ? 512 : 384;
+  static constexpr int soft_regs = codes ? 176 : 208, other_regs = codes ? 80 : 88;
+  static constexpr uint32_t tile = kTile * D * 2;                    // a Q, K or V tile in bf16
+  static constexpr int slots = D == 64 ? (codes ? 6 : 8) : (codes ? 3 : 5);
+  static constexpr uint32_t raw = codes ? kTile * D + kTile * 4 : 0;  // a tile as it lies in the cache, and its scales
+  static constexpr int raws = D == 64 ? 6 : 3;
+  static constexpr uint32_t ring_off = 2 * tile;
+  static constexpr uint32_t raw_off = ring_off + slots * tile;
+  static constexpr uint32_t scale_off = raw_off + (codes ? raws * raw : 0);
+  static constexpr uint32_t ml_off = scale_off + (codes ? kScaleRing * 2 * kTile * 4 : 0);
+  static constexpr uint32_t bar_off = ml_off + kTile * 8;
+  static constexpr uint32_t smem = bar_off + 512 + 1024;             // barriers, slack for the alignment
 };
 
 // Instruction descriptor: A and B bf16, D fp32, M x N; B MN-major if asked.
@@ -100,17 +115,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
-      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
-      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -121,6 +125,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -154,155 +163,258 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 struct Bars {
   uint32_t base;
-  __device__ uint32_t full(int s) const { return base + 8u * s; }
+  __device__ uint32_t full(int s) const { return base + 8u * s; }               // K/V tile ready for the MMAs
   __device__ uint32_t empty(int s) const { return base + 64u + 8u * s; }
-  __device__ uint32_t q_full(int t) const { return base + 128u + 8u * t; }
-  __device__ uint32_t s_full(int t) const { return base + 144u + 8u * t; }
-  __device__ uint32_t p_full(int t) const { return base + 160u + 8u * t; }
-  __device__ uint32_t o_done(int t) const { return base + 176u + 8u * t; }
-  __device__ uint32_t sc_full(int i) const { return base + 192u + 8u * i; }
-  __device__ uint32_t sc_empty(int i) const { return base + 224u + 8u * i; }
-  __device__ uint32_t v_tail() const { return base + 256u; }
-  __device__ uint32_t drained() const { return base + 264u; }
-  __device__ uint32_t tmem_slot() const { return base + 272u; }
+  __device__ uint32_t raw_full(int s) const { return base + 128u + 8u * s; }    // codes ready for the converters
+  __device__ uint32_t raw_empty(int s) const { return base + 176u + 8u * s; }
+  __device__ uint32_t sc_full(int i) const { return base + 224u + 8u * i; }     // scales ready for the softmax
+  __device__ uint32_t sc_empty(int i) const { return base + 256u + 8u * i; }
+  __device__ uint32_t q_full(int t) const { return base + 288u + 8u * t; }
+  __device__ uint32_t q_empty(int t) const { return base + 304u + 8u * t; }
+  __device__ uint32_t s_full(int t) const { return base + 320u + 8u * t; }      // scores in tensor memory
+  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // weights in tensor memory
+  __device__ uint32_t o_done(int t) const { return base + 352u + 8u * t; }      // the last product of a piece
+  __device__ uint32_t ml_full() const { return base + 368u; }                   // the second half's m and l
+  __device__ uint32_t ml_empty() const { return base + 376u; }
+  __device__ uint32_t v_tail() const { return base + 384u; }
+  __device__ uint32_t drained() const { return base + 392u; }
+  __device__ uint32_t tmem_slot() const { return base + 400u; }
 };
 
-// What a CTA works on.
+// The pieces of work of a launch: (query tile pair, split of the keys,
+// sequence, K/V head), the pairs that see most keys first, so that the CTAs,
+// which take every gridDim.x-th piece, get about the same.
+struct Sched {
+  int tiles, splits;  // as many as the longest sequence has
+  __device__ int64_t total(const AttnParams& p) const { return (int64_t)tiles * splits * p.B * p.n_kv_heads; }
+};
+
+// A piece.  With more than one tile of rows, query tile t walks n_t[t] key
+// tiles.  With one (dual), both halves of the CTA walk its keys, half t the key
+// tiles t, t + 2, ..., and their sums are joined at the end.
 struct Work {
   int b, h, split;
   int r0, rows;      // query rows [r0, r0 + rows) of the sequence's head
   int k0, k1, n;     // keys [k0, k1), n tiles
-  int n_t[2];        // key tiles that query tile 0, 1 takes
+  int n0, n1;        // key tiles of half 0 and 1
+  bool dual;
+  __device__ int n_t(int t) const { return t ? n1 : n0; }
+  __device__ bool has_q(int t) const { return t ? n1 > 0 && !dual : n0 > 0; }
+  __device__ int tile_of(int t, int k) const { return dual ? 2 * k + t : k; }
 };
 
-// ---------------------------------------------------------------------------
-// bf16 K/V tiles by TMA (one warp)
-// ---------------------------------------------------------------------------
-template <int D>
-__device__ __forceinline__ void load_tiles_tma(const AttnParams& p, const AttnSeq& s, const Work& w, const CUtensorMap* km,
-                                               const CUtensorMap* vm, uint32_t ring, const Bars& bars) {
-  using C = Cfg<D, WAL_KV_BF16>;
-  const int lane = threadIdx.x & 31;
-  int item = 0;
-  bool ok = true, tail = false;
-  for (int j = 0; j < w.n && ok; ++j) {
-    const int kb = w.k0 + kTile * j, cnt = min(kTile, w.k1 - kb);
-    // this tile's boxes: lane i's page (paged) or the packed rows
-    int boxes = 1, box_rows = kTile, page = 0;
-    if (p.table) {
-      box_rows = min(kTile, 1 << p.shift);
-      boxes = (cnt + box_rows - 1) / box_rows;
-      if (lane < boxes) {
-        page = __ldg(p.table + w.b * p.ld_table + ((kb + lane * box_rows) >> p.shift));
-        if ((uint32_t)page >= (uint32_t)p.n_pages) {
-          atomicExch(p.status, (int32_t)WAL_ERR_ARG);
-          page = 0;
-        }
-      }
-    }
-    for (int kv = 0; kv < 2; ++kv, ++item) {
-      const int slot = item % C::slots;
-      if (item >= C::slots) ok = mbar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tail = kv == 1 && cnt < kTile;
-      const uint32_t dst = ring + (uint32_t)slot * C::tile_bytes, bar = tail ? bars.v_tail() : bars.full(slot);
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows) * D * 2);
-      __syncwarp();
-      const int x0 = p.table ? 0 : w.h * D, z0 = p.table ? w.h : 0;
-      const int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
-      for (int i = 0; i < boxes; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, i);
-        if (lane == 0)
-#pragma unroll
-          for (int a = 0; a < D / 64; ++a)
-            tma_4d(dst + a * 16384u + (uint32_t)(i * box_rows) * 128u, kv ? vm : km, x0 + 64 * a, y0, z0, pg, bar);
-      }
-      if (tail) {  // the last V tile: zero the rows that hold no key of this CTA
-        ok = __all_sync(0xffffffffu, mbar_wait(bar, 0, p.status));
-        if (!ok) break;
-        for (int i = lane; i < (kTile - cnt) * (D / 8); i += 32) {
-          const int r = cnt + i / (D / 8), ch = i % (D / 8);
-          sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7), make_uint4(0, 0, 0, 0));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.full(slot));
-      }
+// Piece i; false where there are no rows.
+template <int TYPE>
+__device__ __forceinline__ bool get_work(const AttnParams& p, const Sched& sc, int64_t i, Work& w, AttnSeq& s) {
+  const int64_t per = (int64_t)p.B * p.n_kv_heads, ts = i / per;
+  const int r = (int)(i - ts * per);
+  w.b = r / p.n_kv_heads;
+  w.h = r - w.b * p.n_kv_heads;
+  w.split = (int)(ts % sc.splits);
+  s = attn_seq(p, w.b);
+  const int rows_all = s.n_q * p.group;
+  w.r0 = (sc.tiles - 1 - (int)(ts / sc.splits)) * kTcAttnRows;
+  w.rows = min(kTcAttnRows, rows_all - w.r0);
+  if (w.rows <= 0) return false;
+  w.k0 = w.split * p.split_keys;
+  if (w.split > 0 && w.k0 >= s.len) return false;  // not a split of this sequence
+  w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
+  w.n = w.k1 > w.k0 ? (w.k1 - w.k0 + kTile - 1) / kTile : 0;
+  w.dual = w.rows <= kTile && w.n > 1;
+  if (w.dual) {
+    w.n0 = (w.n + 1) / 2;
+    w.n1 = w.n / 2;
+  } else {
+    w.n0 = w.n;
+    w.n1 = w.rows > kTile ? w.n : 0;
+    if (TYPE == WAL_KV_BF16 && w.rows > kTile) {  // the first tile's rows may see fewer keys
+      const int end = min(w.k1, attn_limit(s, (w.r0 + kTile - 1) / p.group));
+      w.n0 = end > w.k0 ? (end - w.k0 + kTile - 1) / kTile : 0;
     }
   }
-  // nothing of this warp's stays in flight, whatever the MMA thread waited for
-  if (!ok && tail) mbar_drain(bars.v_tail(), 0, p.status);
-  for (int i = max(0, item - C::slots); i < item; ++i)
-    mbar_drain(bars.full(i % C::slots), (i / C::slots) & 1, p.status);
+  return true;
 }
 
 // ---------------------------------------------------------------------------
-// 8-bit K/V tiles through registers (three warps)
+// K/V tiles by TMA (one warp): bf16 tiles as the MMAs want them, or codes and
+// scales for the converters
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void load_tiles_codes(const AttnParams& p, const Work& w, float sl, uint32_t ring, float* scales,
-                                                 const Bars& bars) {
+__device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sched, const CUtensorMap* km, const CUtensorMap* vm,
+                                           uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
-  constexpr int kPer = D / 16;                                // 16-code pieces of a row
-  constexpr int kN = (kTile * kPer + kConv - 1) / kConv;      // pieces of a thread
-  const int tid = threadIdx.x - (kThreads - kConv);
-  const int items = 2 * w.n;
-  uint4 cur[kN];
-  auto fetch = [&](int item, uint4(&d)[kN]) {
-    const int kb = w.k0 + kTile * (item >> 1), cnt = min(kTile, w.k1 - kb);
-    const uint8_t* src = static_cast<const uint8_t*>((item & 1) ? p.v : p.k);
+  constexpr int kSlots = C::codes ? C::raws : C::slots;
+  constexpr uint32_t kBytes = C::codes ? C::raw : C::tile;
+  const uint32_t ring = base + (C::codes ? C::raw_off : C::ring_off);
+  const int lane = threadIdx.x & 31;
+  auto full = [&](int s) { return C::codes ? bars.raw_full(s) : bars.full(s); };
+  auto empty = [&](int s) { return C::codes ? bars.raw_empty(s) : bars.empty(s); };
+  uint32_t item = 0, tails = 0;
+  bool ok = true, tail = false;
+  const int64_t total = sched.total(p);
+  for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    Work w;
+    AttnSeq s;
+    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+    for (int j = 0; j < w.n && ok; ++j) {
+      const int kb = w.k0 + kTile * j, cnt = min(kTile, w.k1 - kb);
+      // this tile's boxes: lane i's page (paged) or the packed rows
+      int boxes = 1, box_rows = kTile, page = 0;
+      if (p.table) {
+        box_rows = min(kTile, 1 << p.shift);
+        boxes = (cnt + box_rows - 1) / box_rows;
+        if (lane < boxes) page = attn_page(p, w.b, kb + lane * box_rows);
+      }
+      const int x0 = p.table ? 0 : w.h * D, z0 = p.table ? w.h : 0;
+      const int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
+      for (int kv = 0; kv < 2; ++kv, ++item) {
+        const int slot = item % kSlots;
+        if (item >= kSlots) ok = mbar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tail = !C::codes && kv == 1 && cnt < kTile;
+        const uint32_t dst = ring + (uint32_t)slot * kBytes, bar = tail ? bars.v_tail() : full(slot);
+        const uint32_t row_bytes = C::codes ? D + 4 : D * 2;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows) * row_bytes);
+        __syncwarp();
+        for (int q = 0; q < boxes; ++q) {
+          const int pg = __shfl_sync(0xffffffffu, page, q);
+          if (lane == 0) {
+            if (C::codes) {
+              tma_4d(dst + (uint32_t)(q * box_rows) * D, kv ? vm : km, 0, y0, z0, pg, bar);
+              const float* sc = (kv ? p.vs : p.ks) + ((((int64_t)pg * p.n_kv_heads + w.h) << p.shift) + y0);
+              bulk_g2s(dst + kTile * D + (uint32_t)(q * box_rows) * 4u, sc, (uint32_t)box_rows * 4u, bar);
+            } else {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = tid + kConv * i, key = e / kPer, part = e % kPer;
-      d[i] = make_uint4(0, 0, 0, 0);
-      if (e < kTile * kPer && key < cnt)
-        d[i] = __ldg(reinterpret_cast<const uint4*>(src + attn_page_row(p, w.b, w.h, kb + key) * D) + part);
-    }
-  };
-  if (items) fetch(0, cur);
-  bool ok = true;
-  for (int item = 0; item < items; ++item) {
-    uint4 nxt[kN];
-    if (item + 1 < items) fetch(item + 1, nxt);
-    const int j = item >> 1, slot = item % C::slots;
-    if (!(item & 1)) {  // the scales of this tile's keys
-      const int kb = w.k0 + kTile * j;
-      float* sc = scales + (j % kScaleRing) * 2 * kTile;
-      if (j >= kScaleRing) ok = mbar_wait(bars.sc_empty(j % kScaleRing), ((j / kScaleRing) & 1) ^ 1, p.status);
-      if (!ok) break;
-      for (int i = tid; i < 2 * kTile; i += kConv) {
-        const int key = kb + (i & (kTile - 1));
-        float v = 0.f;
-        if (key < w.k1) {
-          const int64_t row = attn_page_row(p, w.b, w.h, key);
-          v = i < kTile ? __ldg(p.ks + row) * sl : __ldg(p.vs + row);
+              for (int a = 0; a < D / 64; ++a)
+                tma_4d(dst + a * 16384u + (uint32_t)(q * box_rows) * 128u, kv ? vm : km, x0 + 64 * a, y0, z0, pg, bar);
+            }
+          }
         }
-        sc[i] = v;
-      }
-      mbar_arrive(bars.sc_full(j % kScaleRing));
-    }
-    if (item >= C::slots) ok = mbar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
-    if (!ok) break;
-    const uint32_t dst = ring + (uint32_t)slot * C::tile_bytes;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = tid + kConv * i, key = e / kPer, part = e % kPer;
-      if (e < kTile * kPer) {
-        const uint32_t a = dst + (part >> 2) * 16384u;
-        uint4 x, y;
-        dev::codes4_to_bf16<TYPE>(cur[i].x, x.x, x.y);
-        dev::codes4_to_bf16<TYPE>(cur[i].y, x.z, x.w);
-        dev::codes4_to_bf16<TYPE>(cur[i].z, y.x, y.y);
-        dev::codes4_to_bf16<TYPE>(cur[i].w, y.z, y.w);
-        sts128(a + sw128(key, 2 * (part & 3)), x);
-        sts128(a + sw128(key, 2 * (part & 3) + 1), y);
+        if (tail) {  // the piece's last V tile: zero the rows that hold no key of it
+          ok = __all_sync(0xffffffffu, mbar_wait(bar, tails & 1, p.status));
+          if (!ok) break;
+          ++tails;
+          for (int r8 = lane; r8 < (kTile - cnt) * (D / 8); r8 += 32) {
+            const int r = cnt + r8 / (D / 8), ch = r8 % (D / 8);
+            sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7), make_uint4(0, 0, 0, 0));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.full(slot));
+        }
       }
     }
-    fence_proxy_async_smem();
-    mbar_arrive(bars.full(slot));
+  }
+  // nothing of this warp's stays in flight, whatever its readers waited for
+  if (!ok && tail) mbar_drain(bars.v_tail(), tails & 1, p.status);
+  for (uint32_t i = item > kSlots ? item - kSlots : 0; i < item; ++i) mbar_drain(full(i % kSlots), (i / kSlots) & 1, p.status);
+}
+
+// ---------------------------------------------------------------------------
+// codes to bf16 tiles (four warps)
+// ---------------------------------------------------------------------------
+template <int D, int TYPE>
+__device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
+  using C = Cfg<D, TYPE>;
+  const int tid = threadIdx.x & 127;
+  uint32_t item = 0, tiles = 0;
+  const int64_t total = sched.total(p);
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    Work w;
+    AttnSeq s;
+    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+    for (int j = 0; j < w.n; ++j, ++tiles) {
+      const int cnt = min(kTile, w.k1 - w.k0 - kTile * j);
+      const int si = tiles % kScaleRing;
+      for (int kv = 0; kv < 2; ++kv, ++item) {
+        const int rs = item % C::raws, slot = item % C::slots;
+        bool ok = mbar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
+        if (ok && kv == 0 && tiles >= kScaleRing) ok = mbar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
+        if (ok && item >= C::slots) ok = mbar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
+        if (!ok) return;
+        const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
+        // keys that are not there get codes and scales of zero
+        sts32(base + C::scale_off + (uint32_t)(si * 2 + kv) * (kTile * 4) + 4u * tid,
+              tid < cnt ? lds32(src + kTile * D + 4u * tid) : 0u);
+#pragma unroll 4
+        for (int q = 0; q < D / 16; ++q) {
+          // 16 codes: piece `part` (of 64 columns' four) of `atom` in `row`.  Eight
+          // lanes read 128 bytes in different banks and write chunks that are.
+          const int e = q * 128 + tid, part = e & 3;
+          int row, atom;
+          if (D == 128) {
+            row = 2 * (e >> 4) + ((e >> 2) & 1);
+            atom = ((e >> 2) ^ (e >> 3)) & 1;
+          } else {
+            row = e >> 2;
+            atom = 0;
+          }
+          uint4 v = lds128(src + (uint32_t)row * D + atom * 64u + part * 16u);
+          if (row >= cnt) v = make_uint4(0, 0, 0, 0);
+          uint4 x, y;
+          dev::codes4_to_bf16<TYPE>(v.x, x.x, x.y);
+          dev::codes4_to_bf16<TYPE>(v.y, x.z, x.w);
+          dev::codes4_to_bf16<TYPE>(v.z, y.x, y.y);
+          dev::codes4_to_bf16<TYPE>(v.w, y.z, y.w);
+          const uint32_t a = dst + atom * 16384u;
+          sts128(a + sw128(row, 2 * part), x);
+          sts128(a + sw128(row, 2 * part + 1), y);
+        }
+        mbar_arrive(bars.raw_empty(rs));
+        if (kv == 1) mbar_arrive(bars.sc_full(si));
+        fence_proxy_async_smem();
+        mbar_arrive(bars.full(slot));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Q tiles (two warps)
+// ---------------------------------------------------------------------------
+template <int D, int TYPE>
+__device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
+  using C = Cfg<D, TYPE>;
+  constexpr int kBatch = 4, kN = kTile * (D / 8) / kQThreads;
+  const int tid = threadIdx.x & (kQThreads - 1);
+  // A negative scale is a sign on Q, a scale of zero makes it zero: the scores
+  // are then multiplied by sl > 0.
+  const uint32_t keep = p.scale_log2 == 0.f ? 0u : ~0u, flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+  uint32_t uses[2] = {0, 0};
+  const int64_t total = sched.total(p);
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    Work w;
+    AttnSeq s;
+    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) cur[i] = nxt[i];
+    for (int t = 0; t < 2; ++t) {
+      if (!w.has_q(t)) continue;
+      if (uses[t] > 0 && !mbar_wait(bars.q_empty(t), (uses[t] - 1) & 1, p.status)) return;
+      ++uses[t];
+      const uint32_t dst = base + t * C::tile;
+#pragma unroll 1
+      for (int e0 = 0; e0 < kN; e0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int idx = (e0 + e) * kQThreads + tid, r = kTile * t + idx / (D / 8), ch = idx % (D / 8);
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (r < w.rows) {
+            const int row = w.r0 + r, tok = row / p.group, head = w.h * p.group + row - tok * p.group;
+            v[e] = __ldg(reinterpret_cast<const uint4*>(p.Q + (s.q0 + tok) * p.ldq + head * D) + ch);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int idx = (e0 + e) * kQThreads + tid, r = idx / (D / 8), ch = idx % (D / 8);
+          sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7),
+                 make_uint4((v[e].x & keep) ^ flip, (v[e].y & keep) ^ flip, (v[e].z & keep) ^ flip, (v[e].w & keep) ^ flip));
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bars.q_full(t));
+    }
   }
 }
 
@@ -310,12 +422,15 @@ __device__ __forceinline__ void load_tiles_codes(const AttnParams& p, const Work
 // MMA issue (one thread)
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void issue_mmas(const AttnParams& p, const Work& w, uint32_t q_smem, uint32_t ring, uint32_t tmem,
-                                           const Bars& bars) {
+__device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sched, uint32_t base, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
-  auto scores = [&](int t, int item) {
-    const uint32_t a = q_smem + t * C::tile_bytes, b = ring + (uint32_t)(item % C::slots) * C::tile_bytes;
+  const uint32_t ring = base + C::ring_off;
+  uint32_t first = 0;             // ring item of the piece's first K tile
+  uint32_t quse[2] = {0, 0}, puse[2] = {0, 0};
+  auto kv_wait = [&](uint32_t item) { return mbar_wait(bars.full(item % C::slots), (item / C::slots) & 1, p.status); };
+  auto scores = [&](int t, int qt, uint32_t item) {  // S_t = Q_qt K^T
+    const uint32_t a = base + qt * C::tile, b = ring + (item % C::slots) * C::tile;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (k >> 2) * 16384u + (k & 3) * 32u;
@@ -323,269 +438,328 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Work& w, u
     }
     mma_commit(bars.s_full(t));
   };
+  auto weigh = [&](int t, uint32_t item, bool more) {  // O_t (+)= P_t V
+    const uint32_t b = ring + (item % C::slots) * C::tile;
+#pragma unroll
+    for (int k = 0; k < kTile / 16; ++k)
+      mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, sdesc_mn_sw128(b + 2048u * k, 16384u), id_o, more || k > 0);
+  };
   bool ok = true;
-  for (int t = 0; t < 2 && ok; ++t)
-    if (w.n_t[t] > 0) ok = mbar_wait(bars.q_full(t), 0, p.status);
-  ok = ok && mbar_wait(bars.full(0), 0, p.status);
-  if (ok) {
-    tc_fence_after();
+  const int64_t total = sched.total(p);
+  for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    Work w;
+    AttnSeq s;
+    if (!get_work<TYPE>(p, sched, i, w, s) || w.n == 0) continue;
+#pragma unroll
     for (int t = 0; t < 2; ++t)
-      if (w.n_t[t] > 0) scores(t, 0);
-    mma_commit(bars.empty(0));
-  }
-  for (int j = 0; j < w.n && ok; ++j) {
-    const int vi = 2 * j + 1, ki = 2 * j + 2;
-    ok = mbar_wait(bars.full(vi % C::slots), (vi / C::slots) & 1, p.status);
-    if (ok && j + 1 < w.n) ok = mbar_wait(bars.full(ki % C::slots), (ki / C::slots) & 1, p.status);
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (j >= w.n_t[t]) continue;
-      ok = mbar_wait(bars.p_full(t), j & 1, p.status);
+      if (ok && w.has_q(t)) ok = mbar_wait(bars.q_full(t), quse[t]++ & 1, p.status);
+    if (!w.dual) {
+      ok = ok && kv_wait(first);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t b = ring + (uint32_t)(vi % C::slots) * C::tile_bytes;
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, sdesc_mn_sw128(b + 2048u * k, 16384u), id_o,
-                   j > 0 || k > 0);
-      if (j + 1 < w.n_t[t])
-        scores(t, ki);
-      else
-        mma_commit(bars.o_done(t));
+      for (int t = 0; t < 2; ++t)
+        if (w.n_t(t) > 0) {
+          scores(t, t, first);
+          if (w.n_t(t) == 1) mma_commit(bars.q_empty(t));
+        }
+      mma_commit(bars.empty(first % C::slots));
+      for (int j = 0; j < w.n && ok; ++j) {
+        const uint32_t vi = first + 2 * j + 1, ki = vi + 1;
+        ok = kv_wait(vi);
+        if (ok && j + 1 < w.n) ok = kv_wait(ki);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || j >= w.n_t(t)) continue;
+          ok = mbar_wait(bars.p_full(t), puse[t]++ & 1, p.status);
+          if (!ok) continue;
+          tc_fence_after();
+          weigh(t, vi, j > 0);
+          if (j + 1 < w.n_t(t)) {
+            scores(t, t, ki);
+            if (j + 2 == w.n_t(t)) mma_commit(bars.q_empty(t));
+          } else {
+            mma_commit(bars.o_done(t));
+          }
+        }
+        if (!ok) break;
+        mma_commit(bars.empty(vi % C::slots));
+        if (j + 1 < w.n) mma_commit(bars.empty(ki % C::slots));
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        ok = ok && kv_wait(first + 2 * t);
+        if (!ok) continue;
+        tc_fence_after();
+        scores(t, 0, first + 2 * t);
+        mma_commit(bars.empty((first + 2 * t) % C::slots));
+      }
+      if (ok && w.n == 2) mma_commit(bars.q_empty(0));
+      for (int j = 0; j < w.n && ok; ++j) {
+        const uint32_t vi = first + 2 * j + 1, ki = vi + 3;
+        const int t = j & 1;
+        ok = kv_wait(vi) && mbar_wait(bars.p_full(t), (t ? puse[1]++ : puse[0]++) & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        weigh(t, vi, j > 1);
+        if (j + 2 < w.n) {
+          mma_commit(bars.empty(vi % C::slots));
+          ok = kv_wait(ki);
+          if (!ok) break;
+          tc_fence_after();
+          scores(t, 0, ki);
+          mma_commit(bars.empty(ki % C::slots));
+          if (j + 3 == w.n) mma_commit(bars.q_empty(0));
+        } else {
+          mma_commit(bars.o_done(t));
+          mma_commit(bars.empty(vi % C::slots));
+        }
+      }
     }
-    if (!ok) break;
-    mma_commit(bars.empty(vi % C::slots));
-    if (j + 1 < w.n) mma_commit(bars.empty(ki % C::slots));
+    first += 2 * w.n;
   }
   mma_commit(bars.drained());
   mbar_drain(bars.drained(), 0, p.status);
 }
 
 // ---------------------------------------------------------------------------
-// softmax and output of one query tile (four warps, a row a thread)
+// softmax and output (four warps a half of the CTA, a row a thread)
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void softmax_tile(const AttnParams& p, const AttnSeq& s, const Work& w, int t, float sl,
-                                             uint32_t q_smem, const float* scales, uint32_t tmem, const Bars& bars) {
+__device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, float sl, uint32_t base, const uint8_t* gbase,
+                                             uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
-  const int tid = threadIdx.x & 127, warp = tid >> 5;
-  const int n = w.n_t[t], rows_all = s.n_q * p.group;
-
-  // Q into shared memory.  A negative scale is a sign on Q, a scale of zero
-  // makes it zero: the scores below are then multiplied by sl > 0.
-  {
-    const uint32_t keep = p.scale_log2 == 0.f ? 0u : ~0u, flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const uint32_t dst = q_smem + t * C::tile_bytes;
-    for (int i = tid; i < kTile * (D / 8); i += 128) {
-      const int r = i / (D / 8), ch = i % (D / 8), row = w.r0 + kTile * t + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < rows_all) {
-        const int tok = row / p.group, head = w.h * p.group + row - tok * p.group;
-        v = __ldg(reinterpret_cast<const uint4*>(p.Q + (s.q0 + tok) * p.ldq + head * D) + ch);
-        v = make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip);
-      }
-      sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7), v);
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(bars.q_full(t));
-  }
-
-  const int row = w.r0 + kTile * t + tid;
-  const bool live = row < rows_all;
-  const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
-  const int lim = live ? min(w.k1, attn_limit(s, tok)) : w.k1;
-  const int lim0 = __shfl_sync(0xffffffffu, lim, 0);  // the warp's smallest: limits grow with the row
-  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+  const int tid = threadIdx.x & 127;
+  const uint32_t lanes = (uint32_t)(tid & 96) << 16;
   const uint32_t t_s = tmem + 128u * t + lanes, t_o = tmem + 256u + (uint32_t)D * t + lanes;
-  float m = -INFINITY, l = 0.f;
+  const float2 sl2 = make_float2(sl, sl);
+  uint32_t steps = 0, pieces = 0, duals = 0, tiles = 0;
   bool ok = true;
-  for (int j = 0; j < n; ++j) {
-    const int kb = w.k0 + kTile * j;
-    const float* sc = scales + (j % kScaleRing) * 2 * kTile;
-    ok = mbar_wait(bars.s_full(t), j & 1, p.status);
-    if (TYPE != WAL_KV_BF16) ok = ok && mbar_wait(bars.sc_full(j % kScaleRing), (j / kScaleRing) & 1, p.status);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    tc_fence_after();
-    float x[kTile];
+  const int64_t total = sched.total(p);
+  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+    Work w;
+    AttnSeq s;
+    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+    const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
+    const int n = w.n_t(t);
+    // the half that writes these rows: both of a dual piece lead to half 0
+    const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
+    const int tok = live || w.dual ? min(row, w.r0 + w.rows - 1) / p.group : 0;
+    const int lim = row < w.r0 + w.rows ? min(w.k1, attn_limit(s, row / p.group)) : w.k1;
+    const int lim0 = __shfl_sync(0xffffffffu, lim, 0);  // the warp's smallest: limits grow with the row
+    float m = -INFINITY, l = 0.f;
+    for (int k = 0; k < n; ++k, ++steps) {
+      const int kb = w.k0 + kTile * w.tile_of(t, k);
+      const uint32_t ti = tiles + w.tile_of(t, k);
+      const float* sc = reinterpret_cast<const float*>(gbase + C::scale_off) + (ti % kScaleRing) * 2 * kTile;
+      ok = mbar_wait(bars.s_full(t), steps & 1, p.status);
+      if (C::codes) ok = ok && mbar_wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after();
+      float x[kTile];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tmem_ld32(t_s + 32u * i, x + 32 * i);
-    tmem_ld_wait();
-    if (TYPE != WAL_KV_BF16) {
+      for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
+      tmem_ld_wait();
+      if (C::codes) {
 #pragma unroll
-      for (int i = 0; i < kTile; i += 2) {
-        const float2 y = mul2(make_float2(x[i], x[i + 1]), *reinterpret_cast<const float2*>(sc + i));
-        x[i] = y.x;
-        x[i + 1] = y.y;
+        for (int q = 0; q < kTile; q += 2) {
+          const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
+          x[q] = y.x;
+          x[q + 1] = y.y;
+        }
       }
-    }
-    if (kb + kTile > lim0) {
-      const int c = lim - kb;
+      if (kb + kTile > lim0) {
+        const int c = lim - kb;
 #pragma unroll
-      for (int i = 0; i < kTile; ++i) x[i] = i < c ? x[i] : -INFINITY;
-    }
-    float mx = -INFINITY;
+        for (int q = 0; q < kTile; ++q) x[q] = q < c ? x[q] : -INFINITY;
+      }
+      float mx = fmaxf(x[0], x[1]), mx1 = fmaxf(x[2], x[3]);
 #pragma unroll
-    for (int i = 0; i < kTile; i += 4) mx = fmaxf(mx, fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])));
-    if (TYPE == WAL_KV_BF16) mx *= sl;
-    const bool grow = mx > m + kLazy || (m == -INFINITY && mx > m);
-    if (__any_sync(0xffffffffu, grow)) {
-      const float mn = grow ? mx : m;
-      const float f = grow ? ex2(m - mn) : 1.f;  // 0 for a row that had no key yet
-      m = mn;
-      l *= f;
-      if (j > 0) {
+      for (int q = 4; q < kTile; q += 4) {
+        mx = max3(mx, x[q], x[q + 1]);
+        mx1 = max3(mx1, x[q + 2], x[q + 3]);
+      }
+      mx = fmaxf(mx, mx1) * sl;
+      const bool grow = mx > m + kLazy || (m == -INFINITY && mx > m);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? mx : m;
+        const float f = grow ? ex2(m - mn) : 1.f;  // 0 for a row that had no key yet
+        m = mn;
+        l *= f;
+        if (k > 0) {
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(t_o + 16u * q, o);
+            tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float o[32];
-          tmem_ld32(t_o + 32u * i, o);
-          tmem_ld_wait();
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(t_o + 16u * q, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : -m;
+      const float2 ref2 = make_float2(ref, ref);
+      float2 sum = make_float2(0.f, 0.f), sum_b = sum;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= f;
-          tmem_st32(t_o + 32u * i, o);
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int c = 32 * q + 2 * e;
+          float2 y = fma2(make_float2(x[c], x[c + 1]), sl2, ref2);
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          if (e & 1) sum_b = add2(sum_b, y); else sum = add2(sum, y);
+          if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + c));
+          pk[e] = dev::float2_to_bf16x2(y.x, y.y);
+        }
+        tmem_st16(t_s + 16u * q, pk);
+      }
+      sum = add2(sum, sum_b);
+      l += sum.x + sum.y;
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bars.p_full(t));
+      if (C::codes) {  // eight arrivals free the scales: one of a warp, two where one half alone reads them
+        __syncwarp();
+        if ((tid & 31) == 0) {
+          mbar_arrive(bars.sc_empty(ti % kScaleRing));
+          if (w.dual || w.rows <= kTile) mbar_arrive(bars.sc_empty(ti % kScaleRing));
         }
       }
     }
-    const float ref = m == -INFINITY ? 0.f : -m;
-    const float2 ref2 = make_float2(ref, ref), sl2 = TYPE == WAL_KV_BF16 ? make_float2(sl, sl) : make_float2(1.f, 1.f);
-    float2 sum = make_float2(0.f, 0.f), sum_b = sum;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int e = 32 * i + 2 * k;
-        float2 y = make_float2(x[e], x[e + 1]);
-        y = TYPE == WAL_KV_BF16 ? fma2(y, sl2, ref2) : add2(y, ref2);
-        y.x = ex2(y.x);
-        y.y = ex2(y.y);
-        if (k & 1) sum_b = add2(sum_b, y); else sum = add2(sum, y);
-        if (TYPE != WAL_KV_BF16) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + e));
-        pk[k] = dev::float2_to_bf16x2(y.x, y.y);
-      }
-      tmem_st16(t_s + 16u * i, pk);
-    }
-    sum = add2(sum, sum_b);
-    l += sum.x + sum.y;
-    tmem_st_wait();
-    tc_fence_before();
-    mbar_arrive(bars.p_full(t));
-    if (TYPE != WAL_KV_BF16) mbar_arrive(bars.sc_empty(j % kScaleRing));
-  }
+    tiles += w.n;
 
-  // output: the row's sums, or its share of them
-  if (n > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait(bars.o_done(t), 0, p.status));
-  if (!ok) return;
-  tc_fence_after();
-  const bool partial = p.n_split > 1;
-  const float inv = lim == 0 ? 0.f : 1.f / l;
-  bool nan = false;
-  const int64_t pr = (int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    float o[32];
+    // output: the row's sums over its keys, or its share of them
     if (n > 0) {
-      tmem_ld32(t_o + 32u * i, o);
-      tmem_ld_wait();
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      ok = __all_sync(0xffffffffu, mbar_wait(bars.o_done(t), pieces & 1, p.status));
+      if (!ok) return;
+      ++pieces;
     }
-    if (live && partial) {
-      float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * i);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-    } else if (live) {
-      uint32_t u[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float a = lim == 0 ? 0.f : o[2 * k] * inv, b = lim == 0 ? 0.f : o[2 * k + 1] * inv;
-        nan |= a != a || b != b;
-        u[k] = dev::float2_to_bf16x2(a, b);
+    float f = 1.f, f1 = 0.f;  // factors of this half's and the other half's sums
+    if (w.dual) {
+      const uint32_t ml = base + C::ml_off + 8u * tid;
+      if (t == 1) {
+        sts64(ml, make_uint2(__float_as_uint(m), __float_as_uint(l)));
+        tc_fence_after();
+        tc_fence_before();
+        mbar_arrive(bars.ml_full());  // O_1 is complete too: this thread has seen o_done
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.ml_empty(), duals & 1, p.status));
+        if (!ok) return;
+        ++duals;
+        continue;
       }
-      uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + 32 * i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) dst[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+      ok = __all_sync(0xffffffffu, mbar_wait(bars.ml_full(), duals & 1, p.status));
+      if (!ok) return;
+      ++duals;
+      const uint2 u = lds64(ml);
+      const float m1 = __uint_as_float(u.x), l1 = __uint_as_float(u.y), mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
+      f = ex2(m - ref);
+      f1 = ex2(m1 - ref);
+      m = mm;
+      l = l * f + l1 * f1;
     }
-    __syncwarp();
-  }
-  if (partial) {
-    if (live) p.part_ml[pr] = make_float2(m, l);
-    return;
-  }
-  // a key that the row does not see may have made it NaN
-  uint32_t again = __ballot_sync(0xffffffffu, live && nan && lim < w.k1);
-  while (again) {
-    const int src = __ffs(again) - 1;
-    again &= again - 1;
-    attend_row<D>(p, s, w.b, __shfl_sync(0xffffffffu, head, src), __shfl_sync(0xffffffffu, tok, src));
+    tc_fence_after();
+    const bool partial = p.n_split > 1;
+    const int head = w.h * p.group + (live ? row - tok * p.group : 0);
+    const float inv = lim == 0 ? 0.f : 1.f / l;
+    bool nan = false;
+    const int64_t pr = (int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      float o[32];
+      if (n > 0) {
+        tmem_ld32(t_o + 32u * q, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+      if (w.dual) {
+        float o1[32];
+        tmem_ld32(t_o + (uint32_t)D + 32u * q, o1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = o[e] * f + o1[e] * f1;
+      }
+      if (live && partial) {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      } else if (live) {
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a = lim == 0 ? 0.f : o[2 * e] * inv, b = lim == 0 ? 0.f : o[2 * e + 1] * inv;
+          nan |= a != a || b != b;
+          u[e] = dev::float2_to_bf16x2(a, b);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+      }
+      __syncwarp();
+    }
+    if (w.dual) {
+      tc_fence_before();
+      mbar_arrive(bars.ml_empty());
+    }
+    if (partial) {
+      if (live) p.part_ml[pr] = make_float2(m, l);
+      continue;
+    }
+    // a key that the row does not see may have made it NaN
+    uint32_t again = __ballot_sync(0xffffffffu, live && nan && lim < w.k1);
+    while (again) {
+      const int src = __ffs(again) - 1;
+      again &= again - 1;
+      attend_row<D>(p, s, w.b, __shfl_sync(0xffffffffu, head, src), __shfl_sync(0xffffffffu, tok, src));
+    }
   }
 }
 
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, TYPE>::threads, 1)
 attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
   using C = Cfg<D, TYPE>;
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Work w;
-  w.b = blockIdx.z;
-  w.h = blockIdx.y;
-  w.split = blockIdx.x % p.n_split;
-  const int tile = (int)(gridDim.x / p.n_split) - 1 - (int)(blockIdx.x / p.n_split);  // longest rows of keys first
-  const AttnSeq s = attn_seq(p, w.b);
-  if (s.bad) {
-    if (blockIdx.x == 0 && w.h == 0 && threadIdx.x == 0) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
-    return;
-  }
-  const int rows_all = s.n_q * p.group;
-  w.r0 = tile * kTcAttnRows;
-  w.rows = min(kTcAttnRows, rows_all - w.r0);
-  if (w.rows <= 0) return;
-  w.k0 = w.split * p.split_keys;
-  w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
-  w.n = w.k1 > w.k0 ? (w.k1 - w.k0 + kTile - 1) / kTile : 0;
-  if (w.n == 0) {  // none of the rows sees a key of this split
-    for (int i = threadIdx.x; i < w.rows * (D / 8); i += kThreads) {
-      const int row = w.r0 + i / (D / 8), ch = i % (D / 8), tok = row / p.group, head = w.h * p.group + row - tok * p.group;
-      if (p.n_split > 1) {
-        if (ch == 0)
-          p.part_ml[(int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head)] = make_float2(-INFINITY, 0.f);
-      } else {
-        reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D)[ch] = make_uint4(0, 0, 0, 0);
-      }
-    }
-    return;
-  }
-  w.n_t[1] = w.rows > kTile ? w.n : 0;
-  w.n_t[0] = w.n;
-  if (TYPE == WAL_KV_BF16 && w.rows > kTile) {  // the first tile's rows may see fewer keys
-    const int end = min(w.k1, attn_limit(s, (w.r0 + kTile - 1) / p.group));
-    w.n_t[0] = end > w.k0 ? (end - w.k0 + kTile - 1) / kTile : 0;
-  }
-
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  float* scales = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + C::scale_off);
-  const uint32_t ring = base + 2 * C::tile_bytes;
+  uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
   const Bars bars = {base + C::bar_off};
+  int* shape = reinterpret_cast<int*>(gbase + C::bar_off + 404);  // most tiles, most splits of a sequence, any out of range
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::slots; ++i) {
-      mbar_init(bars.full(i), TYPE == WAL_KV_BF16 ? 1 : kConv);
+      mbar_init(bars.full(i), C::codes ? 128 : 1);
       mbar_init(bars.empty(i), 1);
     }
+    if (C::codes) {
+      for (int i = 0; i < C::raws; ++i) {
+        mbar_init(bars.raw_full(i), 1);
+        mbar_init(bars.raw_empty(i), 128);
+      }
+      for (int i = 0; i < kScaleRing; ++i) {
+        mbar_init(bars.sc_full(i), 128);
+        mbar_init(bars.sc_empty(i), 8);
+      }
+    }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bars.q_full(t), 128);
+      mbar_init(bars.q_full(t), kQThreads);
+      mbar_init(bars.q_empty(t), 1);
       mbar_init(bars.s_full(t), 1);
       mbar_init(bars.p_full(t), 128);
       mbar_init(bars.o_done(t), 1);
     }
-    for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(bars.sc_full(i), kConv);
-      mbar_init(bars.sc_empty(i), w.rows > kTile ? 256 : 128);
-    }
+    mbar_init(bars.ml_full(), 128);
+    mbar_init(bars.ml_empty(), 128);
     mbar_init(bars.v_tail(), 1);
     mbar_init(bars.drained(), 1);
     mbar_init_fence();
+    shape[0] = shape[1] = shape[2] = 0;
   }
   if (warp == 8) {
     tmem_alloc(bars.tmem_slot(), 512);
@@ -595,17 +769,42 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = lds32(bars.tmem_slot());
+  // how far the pieces reach, and which sequences are out of range
+  {
+    int tiles = 0, splits = 1, bad = 0;
+    for (int b = threadIdx.x; b < p.B; b += C::threads) {
+      const AttnSeq s = attn_seq(p, b);
+      bad |= s.bad;
+      tiles = max(tiles, (int)(((int64_t)s.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows));
+      if (s.n_q > 0) splits = max(splits, (int)(((int64_t)s.len + p.split_keys - 1) / p.split_keys));
+    }
+    atomicMax(&shape[0], tiles);
+    atomicMax(&shape[1], splits);
+    if (bad) shape[2] = 1;
+  }
+  __syncthreads();
+  const Sched sched = {shape[0], shape[1]};
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (p.clear) *p.status = p.n_split == 1 && shape[2] ? (int32_t)WAL_ERR_ARG : 0;
+    else if (shape[2]) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+  }
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
   if (warp < 8) {
-    if (warp < 4 || w.rows > kTile) softmax_tile<D, TYPE>(p, s, w, warp >> 2, sl, base, scales, tmem, bars);
-  } else if (warp == 8) {
-    if ((threadIdx.x & 31) == 0) issue_mmas<D, TYPE>(p, w, base, ring, tmem, bars);
-    __syncwarp();
-  } else if (TYPE == WAL_KV_BF16) {
-    if (warp == 9) load_tiles_tma<D>(p, s, w, &km, &vm, ring, bars);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
+    softmax_rows<D, TYPE>(p, sched, warp >> 2, sl, base, gbase, tmem, bars);
   } else {
-    load_tiles_codes<D, TYPE>(p, w, sl, ring, scales, bars);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
+    if (warp == 8) {
+      if ((threadIdx.x & 31) == 0) issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
+      __syncwarp();
+    } else if (warp == 9) {
+      load_tiles<D, TYPE>(p, sched, &km, &vm, base, bars);
+    } else if (warp < 12) {
+      load_q<D, TYPE>(p, sched, base, bars);
+    } else {
+      convert_tiles<D, TYPE>(p, sched, base, bars);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -633,40 +832,45 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// K or V as (column, row, head, page): boxes of 64 columns and up to 128 rows.
+// K or V as (column, row, head, page): boxes of up to 128 rows, and of 64 bf16
+// columns in the 128-byte swizzle or of whole rows of codes.
 int make_map(CUtensorMap* map, const AttnParams& p, const void* base, int64_t ld) {
   const EncodeFn enc = encode_fn();
   if (!enc) return fail(WAL_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t D = (cuuint64_t)p.head_dim, H = (cuuint64_t)p.n_kv_heads;
+  const bool codes = p.type != WAL_KV_BF16;
+  const cuuint64_t D = (cuuint64_t)p.head_dim, H = (cuuint64_t)p.n_kv_heads, size = codes ? 1 : 2;
   cuuint64_t dims[4] = {H * D, (cuuint64_t)p.T, 1, 1};  // packed rows: the head is part of the column
   cuuint64_t strides[3] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2, (cuuint64_t)ld * 2};
-  cuuint32_t box[4] = {64, kTile, 1, 1}, step[4] = {1, 1, 1, 1};
+  cuuint32_t box[4] = {codes ? (cuuint32_t)D : 64, kTile, 1, 1}, step[4] = {1, 1, 1, 1};
   if (p.table) {
     const cuuint64_t page = (cuuint64_t)1 << p.shift;
     dims[0] = D;
     dims[1] = page;
     dims[2] = H;
     dims[3] = (cuuint64_t)p.n_pages;
-    strides[0] = D * 2;
-    strides[1] = page * D * 2;
-    strides[2] = H * page * D * 2;
+    strides[0] = D * size;
+    strides[1] = page * D * size;
+    strides[2] = H * page * D * size;
     if (page < kTile) box[1] = (cuuint32_t)page;
   }
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                         strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(WAL_ERR_CUDA, "cuTensorMapEncodeTiled failed with " + std::to_string((int)r));
   return WAL_OK;
 }
 
 template <int D, int TYPE>
-int launch_one(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
+int launch_one(const AttnParams& p, cudaStream_t stream) {
+  CUtensorMap km = {}, vm = {};
+  int st = make_map(&km, p, p.k, p.ldk);
+  if (st || (st = make_map(&vm, p, p.v, p.ldv))) return st;
   // the attribute is per device; setting it again is cheap and needs no state
   cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, TYPE>::smem);
   if (e == cudaSuccess) {
     const int64_t tiles = ((int64_t)p.max_q * p.group + kTcAttnRows - 1) / kTcAttnRows;
-    const dim3 grid((unsigned)(tiles * p.n_split), (unsigned)p.n_kv_heads, (unsigned)p.B);
-    attn_tc_kernel<D, TYPE><<<grid, kThreads, Cfg<D, TYPE>::smem, stream>>>(p, km, vm);
+    const int64_t pieces = tiles * p.n_split * p.n_kv_heads * p.B;
+    attn_tc_kernel<D, TYPE><<<(unsigned)(pieces < kGrid ? pieces : kGrid), Cfg<D, TYPE>::threads, Cfg<D, TYPE>::smem, stream>>>(p, km, vm);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string("attn_tc_kernel launch: ") + cudaGetErrorString(e));
@@ -676,16 +880,12 @@ int launch_one(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm
 }  // namespace
 
 int launch_attn_tc(const AttnParams& p, cudaStream_t stream) {
-  CUtensorMap km = {}, vm = {};
   const bool wide = p.head_dim == 128;
-  if (p.type == WAL_KV_BF16) {
-    int st = make_map(&km, p, p.k, p.ldk);
-    if (st || (st = make_map(&vm, p, p.v, p.ldv))) return st;
-    return wide ? launch_one<128, WAL_KV_BF16>(p, km, vm, stream) : launch_one<64, WAL_KV_BF16>(p, km, vm, stream);
+  switch (p.type) {
+    case WAL_KV_BF16: return wide ? launch_one<128, WAL_KV_BF16>(p, stream) : launch_one<64, WAL_KV_BF16>(p, stream);
+    case WAL_KV_INT8: return wide ? launch_one<128, WAL_KV_INT8>(p, stream) : launch_one<64, WAL_KV_INT8>(p, stream);
+    default: return wide ? launch_one<128, WAL_KV_E4M3>(p, stream) : launch_one<64, WAL_KV_E4M3>(p, stream);
   }
-  if (p.type == WAL_KV_INT8)
-    return wide ? launch_one<128, WAL_KV_INT8>(p, km, vm, stream) : launch_one<64, WAL_KV_INT8>(p, km, vm, stream);
-  return wide ? launch_one<128, WAL_KV_E4M3>(p, km, vm, stream) : launch_one<64, WAL_KV_E4M3>(p, km, vm, stream);
 }
 
 }  // namespace wal

@@ -31,7 +31,7 @@ int check_cache(const wal_kv_cache* c) {
 }
 
 int clear_status(void* ws, cudaStream_t stream, int32_t** status) {
-  *status = reinterpret_cast<int32_t*>(align_up((uintptr_t)ws, 256));
+  *status = status_word(ws);
   const cudaError_t e = cudaMemsetAsync(*status, 0, 4, stream);
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string("status clear: ") + cudaGetErrorString(e));
   return WAL_OK;
