@@ -13,7 +13,7 @@
 // the CTA's pieces by itself, so the loads and the first products of a piece run
 // under the end of the one before.
 //   warps 0-3, 4-7   softmax, rescaling and output of half 0 and 1
-//   warp 8           issues the MMAs (lane 0)
+//   warp 8           issues the MMAs
 //   warp 9           K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
 //                    into a ring in the 128-byte swizzle, 8-bit codes and their
 //                    scales into a ring as they lie
@@ -419,30 +419,36 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
 }
 
 // ---------------------------------------------------------------------------
-// MMA issue (one thread)
+// MMA issue (one warp; the same elected lane issues everything)
 // ---------------------------------------------------------------------------
+// The whole warp walks the loop: with one lane alone in it the operands are not
+// known to be uniform, and an MMA took about 200 cycles to issue instead of the
+// 64 that it runs.
 template <int D, int TYPE>
 __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sched, uint32_t base, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
-  const uint32_t ring = base + C::ring_off;
+  const uint64_t q_desc = sdesc_sw128(base), k_desc = sdesc_sw128(base + C::ring_off);
+  const uint64_t v_desc = sdesc_mn_sw128(base + C::ring_off, 16384u);
   uint32_t first = 0;             // ring item of the piece's first K tile
-  uint32_t quse[2] = {0, 0}, puse[2] = {0, 0};
-  auto kv_wait = [&](uint32_t item) { return mbar_wait(bars.full(item % C::slots), (item / C::slots) & 1, p.status); };
+  uint32_t quse0 = 0, quse1 = 0, puse0 = 0, puse1 = 0;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, p.status)); };
+  auto kv_wait = [&](uint32_t item) { return wait(bars.full(item % C::slots), (item / C::slots) & 1); };
+  // the functions below run in the elected lane
   auto scores = [&](int t, int qt, uint32_t item) {  // S_t = Q_qt K^T
-    const uint32_t a = base + qt * C::tile, b = ring + (item % C::slots) * C::tile;
+    const uint64_t a = q_desc + (uint64_t)(qt * (C::tile >> 4)), b = k_desc + (uint64_t)((item % C::slots) * (C::tile >> 4));
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * 16384u + (k & 3) * 32u;
-      mma_f16(tmem + 128u * t, sdesc_sw128(a + off), sdesc_sw128(b + off), id_s, k > 0);
+      const uint32_t off = ((k >> 2) * 16384u + (k & 3) * 32u) >> 4;
+      mma_f16(tmem + 128u * t, a + off, b + off, id_s, k > 0);
     }
     mma_commit(bars.s_full(t));
   };
   auto weigh = [&](int t, uint32_t item, bool more) {  // O_t (+)= P_t V
-    const uint32_t b = ring + (item % C::slots) * C::tile;
+    const uint64_t b = v_desc + (uint64_t)((item % C::slots) * (C::tile >> 4));
 #pragma unroll
     for (int k = 0; k < kTile / 16; ++k)
-      mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, sdesc_mn_sw128(b + 2048u * k, 16384u), id_o, more || k > 0);
+      mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
   };
   bool ok = true;
   const int64_t total = sched.total(p);
@@ -450,20 +456,22 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
     Work w;
     AttnSeq s;
     if (!get_work<TYPE>(p, sched, i, w, s) || w.n == 0) continue;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (ok && w.has_q(t)) ok = mbar_wait(bars.q_full(t), quse[t]++ & 1, p.status);
+    if (w.has_q(0)) ok = wait(bars.q_full(0), quse0++ & 1);
+    if (ok && w.has_q(1)) ok = wait(bars.q_full(1), quse1++ & 1);
+    if (!ok) break;
     if (!w.dual) {
-      ok = ok && kv_wait(first);
-      if (!ok) break;
+      if (!(ok = kv_wait(first))) break;
       tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (w.n_t(t) > 0) {
-          scores(t, t, first);
-          if (w.n_t(t) == 1) mma_commit(bars.q_empty(t));
-        }
-      mma_commit(bars.empty(first % C::slots));
+        for (int t = 0; t < 2; ++t)
+          if (w.n_t(t) > 0) {
+            scores(t, t, first);
+            if (w.n_t(t) == 1) mma_commit(bars.q_empty(t));
+          }
+        mma_commit(bars.empty(first % C::slots));
+      }
+      __syncwarp();
       for (int j = 0; j < w.n && ok; ++j) {
         const uint32_t vi = first + 2 * j + 1, ki = vi + 1;
         ok = kv_wait(vi);
@@ -471,20 +479,26 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || j >= w.n_t(t)) continue;
-          ok = mbar_wait(bars.p_full(t), puse[t]++ & 1, p.status);
+          ok = wait(bars.p_full(t), (t ? puse1++ : puse0++) & 1);
           if (!ok) continue;
           tc_fence_after();
-          weigh(t, vi, j > 0);
-          if (j + 1 < w.n_t(t)) {
-            scores(t, t, ki);
-            if (j + 2 == w.n_t(t)) mma_commit(bars.q_empty(t));
-          } else {
-            mma_commit(bars.o_done(t));
+          if (elect_one()) {
+            weigh(t, vi, j > 0);
+            if (j + 1 < w.n_t(t)) {
+              scores(t, t, ki);
+              if (j + 2 == w.n_t(t)) mma_commit(bars.q_empty(t));
+            } else {
+              mma_commit(bars.o_done(t));
+            }
           }
+          __syncwarp();
         }
         if (!ok) break;
-        mma_commit(bars.empty(vi % C::slots));
-        if (j + 1 < w.n) mma_commit(bars.empty(ki % C::slots));
+        if (elect_one()) {
+          mma_commit(bars.empty(vi % C::slots));
+          if (j + 1 < w.n) mma_commit(bars.empty(ki % C::slots));
+        }
+        __syncwarp();
       }
     } else {
 #pragma unroll
@@ -492,34 +506,40 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
         ok = ok && kv_wait(first + 2 * t);
         if (!ok) continue;
         tc_fence_after();
-        scores(t, 0, first + 2 * t);
-        mma_commit(bars.empty((first + 2 * t) % C::slots));
+        if (elect_one()) {
+          scores(t, 0, first + 2 * t);
+          mma_commit(bars.empty((first + 2 * t) % C::slots));
+          if (t == 1 && w.n == 2) mma_commit(bars.q_empty(0));
+        }
+        __syncwarp();
       }
-      if (ok && w.n == 2) mma_commit(bars.q_empty(0));
       for (int j = 0; j < w.n && ok; ++j) {
         const uint32_t vi = first + 2 * j + 1, ki = vi + 3;
         const int t = j & 1;
-        ok = kv_wait(vi) && mbar_wait(bars.p_full(t), (t ? puse[1]++ : puse[0]++) & 1, p.status);
+        ok = kv_wait(vi) && wait(bars.p_full(t), (t ? puse1++ : puse0++) & 1);
         if (!ok) break;
         tc_fence_after();
-        weigh(t, vi, j > 1);
-        if (j + 2 < w.n) {
+        if (elect_one()) {
+          weigh(t, vi, j > 1);
+          if (j + 2 >= w.n) mma_commit(bars.o_done(t));
           mma_commit(bars.empty(vi % C::slots));
-          ok = kv_wait(ki);
-          if (!ok) break;
-          tc_fence_after();
+        }
+        __syncwarp();
+        if (j + 2 >= w.n) continue;
+        if (!(ok = kv_wait(ki))) break;
+        tc_fence_after();
+        if (elect_one()) {
           scores(t, 0, ki);
           mma_commit(bars.empty(ki % C::slots));
           if (j + 3 == w.n) mma_commit(bars.q_empty(0));
-        } else {
-          mma_commit(bars.o_done(t));
-          mma_commit(bars.empty(vi % C::slots));
         }
+        __syncwarp();
       }
     }
     first += 2 * w.n;
   }
-  mma_commit(bars.drained());
+  if (elect_one()) mma_commit(bars.drained());
+  __syncwarp();
   mbar_drain(bars.drained(), 0, p.status);
 }
 
@@ -731,7 +751,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
   const Bars bars = {base + C::bar_off};
   int* shape = reinterpret_cast<int*>(gbase + C::bar_off + 404);  // most tiles, most splits of a sequence, any out of range
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(bars.full(i), C::codes ? 128 : 1);
@@ -768,7 +788,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = lds32(bars.tmem_slot());
+  const uint32_t tmem = __shfl_sync(0xffffffffu, lds32(bars.tmem_slot()), 0);
   // how far the pieces reach, and which sequences are out of range
   {
     int tiles = 0, splits = 1, bad = 0;
@@ -796,8 +816,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
     if (warp == 8) {
-      if ((threadIdx.x & 31) == 0) issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
-      __syncwarp();
+      issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
     } else if (warp == 9) {
       load_tiles<D, TYPE>(p, sched, &km, &vm, base, bars);
     } else if (warp < 12) {
