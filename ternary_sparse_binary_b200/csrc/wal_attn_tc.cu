@@ -54,6 +54,7 @@ namespace {
 constexpr int kTile = 128;      // query rows of a tile, keys of a step
 constexpr int kScaleRing = 4;   // key tiles whose scales are held at once
 constexpr int kQThreads = 64;   // threads that load Q
+constexpr int kPoly = 4;        // one in so many pairs of weights goes without the exp2 unit
 constexpr float kLazy = 8.f;    // growth of the maximum, in log2, that O is rescaled for
 constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobody, so any number is right
 
@@ -125,9 +126,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one of them is
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -161,6 +162,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// 2^x for x in [-126, 8] without the exp2 unit: x = n + f, |f| <= 1/2, a cubic
+// in f fitted to the least relative error (2^-13.7, far below the 2^-8 of the
+// weights' rounding to bf16), and n added to the exponent.  Below -126 it
+// stays at 2^-126.
+__device__ __forceinline__ float2 poly_ex2(float2 x) {
+  const float2 big = make_float2(12582912.f, 12582912.f), nbig = make_float2(-12582912.f, -12582912.f);  // 1.5 * 2^23
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 t = add2(x, big), n = add2(t, nbig);
+  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+  float2 r = fma2(make_float2(0.055171434f, 0.055171434f), f, make_float2(0.24261081f, 0.24261081f));
+  r = fma2(r, f, make_float2(0.69326097f, 0.69326097f));
+  r = fma2(r, f, make_float2(0.99992812f, 0.99992812f));
+  r.x = __int_as_float(__float_as_int(r.x) + (__float_as_int(t.x) << 23));
+  r.y = __int_as_float(__float_as_int(r.y) + (__float_as_int(t.y) << 23));
+  return r;
+}
+
 struct Bars {
   uint32_t base;
   __device__ uint32_t full(int s) const { return base + 8u * s; }               // K/V tile ready for the MMAs
@@ -172,7 +191,8 @@ struct Bars {
   __device__ uint32_t q_full(int t) const { return base + 288u + 8u * t; }
   __device__ uint32_t q_empty(int t) const { return base + 304u + 8u * t; }
   __device__ uint32_t s_full(int t) const { return base + 320u + 8u * t; }      // scores in tensor memory
-  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // weights in tensor memory
+  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // weights in tensor memory: all,
+  __device__ uint32_t p_half(int t) const { return base + 416u + 8u * t; }      // and those of the first 64 keys
   __device__ uint32_t o_done(int t) const { return base + 352u + 8u * t; }      // the last product of a piece
   __device__ uint32_t ml_full() const { return base + 368u; }                   // the second half's m and l
   __device__ uint32_t ml_empty() const { return base + 376u; }
@@ -430,13 +450,25 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
   const uint64_t q_desc = sdesc_sw128(base), k_desc = sdesc_sw128(base + C::ring_off);
   const uint64_t v_desc = sdesc_mn_sw128(base + C::ring_off, 16384u);
-  uint32_t first = 0;             // ring item of the piece's first K tile
-  uint32_t quse0 = 0, quse1 = 0, puse0 = 0, puse1 = 0;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, p.status)); };
-  auto kv_wait = [&](uint32_t item) { return wait(bars.full(item % C::slots), (item / C::slots) & 1); };
+  uint32_t quse0 = 0, quse1 = 0, ph0 = 0, ph1 = 0;  // parities: of the Q tiles' uses, of the halves' weights
+  // Ring position of the next K or V tile.  The loop is on the path of every
+  // step, with few instructions between two waits: votes only after a group of
+  // them, no divisions, one elected region per group of MMAs.
+  struct Pos {
+    uint32_t slot, parity;
+    __device__ void next() {
+      if (++slot == C::slots) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+  } pos = {0, 0};
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, p.status); };
+  auto kv_wait = [&](const Pos& at) { return mbar_wait(bars.full(at.slot), at.parity, p.status); };
+  auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
   // the functions below run in the elected lane
-  auto scores = [&](int t, int qt, uint32_t item) {  // S_t = Q_qt K^T
-    const uint64_t a = q_desc + (uint64_t)(qt * (C::tile >> 4)), b = k_desc + (uint64_t)((item % C::slots) * (C::tile >> 4));
+  auto scores = [&](int t, int qt, uint32_t slot) {  // S_t = Q_qt K^T
+    const uint64_t a = q_desc + (uint64_t)(qt * (C::tile >> 4)), b = k_desc + (uint64_t)(slot * (C::tile >> 4));
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = ((k >> 2) * 16384u + (k & 3) * 32u) >> 4;
@@ -444,10 +476,10 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
     }
     mma_commit(bars.s_full(t));
   };
-  auto weigh = [&](int t, uint32_t item, bool more) {  // O_t (+)= P_t V
-    const uint64_t b = v_desc + (uint64_t)((item % C::slots) * (C::tile >> 4));
+  auto weigh = [&](int t, int half, uint32_t slot, bool more) {  // O_t (+)= P_t V over the first or last 64 keys
+    const uint64_t b = v_desc + (uint64_t)(slot * (C::tile >> 4));
 #pragma unroll
-    for (int k = 0; k < kTile / 16; ++k)
+    for (int k = 4 * half; k < 4 * half + 4; ++k)
       mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
   };
   bool ok = true;
@@ -456,87 +488,122 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
     Work w;
     AttnSeq s;
     if (!get_work<TYPE>(p, sched, i, w, s) || w.n == 0) continue;
-    if (w.has_q(0)) ok = wait(bars.q_full(0), quse0++ & 1);
-    if (ok && w.has_q(1)) ok = wait(bars.q_full(1), quse1++ & 1);
+    if (w.has_q(0)) {
+      ok = wait(bars.q_full(0), quse0);
+      quse0 ^= 1;
+    }
+    if (ok && w.has_q(1)) {
+      ok = wait(bars.q_full(1), quse1);
+      quse1 ^= 1;
+    }
+    Pos v = pos;  // V_j; `pos` itself runs over the K tiles
+    v.next();
+    ok = all(ok && kv_wait(pos));
     if (!ok) break;
+    tc_fence_after();
     if (!w.dual) {
-      if (!(ok = kv_wait(first))) break;
-      tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (w.n_t(t) > 0) {
-            scores(t, t, first);
+            scores(t, t, pos.slot);
             if (w.n_t(t) == 1) mma_commit(bars.q_empty(t));
           }
-        mma_commit(bars.empty(first % C::slots));
+        mma_commit(bars.empty(pos.slot));
       }
       __syncwarp();
-      for (int j = 0; j < w.n && ok; ++j) {
-        const uint32_t vi = first + 2 * j + 1, ki = vi + 1;
-        ok = kv_wait(vi);
-        if (ok && j + 1 < w.n) ok = kv_wait(ki);
+      for (int j = 0; j < w.n; ++j) {
+        pos.next();
+        pos.next();
+        const bool last = j + 1 == w.n;
+        ok = kv_wait(v) && (last || kv_wait(pos));
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || j >= w.n_t(t)) continue;
-          ok = wait(bars.p_full(t), (t ? puse1++ : puse0++) & 1);
-          if (!ok) continue;
+          if (j >= w.n_t(t)) continue;
+          uint32_t& ph = t ? ph1 : ph0;
+          ok = all(ok && wait(bars.p_half(t), ph));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) weigh(t, 0, v.slot, j > 0);
+          __syncwarp();
+          ok = all(wait(bars.p_full(t), ph));
+          if (!ok) break;
+          ph ^= 1;
           tc_fence_after();
           if (elect_one()) {
-            weigh(t, vi, j > 0);
+            weigh(t, 1, v.slot, true);
             if (j + 1 < w.n_t(t)) {
-              scores(t, t, ki);
+              scores(t, t, pos.slot);
               if (j + 2 == w.n_t(t)) mma_commit(bars.q_empty(t));
             } else {
               mma_commit(bars.o_done(t));
+            }
+            if (t == 1 || w.n1 == 0) {  // the step's last products
+              mma_commit(bars.empty(v.slot));
+              if (!last) mma_commit(bars.empty(pos.slot));
             }
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (elect_one()) {
-          mma_commit(bars.empty(vi % C::slots));
-          if (j + 1 < w.n) mma_commit(bars.empty(ki % C::slots));
-        }
-        __syncwarp();
+        v.next();
+        v.next();
       }
     } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        ok = ok && kv_wait(first + 2 * t);
-        if (!ok) continue;
+      Pos k1 = pos;
+      k1.next();
+      k1.next();
+      if (elect_one()) {
+        scores(0, 0, pos.slot);
+        mma_commit(bars.empty(pos.slot));
+      }
+      __syncwarp();
+      ok = all(kv_wait(k1));
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        scores(1, 0, k1.slot);
+        mma_commit(bars.empty(k1.slot));
+        if (w.n == 2) mma_commit(bars.q_empty(0));
+      }
+      __syncwarp();
+      Pos ahead = k1;  // K_{j + 2}
+      for (int j = 0; j < w.n; ++j) {
+        const int t = j & 1;
+        const uint32_t ph = t ? ph1 : ph0;
+        ok = all(kv_wait(v) && wait(bars.p_half(t), ph));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) weigh(t, 0, v.slot, j > 1);
+        __syncwarp();
+        ok = all(wait(bars.p_full(t), ph));
+        if (!ok) break;
+        if (t) ph1 ^= 1; else ph0 ^= 1;
         tc_fence_after();
         if (elect_one()) {
-          scores(t, 0, first + 2 * t);
-          mma_commit(bars.empty((first + 2 * t) % C::slots));
-          if (t == 1 && w.n == 2) mma_commit(bars.q_empty(0));
+          weigh(t, 1, v.slot, true);
+          if (j + 2 >= w.n) mma_commit(bars.o_done(t));
+          mma_commit(bars.empty(v.slot));
         }
         __syncwarp();
-      }
-      for (int j = 0; j < w.n && ok; ++j) {
-        const uint32_t vi = first + 2 * j + 1, ki = vi + 3;
-        const int t = j & 1;
-        ok = kv_wait(vi) && wait(bars.p_full(t), (t ? puse1++ : puse0++) & 1);
+        v.next();
+        v.next();
+        pos.next();
+        pos.next();
+        if (j + 2 >= w.n) continue;
+        ahead.next();
+        ahead.next();
+        ok = all(kv_wait(ahead));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          weigh(t, vi, j > 1);
-          if (j + 2 >= w.n) mma_commit(bars.o_done(t));
-          mma_commit(bars.empty(vi % C::slots));
-        }
-        __syncwarp();
-        if (j + 2 >= w.n) continue;
-        if (!(ok = kv_wait(ki))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          scores(t, 0, ki);
-          mma_commit(bars.empty(ki % C::slots));
+          scores(t, 0, ahead.slot);
+          mma_commit(bars.empty(ahead.slot));
           if (j + 3 == w.n) mma_commit(bars.q_empty(0));
         }
         __syncwarp();
       }
     }
-    first += 2 * w.n;
   }
   if (elect_one()) mma_commit(bars.drained());
   __syncwarp();
@@ -578,33 +645,44 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       tc_fence_after();
-      float x[kTile];
+      const int seen = lim - kb;                  // this row's keys in the tile
+      const bool masked = kb + kTile > lim0;
+      // First pass over the scores: the maximum.  They are read from tensor
+      // memory again below (about 110 cycles) rather than kept: that leaves one
+      // rolled loop, and the code of a step stays in the instruction cache of
+      // the warp schedulers, which the MMA warp shares.
+      float top;
+      {
+        float x[kTile];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
-      tmem_ld_wait();
-      if (C::codes) {
+        for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
+        tmem_ld_wait();
+        if (C::codes) {
 #pragma unroll
-        for (int q = 0; q < kTile; q += 2) {
-          const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
-          x[q] = y.x;
-          x[q + 1] = y.y;
+          for (int q = 0; q < kTile; q += 2) {
+            const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
+            x[q] = y.x;
+            x[q + 1] = y.y;
+          }
         }
-      }
-      if (kb + kTile > lim0) {
-        const int c = lim - kb;
+        if (masked) {
 #pragma unroll
-        for (int q = 0; q < kTile; ++q) x[q] = q < c ? x[q] : -INFINITY;
-      }
-      float mx = fmaxf(x[0], x[1]), mx1 = fmaxf(x[2], x[3]);
+          for (int q = 0; q < kTile; ++q) x[q] = q < seen ? x[q] : -INFINITY;
+        }
+        float mx[4];
 #pragma unroll
-      for (int q = 4; q < kTile; q += 4) {
-        mx = max3(mx, x[q], x[q + 1]);
-        mx1 = max3(mx1, x[q + 2], x[q + 3]);
+        for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
+#pragma unroll
+        for (int q = 8; q < kTile; q += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[q + 2 * e], x[q + 2 * e + 1]);
+        top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl;
       }
-      mx = fmaxf(mx, mx1) * sl;
-      const bool grow = mx > m + kLazy || (m == -INFINITY && mx > m);
+      const bool grow = !(top <= m + kLazy);
       if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? mx : m;
+        // a NaN or +inf among the scores makes the row NaN, and m says so: the
+        // cubic would not carry it
+        const float mn = !grow ? m : top < INFINITY ? top : __int_as_float(0x7FC00000);
         const float f = grow ? ex2(m - mn) : 1.f;  // 0 for a row that had no key yet
         m = mn;
         l *= f;
@@ -622,29 +700,58 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
       }
       const float ref = m == -INFINITY ? 0.f : -m;
       const float2 ref2 = make_float2(ref, ref);
-      float2 sum = make_float2(0.f, 0.f), sum_b = sum;
+      float2 sum = make_float2(0.f, 0.f);
+      // weights of 32 keys; every kPoly-th pair goes without the exp2 unit,
+      // which alone would take as long as the tensor core's part of the step
+      auto weights = [&](const float(&x)[32], int q) {
+        float2 sum_b = make_float2(0.f, 0.f);
+        float2 y[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+        for (int e = 0; e < 16; ++e) {
+          float2 z = make_float2(x[2 * e], x[2 * e + 1]);
+          if (C::codes) z = mul2(z, *reinterpret_cast<const float2*>(sc + 32 * q + 2 * e));
+          z = fma2(z, sl2, ref2);
+          if (e % kPoly == kPoly - 1) {
+            y[e] = poly_ex2(z);
+          } else {
+            y[e].x = ex2(z.x);
+            y[e].y = ex2(z.y);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            y[e].x = 32 * q + 2 * e < seen ? y[e].x : 0.f;
+            y[e].y = 32 * q + 2 * e + 1 < seen ? y[e].y : 0.f;
+          }
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int c = 32 * q + 2 * e;
-          float2 y = fma2(make_float2(x[c], x[c + 1]), sl2, ref2);
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          if (e & 1) sum_b = add2(sum_b, y); else sum = add2(sum, y);
-          if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + c));
-          pk[e] = dev::float2_to_bf16x2(y.x, y.y);
+          if (e & 1) sum_b = add2(sum_b, y[e]); else sum = add2(sum, y[e]);
+          if (C::codes) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(sc + kTile + 32 * q + 2 * e));
+          pk[e] = dev::float2_to_bf16x2(y[e].x, y[e].y);
         }
-        tmem_st16(t_s + 16u * q, pk);
-      }
-      sum = add2(sum, sum_b);
-      l += sum.x + sum.y;
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(bars.p_full(t));
-      if (C::codes) {  // eight arrivals free the scales: one of a warp, two where one half alone reads them
+        sum = add2(sum, sum_b);
+        tmem_st16(t_s + 16u * q, pk);  // over scores that have been read
+      };
+      float xa[32], xb[32];
+      tmem_ld32(t_s, xa);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        tmem_ld_wait();
+        tmem_ld32(t_s + 64u * half + 32u, xb);
+        weights(xa, 2 * half);
+        tmem_ld_wait();
+        if (half == 0) tmem_ld32(t_s + 64u, xa);
+        weights(xb, 2 * half + 1);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(half ? bars.p_full(t) : bars.p_half(t));
+      }
+      l += sum.x + sum.y;
+      if (C::codes) {  // eight arrivals free the scales: one of a warp, two where one half alone reads them
         if ((tid & 31) == 0) {
           mbar_arrive(bars.sc_empty(ti % kScaleRing));
           if (w.dual || w.rows <= kTile) mbar_arrive(bars.sc_empty(ti % kScaleRing));
@@ -771,7 +878,8 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       mbar_init(bars.q_full(t), kQThreads);
       mbar_init(bars.q_empty(t), 1);
       mbar_init(bars.s_full(t), 1);
-      mbar_init(bars.p_full(t), 128);
+      mbar_init(bars.p_full(t), 4);
+      mbar_init(bars.p_half(t), 4);
       mbar_init(bars.o_done(t), 1);
     }
     mbar_init(bars.ml_full(), 128);
