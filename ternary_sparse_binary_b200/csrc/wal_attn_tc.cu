@@ -4,7 +4,7 @@
 // the group), token-major, so the heads that share K and V share its tiles) as
 // two tiles of 128, and a range of keys, in tiles of 128:
 //   S_t = Q_t K^T          128 x 128, K-major operands from shared memory
-//   P_t = 2^(S_t - m)      in registers, one row a thread, back to tensor
+//   P_t = 2^(S_t - m)      in registers, half a row a thread, back to tensor
 //                          memory as bf16 over S_t's first half
 //   O_t += P_t V           A from tensor memory, V as it lies (MN-major)
 // While one tile's softmax runs on the CUDA cores, the tensor core works on the
@@ -12,13 +12,14 @@
 // that tile and every other key tile each.  CTAs are persistent: each role walks
 // the CTA's pieces by itself, so the loads and the first products of a piece run
 // under the end of the one before.
-//   warps 0-3, 4-7   softmax, rescaling and output of half 0 and 1
-//   warp 8           issues the MMAs
-//   warp 9           K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
+//   warps 0-7, 8-15  softmax, rescaling and output of half 0 and 1: the first
+//                    four of each take the first 64 columns, the others the rest
+//   warp 16          issues the MMAs
+//   warp 17          K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
 //                    into a ring in the 128-byte swizzle, 8-bit codes and their
 //                    scales into a ring as they lie
-//   warps 10, 11     Q
-//   warps 12-15      (8-bit) codes to bf16 tiles, exact; scales go to a ring of
+//   warps 18, 19     Q
+//   warps 20-23      (8-bit) codes to bf16 tiles, exact; scales go to a ring of
 //                    their own and meet S and P in fp32
 // The MMAs of one thread run in order, so S_t of the next keys may overwrite
 // P_t once P_t V has been issued, and a softmax that sees its S_t finished knows
@@ -59,23 +60,28 @@ constexpr float kLazy = 8.f;    // growth of the maximum, in log2, that O is res
 constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobody, so any number is right
 
 // Shared memory and registers.  Launched registers are shared out again by
-// setmaxnreg: 384 threads of 168 as 2 x 128 x 208 + 128 x 88, 512 threads of 128
-// as 2 x 128 x 176 + 2 x 128 x 80.
+// setmaxnreg: 640 threads of 96 as 512 x 104 + 128 x 64, 768 threads of 80 as
+// 512 x 96 + 256 x 48.
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool codes = TYPE != WAL_KV_BF16;
-  static constexpr int threads = codes ? 512 : 384;
-  static constexpr int soft_regs = codes ? 176 : 208, other_regs = codes ? 80 : 88;
+  static constexpr int threads = codes ? 768 : 640;
+  static constexpr int soft_regs = codes ? 96 : 104, other_regs = codes ? 48 : 64;
   static constexpr uint32_t tile = kTile * D * 2;                    // a Q, K or V tile in bf16
-  static constexpr int slots = D == 64 ? (codes ? 6 : 8) : (codes ? 3 : 5);
+  static constexpr int slots = D == 64 ? (codes ? 6 : 8) : (codes ? 3 : 4);
   static constexpr uint32_t raw = codes ? kTile * D + kTile * 4 : 0;  // a tile as it lies in the cache, and its scales
   static constexpr int raws = D == 64 ? 6 : 3;
   static constexpr uint32_t ring_off = 2 * tile;
   static constexpr uint32_t raw_off = ring_off + slots * tile;
   static constexpr uint32_t scale_off = raw_off + (codes ? raws * raw : 0);
-  static constexpr uint32_t ml_off = scale_off + (codes ? kScaleRing * 2 * kTile * 4 : 0);
-  static constexpr uint32_t bar_off = ml_off + kTile * 8;
+  // what the threads of a row tell each other: [step parity][half][columns][row]
+  // maxima, [half][columns][row] sums, [half][row] references
+  static constexpr uint32_t top_off = scale_off + (codes ? kScaleRing * 2 * kTile * 4 : 0);
+  static constexpr uint32_t sum_off = top_off + 8 * kTile * 4;
+  static constexpr uint32_t ref_off = sum_off + 4 * kTile * 4;
+  static constexpr uint32_t bar_off = ref_off + 2 * kTile * 4;
   static constexpr uint32_t smem = bar_off + 512 + 1024;             // barriers, slack for the alignment
+  static_assert(smem <= 232448, "above the shared memory of an SM");
 };
 
 // Instruction descriptor: A and B bf16, D fp32, M x N; B MN-major if asked.
@@ -126,6 +132,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A wait of a role that runs ahead: it polls now and then, and leaves the issue
+// slots to the others.  Bounded like mbar_wait.
+__device__ __forceinline__ bool wait_ahead(uint32_t bar, uint32_t parity, int32_t* status) {
+  for (uint32_t it = 0; it < kSpinLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    __nanosleep(40);
+  }
+  atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
+  return false;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one of them is
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -191,11 +207,13 @@ struct Bars {
   __device__ uint32_t q_full(int t) const { return base + 288u + 8u * t; }
   __device__ uint32_t q_empty(int t) const { return base + 304u + 8u * t; }
   __device__ uint32_t s_full(int t) const { return base + 320u + 8u * t; }      // scores in tensor memory
-  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // weights in tensor memory: all,
-  __device__ uint32_t p_half(int t) const { return base + 416u + 8u * t; }      // and those of the first 64 keys
+  __device__ uint32_t p_half(int t) const { return base + 416u + 8u * t; }      // weights in tensor memory: keys 0-31, 64-95,
+  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // and the others
   __device__ uint32_t o_done(int t) const { return base + 352u + 8u * t; }      // the last product of a piece
-  __device__ uint32_t ml_full() const { return base + 368u; }                   // the second half's m and l
-  __device__ uint32_t ml_empty() const { return base + 376u; }
+  __device__ uint32_t top_full(int t) const { return base + 432u + 8u * t; }    // a step's maxima of both column groups
+  __device__ uint32_t sum_full(int t) const { return base + 368u + 8u * t; }    // a piece's sums of both
+  __device__ uint32_t join() const { return base + 456u; }                // dual: half 1's sums are there
+  __device__ uint32_t o1_free() const { return base + 448u; }                   // dual: and have been joined
   __device__ uint32_t v_tail() const { return base + 384u; }
   __device__ uint32_t drained() const { return base + 392u; }
   __device__ uint32_t tmem_slot() const { return base + 400u; }
@@ -289,7 +307,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
       const int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int slot = item % kSlots;
-        if (item >= kSlots) ok = mbar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
+        if (item >= kSlots) ok = wait_ahead(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tail = !C::codes && kv == 1 && cnt < kTile;
@@ -349,9 +367,9 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
       const int si = tiles % kScaleRing;
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int rs = item % C::raws, slot = item % C::slots;
-        bool ok = mbar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
-        if (ok && kv == 0 && tiles >= kScaleRing) ok = mbar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
-        if (ok && item >= C::slots) ok = mbar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
+        bool ok = wait_ahead(bars.raw_full(rs), (item / C::raws) & 1, p.status);
+        if (ok && kv == 0 && tiles >= kScaleRing) ok = wait_ahead(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
+        if (ok && item >= C::slots) ok = wait_ahead(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
         if (!ok) return;
         const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
         // keys that are not there get codes and scales of zero
@@ -397,7 +415,7 @@ template <int D, int TYPE>
 __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr int kBatch = 4, kN = kTile * (D / 8) / kQThreads;
-  const int tid = threadIdx.x & (kQThreads - 1);
+  const int tid = threadIdx.x & (kQThreads - 1);  // of warps 18, 19
   // A negative scale is a sign on Q, a scale of zero makes it zero: the scores
   // are then multiplied by sl > 0.
   const uint32_t keep = p.scale_log2 == 0.f ? 0u : ~0u, flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -410,7 +428,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (!w.has_q(t)) continue;
-      if (uses[t] > 0 && !mbar_wait(bars.q_empty(t), (uses[t] - 1) & 1, p.status)) return;
+      if (uses[t] > 0 && !wait_ahead(bars.q_empty(t), (uses[t] - 1) & 1, p.status)) return;
       ++uses[t];
       const uint32_t dst = base + t * C::tile;
 #pragma unroll 1
@@ -476,11 +494,13 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
     }
     mma_commit(bars.s_full(t));
   };
-  auto weigh = [&](int t, int half, uint32_t slot, bool more) {  // O_t (+)= P_t V over the first or last 64 keys
+  auto weigh = [&](int t, int half, uint32_t slot, bool more) {  // O_t (+)= P_t V over the keys of p_half or the others
     const uint64_t b = v_desc + (uint64_t)(slot * (C::tile >> 4));
 #pragma unroll
-    for (int k = 4 * half; k < 4 * half + 4; ++k)
+    for (int i = 0; i < 4; ++i) {
+      const int k = 2 * half + (i & 1) + 4 * (i >> 1);
       mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
+    }
   };
   bool ok = true;
   const int64_t total = sched.total(p);
@@ -611,18 +631,28 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
 }
 
 // ---------------------------------------------------------------------------
-// softmax and output (four warps a half of the CTA, a row a thread)
+// softmax and output: four warps for a half of the CTA and 64 of the columns (g),
+// a row a thread
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, float sl, uint32_t base, const uint8_t* gbase,
-                                             uint32_t tmem, const Bars& bars) {
+__device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, int g, float sl, uint32_t base,
+                                             const uint8_t* gbase, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
+  constexpr int kCols = kTile / 2, kOut = D / 2;  // score and output columns of a thread
   const int tid = threadIdx.x & 127;
+  const bool lead = (tid & 31) == 0;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;
-  const uint32_t t_s = tmem + 128u * t + lanes, t_o = tmem + 256u + (uint32_t)D * t + lanes;
+  const uint32_t t_s = tmem + 128u * t + 64u * g + lanes, t_p = tmem + 128u * t + 32u * g + lanes;
+  const uint32_t t_o = tmem + 256u + (uint32_t)D * t + (uint32_t)kOut * g + lanes;
+  auto at = [&](uint32_t off, int i) { return base + off + (uint32_t)i * (kTile * 4) + 4u * tid; };  // row's word of array i
+  const uint32_t my_top = at(C::top_off, 2 * t + g), other_top = at(C::top_off, 2 * t + (g ^ 1));
   const float2 sl2 = make_float2(sl, sl);
-  uint32_t steps = 0, pieces = 0, duals = 0, tiles = 0;
-  bool ok = true;
+  uint32_t steps = 0, pieces = 0, sums = 0, duals = 0, tiles = 0;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, p.status)); };
+  auto arrive = [&](uint32_t bar) {  // for the warp
+    __syncwarp();
+    if (lead) mbar_arrive(bar);
+  };
   const int64_t total = sched.total(p);
   for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
     Work w;
@@ -630,54 +660,81 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     if (!get_work<TYPE>(p, sched, i, w, s)) continue;
     const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
     const int n = w.n_t(t);
-    // the half that writes these rows: both of a dual piece lead to half 0
-    const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
-    const int tok = live || w.dual ? min(row, w.r0 + w.rows - 1) / p.group : 0;
     const int lim = row < w.r0 + w.rows ? min(w.k1, attn_limit(s, row / p.group)) : w.k1;
     const int lim0 = __shfl_sync(0xffffffffu, lim, 0);  // the warp's smallest: limits grow with the row
     float m = -INFINITY, l = 0.f;
     for (int k = 0; k < n; ++k, ++steps) {
-      const int kb = w.k0 + kTile * w.tile_of(t, k);
+      const int kb = w.k0 + kTile * w.tile_of(t, k) + kCols * g;
       const uint32_t ti = tiles + w.tile_of(t, k);
-      const float* sc = reinterpret_cast<const float*>(gbase + C::scale_off) + (ti % kScaleRing) * 2 * kTile;
-      ok = mbar_wait(bars.s_full(t), steps & 1, p.status);
-      if (C::codes) ok = ok && mbar_wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
+      const float* sc = reinterpret_cast<const float*>(gbase + C::scale_off) + (ti % kScaleRing) * 2 * kTile + kCols * g;
+      if (!wait(bars.s_full(t), steps & 1)) return;
+      if (C::codes && !wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1)) return;
       tc_fence_after();
-      const int seen = lim - kb;                  // this row's keys in the tile
-      const bool masked = kb + kTile > lim0;
-      // First pass over the scores: the maximum.  They are read from tensor
-      // memory again below (about 110 cycles) rather than kept: that leaves one
-      // rolled loop, and the code of a step stays in the instruction cache of
-      // the warp schedulers, which the MMA warp shares.
-      float top;
-      {
-        float x[kTile];
+      float x[kCols];
+      tmem_ld32(t_s, x);
+      tmem_ld32(t_s + 32u, x + 32);
+      tmem_ld_wait();
+      if (C::codes) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
-        tmem_ld_wait();
-        if (C::codes) {
-#pragma unroll
-          for (int q = 0; q < kTile; q += 2) {
-            const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
-            x[q] = y.x;
-            x[q + 1] = y.y;
-          }
+        for (int q = 0; q < kCols; q += 2) {
+          const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
+          x[q] = y.x;
+          x[q + 1] = y.y;
         }
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < kTile; ++q) x[q] = q < seen ? x[q] : -INFINITY;
-        }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
-#pragma unroll
-        for (int q = 8; q < kTile; q += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[q + 2 * e], x[q + 2 * e + 1]);
-        top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl;
       }
+      const int seen = lim - kb;  // this row's keys among the columns
+      const bool masked = kb + kCols > lim0;
+      if (masked) {
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) x[q] = q < seen ? x[q] : -INFINITY;
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
+#pragma unroll
+      for (int q = 8; q < kCols; q += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[q + 2 * e], x[q + 2 * e + 1]);
+      float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl;
+      const uint32_t buf = (steps & 1) * (4 * kTile * 4);
+      sts32(my_top + buf, __float_as_uint(top));
+      tc_fence_before();
+      arrive(bars.top_full(t));
+
+      // weights of 32 keys; every kPoly-th pair goes without the exp2 unit,
+      // which alone would take as long as the tensor core's part of the step
+      auto weights = [&](int q, float ref, uint32_t(&pk)[16]) {
+        const float2 ref2 = make_float2(ref, ref);
+        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int c = 32 * q + 2 * e;
+          float2 y = fma2(make_float2(x[c], x[c + 1]), sl2, ref2);
+          if (e % kPoly == kPoly - 1) {
+            const float2 z = y;
+            y = poly_ex2(z);
+            if (masked) {  // the cubic's smallest weight is not zero
+              y.x = z.x == -INFINITY ? 0.f : y.x;
+              y.y = z.y == -INFINITY ? 0.f : y.y;
+            }
+          } else {
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+          }
+          if (e & 1) sum_b = add2(sum_b, y); else sum = add2(sum, y);
+          if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + c));
+          pk[e] = dev::float2_to_bf16x2(y.x, y.y);
+        }
+        sum = add2(sum, sum_b);
+        return sum.x + sum.y;
+      };
+      // The first 32 columns' weights need no new reference in most steps: they
+      // are computed while the other group's maximum is on its way.
+      uint32_t pk[16];
+      float sum = weights(0, m == -INFINITY ? 0.f : -m, pk);
+      if (!wait(bars.top_full(t), steps & 1)) return;
+      tc_fence_after();
+      top = max3(top, __uint_as_float(lds32(other_top + buf)), top);
       const bool grow = !(top <= m + kLazy);
       if (__any_sync(0xffffffffu, grow)) {
         // a NaN or +inf among the scores makes the row NaN, and m says so: the
@@ -688,7 +745,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
         l *= f;
         if (k > 0) {
 #pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
+          for (int q = 0; q < kOut / 16; ++q) {
             uint32_t o[16];
             tmem_ld16(t_o + 16u * q, o);
             tmem_ld_wait();
@@ -697,106 +754,63 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
             tmem_st16(t_o + 16u * q, o);
           }
         }
+        sum = weights(0, m == -INFINITY ? 0.f : -m, pk);
       }
-      const float ref = m == -INFINITY ? 0.f : -m;
-      const float2 ref2 = make_float2(ref, ref);
-      float2 sum = make_float2(0.f, 0.f);
-      // weights of 32 keys; every kPoly-th pair goes without the exp2 unit,
-      // which alone would take as long as the tensor core's part of the step
-      auto weights = [&](const float(&x)[32], int q) {
-        float2 sum_b = make_float2(0.f, 0.f);
-        float2 y[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 z = make_float2(x[2 * e], x[2 * e + 1]);
-          if (C::codes) z = mul2(z, *reinterpret_cast<const float2*>(sc + 32 * q + 2 * e));
-          z = fma2(z, sl2, ref2);
-          if (e % kPoly == kPoly - 1) {
-            y[e] = poly_ex2(z);
-          } else {
-            y[e].x = ex2(z.x);
-            y[e].y = ex2(z.y);
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            y[e].x = 32 * q + 2 * e < seen ? y[e].x : 0.f;
-            y[e].y = 32 * q + 2 * e + 1 < seen ? y[e].y : 0.f;
-          }
-        }
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (e & 1) sum_b = add2(sum_b, y[e]); else sum = add2(sum, y[e]);
-          if (C::codes) y[e] = mul2(y[e], *reinterpret_cast<const float2*>(sc + kTile + 32 * q + 2 * e));
-          pk[e] = dev::float2_to_bf16x2(y[e].x, y[e].y);
-        }
-        sum = add2(sum, sum_b);
-        tmem_st16(t_s + 16u * q, pk);  // over scores that have been read
-      };
-      float xa[32], xb[32];
-      tmem_ld32(t_s, xa);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        tmem_ld_wait();
-        tmem_ld32(t_s + 64u * half + 32u, xb);
-        weights(xa, 2 * half);
-        tmem_ld_wait();
-        if (half == 0) tmem_ld32(t_s + 64u, xa);
-        weights(xb, 2 * half + 1);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(half ? bars.p_full(t) : bars.p_half(t));
-      }
-      l += sum.x + sum.y;
-      if (C::codes) {  // eight arrivals free the scales: one of a warp, two where one half alone reads them
-        if ((tid & 31) == 0) {
-          mbar_arrive(bars.sc_empty(ti % kScaleRing));
-          if (w.dual || w.rows <= kTile) mbar_arrive(bars.sc_empty(ti % kScaleRing));
-        }
+      tmem_st16(t_p, pk);  // over scores: both groups have read theirs
+      tmem_st_wait();
+      tc_fence_before();
+      arrive(bars.p_half(t));
+      l += sum;
+      l += weights(1, m == -INFINITY ? 0.f : -m, pk);
+      tmem_st16(t_p + 16u, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      arrive(bars.p_full(t));
+      if (C::codes && lead) {  // sixteen arrivals free the scales: one of a warp, two where one half alone reads them
+        mbar_arrive(bars.sc_empty(ti % kScaleRing));
+        if (w.dual || w.rows <= kTile) mbar_arrive(bars.sc_empty(ti % kScaleRing));
       }
     }
     tiles += w.n;
 
-    // output: the row's sums over its keys, or its share of them
-    if (n > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bars.o_done(t), pieces & 1, p.status));
-      if (!ok) return;
-      ++pieces;
-    }
+    // output: the row's sums over its keys, or its share of them.  A dual
+    // piece's rows are half 0's to write.
+    const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
     float f = 1.f, f1 = 0.f;  // factors of this half's and the other half's sums
-    if (w.dual) {
-      const uint32_t ml = base + C::ml_off + 8u * tid;
-      if (t == 1) {
-        sts64(ml, make_uint2(__float_as_uint(m), __float_as_uint(l)));
-        tc_fence_after();
+    if (n > 0) {
+      if (!wait(bars.o_done(t), pieces & 1)) return;
+      tc_fence_after();
+      sts32(at(C::sum_off, 2 * t + g), __float_as_uint(l));
+      if (g == 0) sts32(at(C::ref_off, t), __float_as_uint(m));
+      ++pieces;
+      if (w.dual && t == 1) {  // half 0 takes it from here
         tc_fence_before();
-        mbar_arrive(bars.ml_full());  // O_1 is complete too: this thread has seen o_done
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.ml_empty(), duals & 1, p.status));
-        if (!ok) return;
-        ++duals;
+        arrive(bars.join());
+        if (!wait(bars.o1_free(), duals++ & 1)) return;
         continue;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(bars.ml_full(), duals & 1, p.status));
-      if (!ok) return;
-      ++duals;
-      const uint2 u = lds64(ml);
-      const float m1 = __uint_as_float(u.x), l1 = __uint_as_float(u.y), mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
-      f = ex2(m - ref);
-      f1 = ex2(m1 - ref);
-      m = mm;
-      l = l * f + l1 * f1;
+      arrive(bars.sum_full(t));
+      if (!wait(bars.sum_full(t), sums++ & 1)) return;
+      l += __uint_as_float(lds32(at(C::sum_off, 2 * t + (g ^ 1))));
+      if (w.dual) {
+        if (!wait(bars.join(), duals++ & 1)) return;
+        tc_fence_after();
+        const float l1 = __uint_as_float(lds32(at(C::sum_off, 2))) + __uint_as_float(lds32(at(C::sum_off, 3)));
+        const float m1 = __uint_as_float(lds32(at(C::ref_off, 1)));
+        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
+        f = ex2(m - ref);
+        f1 = ex2(m1 - ref);
+        m = mm;
+        l = l * f + l1 * f1;
+      }
     }
-    tc_fence_after();
+    const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
     const bool partial = p.n_split > 1;
-    const int head = w.h * p.group + (live ? row - tok * p.group : 0);
     const float inv = lim == 0 ? 0.f : 1.f / l;
     bool nan = false;
     const int64_t pr = (int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
 #pragma unroll
-    for (int q = 0; q < D / 32; ++q) {
+    for (int q = 0; q < kOut / 32; ++q) {
       float o[32];
       if (n > 0) {
         tmem_ld32(t_o + 32u * q, o);
@@ -806,14 +820,17 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
       }
       if (w.dual) {
-        float o1[32];
-        tmem_ld32(t_o + (uint32_t)D + 32u * q, o1);
-        tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = o[e] * f + o1[e] * f1;
+        for (int e0 = 0; e0 < 2; ++e0) {
+          uint32_t o1[16];
+          tmem_ld16(t_o + (uint32_t)D + 32u * q + 16u * e0, o1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[16 * e0 + e] = o[16 * e0 + e] * f + __uint_as_float(o1[e]) * f1;
+        }
       }
       if (live && partial) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * q);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + kOut * g + 32 * q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       } else if (live) {
@@ -824,7 +841,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
           nan |= a != a || b != b;
           u[e] = dev::float2_to_bf16x2(a, b);
         }
-        uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + 32 * q);
+        uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + kOut * g + 32 * q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dst[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
       }
@@ -832,10 +849,10 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     }
     if (w.dual) {
       tc_fence_before();
-      mbar_arrive(bars.ml_empty());
+      arrive(bars.o1_free());
     }
     if (partial) {
-      if (live) p.part_ml[pr] = make_float2(m, l);
+      if (live && g == 0) p.part_ml[pr] = make_float2(m, l);
       continue;
     }
     // a key that the row does not see may have made it NaN
@@ -871,25 +888,27 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       }
       for (int i = 0; i < kScaleRing; ++i) {
         mbar_init(bars.sc_full(i), 128);
-        mbar_init(bars.sc_empty(i), 8);
+        mbar_init(bars.sc_empty(i), 16);
       }
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars.q_full(t), kQThreads);
       mbar_init(bars.q_empty(t), 1);
       mbar_init(bars.s_full(t), 1);
-      mbar_init(bars.p_full(t), 4);
-      mbar_init(bars.p_half(t), 4);
+      mbar_init(bars.p_full(t), 8);
+      mbar_init(bars.p_half(t), 8);
+      mbar_init(bars.top_full(t), 8);
+      mbar_init(bars.sum_full(t), 8);
       mbar_init(bars.o_done(t), 1);
     }
-    mbar_init(bars.ml_full(), 128);
-    mbar_init(bars.ml_empty(), 128);
+    mbar_init(bars.join(), 8);
+    mbar_init(bars.o1_free(), 8);
     mbar_init(bars.v_tail(), 1);
     mbar_init(bars.drained(), 1);
     mbar_init_fence();
     shape[0] = shape[1] = shape[2] = 0;
   }
-  if (warp == 8) {
+  if (warp == 16) {
     tmem_alloc(bars.tmem_slot(), 512);
     tmem_relinquish();
   }
@@ -918,16 +937,16 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   }
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
-  if (warp < 8) {
+  if (warp < 16) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
-    softmax_rows<D, TYPE>(p, sched, warp >> 2, sl, base, gbase, tmem, bars);
+    softmax_rows<D, TYPE>(p, sched, warp >> 3, (warp >> 2) & 1, sl, base, gbase, tmem, bars);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
-    if (warp == 8) {
+    if (warp == 16) {
       issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       load_tiles<D, TYPE>(p, sched, &km, &vm, base, bars);
-    } else if (warp < 12) {
+    } else if (warp < 20) {
       load_q<D, TYPE>(p, sched, base, bars);
     } else {
       convert_tiles<D, TYPE>(p, sched, base, bars);
@@ -936,7 +955,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
