@@ -55,7 +55,7 @@ namespace {
 constexpr int kTile = 128;      // query rows of a tile, keys of a step
 constexpr int kScaleRing = 4;   // key tiles whose scales are held at once
 constexpr int kQThreads = 64;   // threads that load Q
-constexpr int kPoly = 4;        // one in so many pairs of weights goes without the exp2 unit
+constexpr int kPoly = 1000;        // one in so many pairs of weights goes without the exp2 unit
 constexpr float kLazy = 8.f;    // growth of the maximum, in log2, that O is rescaled for
 constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobody, so any number is right
 
@@ -132,16 +132,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A wait of a role that runs ahead: it polls now and then, and leaves the issue
-// slots to the others.  Bounded like mbar_wait.
-__device__ __forceinline__ bool wait_ahead(uint32_t bar, uint32_t parity, int32_t* status) {
-  for (uint32_t it = 0; it < kSpinLimit; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    __nanosleep(40);
-  }
-  atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
-  return false;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one of them is
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -307,7 +297,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
       const int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int slot = item % kSlots;
-        if (item >= kSlots) ok = wait_ahead(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
+        if (item >= kSlots) ok = mbar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tail = !C::codes && kv == 1 && cnt < kTile;
@@ -367,9 +357,9 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
       const int si = tiles % kScaleRing;
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int rs = item % C::raws, slot = item % C::slots;
-        bool ok = wait_ahead(bars.raw_full(rs), (item / C::raws) & 1, p.status);
-        if (ok && kv == 0 && tiles >= kScaleRing) ok = wait_ahead(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
-        if (ok && item >= C::slots) ok = wait_ahead(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
+        bool ok = mbar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
+        if (ok && kv == 0 && tiles >= kScaleRing) ok = mbar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
+        if (ok && item >= C::slots) ok = mbar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
         if (!ok) return;
         const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
         // keys that are not there get codes and scales of zero
@@ -411,43 +401,65 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
 // ---------------------------------------------------------------------------
 // Q tiles (two warps)
 // ---------------------------------------------------------------------------
+// 16-byte asynchronous copies, all of a tile in flight at once: a row may be any
+// (token, head), so no box fits every group.
 template <int D, int TYPE>
 __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
-  constexpr int kBatch = 4, kN = kTile * (D / 8) / kQThreads;
-  const int tid = threadIdx.x & (kQThreads - 1);  // of warps 18, 19
-  // A negative scale is a sign on Q, a scale of zero makes it zero: the scores
-  // are then multiplied by sl > 0.
-  const uint32_t keep = p.scale_log2 == 0.f ? 0u : ~0u, flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-  uint32_t uses[2] = {0, 0};
+  constexpr int kChunks = D / 8, kStep = kQThreads / kChunks;  // 16-byte chunks of a row, rows between a thread's copies
+  const int tid = threadIdx.x & (kQThreads - 1);               // of warps 18, 19
+  const int ch = tid % kChunks, r_first = tid / kChunks;
+  const int step_tok = kStep / p.group, step_head = kStep % p.group;
+  uint32_t uses0 = 0, uses1 = 0;
   const int64_t total = sched.total(p);
   for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
     Work w;
     AttnSeq s;
     if (!get_work<TYPE>(p, sched, i, w, s)) continue;
-#pragma unroll
+    const bool both = w.has_q(0) && w.has_q(1);
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {  // both tiles' copies, then what is left to do for each
+      if (!w.has_q(t)) continue;
+      uint32_t& uses = t ? uses1 : uses0;
+      if (uses > 0 && !mbar_wait(bars.q_empty(t), (uses - 1) & 1, p.status)) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+      }
+      ++uses;
+      const uint32_t dst = base + t * C::tile + (ch >> 3) * 16384u;
+      int row = w.r0 + kTile * t + r_first, tok = row / p.group, rem = row - tok * p.group;
+      const uint16_t* q = p.Q + s.q0 * p.ldq + (int64_t)w.h * p.group * D + 8 * ch;
+#pragma unroll 4
+      for (int r = r_first; r < kTile; r += kStep) {
+        const bool there = kTile * t + r < w.rows;  // other rows are zero
+        const uint16_t* src = there ? q + tok * p.ldq + rem * D : p.Q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + sw128(r, ch & 7)), "l"(src), "r"(there ? 16 : 0)
+                     : "memory");
+        tok += step_tok;
+        rem += step_head;
+        if (rem >= p.group) {
+          rem -= p.group;
+          ++tok;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       if (!w.has_q(t)) continue;
-      if (uses[t] > 0 && !wait_ahead(bars.q_empty(t), (uses[t] - 1) & 1, p.status)) return;
-      ++uses[t];
-      const uint32_t dst = base + t * C::tile;
+      if (both && t == 0)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      // A negative scale is a sign on Q, a scale of zero makes it zero: the
+      // scores are then multiplied by sl > 0.
+      if (p.scale_log2 <= 0.f) {
+        const uint32_t keep = p.scale_log2 == 0.f ? 0u : ~0u, flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const uint32_t dst = base + t * C::tile + (ch >> 3) * 16384u;
 #pragma unroll 1
-      for (int e0 = 0; e0 < kN; e0 += kBatch) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int idx = (e0 + e) * kQThreads + tid, r = kTile * t + idx / (D / 8), ch = idx % (D / 8);
-          v[e] = make_uint4(0, 0, 0, 0);
-          if (r < w.rows) {
-            const int row = w.r0 + r, tok = row / p.group, head = w.h * p.group + row - tok * p.group;
-            v[e] = __ldg(reinterpret_cast<const uint4*>(p.Q + (s.q0 + tok) * p.ldq + head * D) + ch);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int idx = (e0 + e) * kQThreads + tid, r = idx / (D / 8), ch = idx % (D / 8);
-          sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7),
-                 make_uint4((v[e].x & keep) ^ flip, (v[e].y & keep) ^ flip, (v[e].z & keep) ^ flip, (v[e].w & keep) ^ flip));
+        for (int r = r_first; r < kTile; r += kStep) {
+          const uint4 v = lds128(dst + sw128(r, ch & 7));
+          sts128(dst + sw128(r, ch & 7), make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip));
         }
       }
       fence_proxy_async_smem();
