@@ -4,7 +4,7 @@
 // the group), token-major, so the heads that share K and V share its tiles) as
 // two tiles of 128, and a range of keys, in tiles of 128:
 //   S_t = Q_t K^T          128 x 128, K-major operands from shared memory
-//   P_t = 2^(S_t - m)      in registers, half a row a thread, back to tensor
+//   P_t = 2^(S_t - m)      in registers, one row a thread, back to tensor
 //                          memory as bf16 over S_t's first half
 //   O_t += P_t V           A from tensor memory, V as it lies (MN-major)
 // While one tile's softmax runs on the CUDA cores, the tensor core works on the
@@ -12,21 +12,20 @@
 // that tile and every other key tile each.  CTAs are persistent: each role walks
 // the CTA's pieces by itself, so the loads and the first products of a piece run
 // under the end of the one before.
-//   warps 0-7, 8-15  softmax, rescaling and output of half 0 and 1: the first
-//                    four of each take the first 64 columns, the others the rest
-//   warp 16          issues the MMAs
-//   warp 17          K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
+//   warps 0-3, 4-7   softmax, rescaling and output of half 0 and 1
+//   warp 8           issues the MMAs
+//   warp 9           K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
 //                    into a ring in the 128-byte swizzle, 8-bit codes and their
 //                    scales into a ring as they lie
-//   warps 18, 19     Q
-//   warps 20-23      (8-bit) codes to bf16 tiles, exact; scales go to a ring of
+//   warps 10, 11     Q
+//   warps 12-15      (8-bit) codes to bf16 tiles, exact; scales go to a ring of
 //                    their own and meet S and P in fp32
 // The MMAs of one thread run in order, so S_t of the next keys may overwrite
 // P_t once P_t V has been issued, and a softmax that sees its S_t finished knows
 // that its O_t is too.
 //
 // The maximum is lazy: m follows the row's running maximum only when that has
-// grown by more than 2^8, since weights up to 2^8 and sums of them keep their
+// grown by more than 2^16, since weights up to 2^16 and sums of them keep their
 // relative precision in bf16 and fp32; O is then rescaled in tensor memory,
 // which after the first tiles hardly ever happens.  Weights are rounded to bf16
 // for the second product (2^-8 of a weight, averaged over the keys), scores, m,
@@ -55,31 +54,26 @@ namespace {
 constexpr int kTile = 128;      // query rows of a tile, keys of a step
 constexpr int kScaleRing = 4;   // key tiles whose scales are held at once
 constexpr int kQThreads = 64;   // threads that load Q
-constexpr int kPoly = 1000;        // one in so many pairs of weights goes without the exp2 unit
-constexpr float kLazy = 8.f;    // growth of the maximum, in log2, that O is rescaled for
+constexpr float kLazy = 16.f;   // growth of the maximum, in log2, that O is rescaled for
 constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobody, so any number is right
 
 // Shared memory and registers.  Launched registers are shared out again by
-// setmaxnreg: 640 threads of 96 as 512 x 104 + 128 x 64, 768 threads of 80 as
-// 512 x 96 + 256 x 48.
+// setmaxnreg: 384 threads of 168 as 256 x 208 + 128 x 88, 512 threads of 128 as
+// 256 x 176 + 256 x 80.
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool codes = TYPE != WAL_KV_BF16;
-  static constexpr int threads = codes ? 768 : 640;
-  static constexpr int soft_regs = codes ? 96 : 104, other_regs = codes ? 48 : 64;
+  static constexpr int threads = codes ? 512 : 384;
+  static constexpr int soft_regs = codes ? 176 : 208, other_regs = codes ? 80 : 88;
   static constexpr uint32_t tile = kTile * D * 2;                    // a Q, K or V tile in bf16
-  static constexpr int slots = D == 64 ? (codes ? 6 : 8) : (codes ? 3 : 4);
+  static constexpr int slots = D == 64 ? (codes ? 6 : 8) : (codes ? 3 : 5);
   static constexpr uint32_t raw = codes ? kTile * D + kTile * 4 : 0;  // a tile as it lies in the cache, and its scales
   static constexpr int raws = D == 64 ? 6 : 3;
   static constexpr uint32_t ring_off = 2 * tile;
   static constexpr uint32_t raw_off = ring_off + slots * tile;
   static constexpr uint32_t scale_off = raw_off + (codes ? raws * raw : 0);
-  // what the threads of a row tell each other: [step parity][half][columns][row]
-  // maxima, [half][columns][row] sums, [half][row] references
-  static constexpr uint32_t top_off = scale_off + (codes ? kScaleRing * 2 * kTile * 4 : 0);
-  static constexpr uint32_t sum_off = top_off + 8 * kTile * 4;
-  static constexpr uint32_t ref_off = sum_off + 4 * kTile * 4;
-  static constexpr uint32_t bar_off = ref_off + 2 * kTile * 4;
+  static constexpr uint32_t ml_off = scale_off + (codes ? kScaleRing * 2 * kTile * 4 : 0);  // half 1's m and l of each row
+  static constexpr uint32_t bar_off = ml_off + kTile * 8;
   static constexpr uint32_t smem = bar_off + 512 + 1024;             // barriers, slack for the alignment
   static_assert(smem <= 232448, "above the shared memory of an SM");
 };
@@ -168,24 +162,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-// 2^x for x in [-126, 8] without the exp2 unit: x = n + f, |f| <= 1/2, a cubic
-// in f fitted to the least relative error (2^-13.7, far below the 2^-8 of the
-// weights' rounding to bf16), and n added to the exponent.  Below -126 it
-// stays at 2^-126.
-__device__ __forceinline__ float2 poly_ex2(float2 x) {
-  const float2 big = make_float2(12582912.f, 12582912.f), nbig = make_float2(-12582912.f, -12582912.f);  // 1.5 * 2^23
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  const float2 t = add2(x, big), n = add2(t, nbig);
-  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
-  float2 r = fma2(make_float2(0.055171434f, 0.055171434f), f, make_float2(0.24261081f, 0.24261081f));
-  r = fma2(r, f, make_float2(0.69326097f, 0.69326097f));
-  r = fma2(r, f, make_float2(0.99992812f, 0.99992812f));
-  r.x = __int_as_float(__float_as_int(r.x) + (__float_as_int(t.x) << 23));
-  r.y = __int_as_float(__float_as_int(r.y) + (__float_as_int(t.y) << 23));
-  return r;
-}
-
 struct Bars {
   uint32_t base;
   __device__ uint32_t full(int s) const { return base + 8u * s; }               // K/V tile ready for the MMAs
@@ -197,11 +173,9 @@ struct Bars {
   __device__ uint32_t q_full(int t) const { return base + 288u + 8u * t; }
   __device__ uint32_t q_empty(int t) const { return base + 304u + 8u * t; }
   __device__ uint32_t s_full(int t) const { return base + 320u + 8u * t; }      // scores in tensor memory
-  __device__ uint32_t p_half(int t) const { return base + 416u + 8u * t; }      // weights in tensor memory: keys 0-31, 64-95,
-  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // and the others
+  __device__ uint32_t p_half(int t) const { return base + 416u + 8u * t; }      // weights in tensor memory: the first 64 keys',
+  __device__ uint32_t p_full(int t) const { return base + 336u + 8u * t; }      // and the others'
   __device__ uint32_t o_done(int t) const { return base + 352u + 8u * t; }      // the last product of a piece
-  __device__ uint32_t top_full(int t) const { return base + 432u + 8u * t; }    // a step's maxima of both column groups
-  __device__ uint32_t sum_full(int t) const { return base + 368u + 8u * t; }    // a piece's sums of both
   __device__ uint32_t join() const { return base + 456u; }                // dual: half 1's sums are there
   __device__ uint32_t o1_free() const { return base + 448u; }                   // dual: and have been joined
   __device__ uint32_t v_tail() const { return base + 384u; }
@@ -305,20 +279,18 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
         const uint32_t row_bytes = C::codes ? D + 4 : D * 2;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows) * row_bytes);
         __syncwarp();
-        for (int q = 0; q < boxes; ++q) {
-          const int pg = __shfl_sync(0xffffffffu, page, q);
-          if (lane == 0) {
-            if (C::codes) {
-              tma_4d(dst + (uint32_t)(q * box_rows) * D, kv ? vm : km, 0, y0, z0, pg, bar);
-              const float* sc = (kv ? p.vs : p.ks) + ((((int64_t)pg * p.n_kv_heads + w.h) << p.shift) + y0);
-              bulk_g2s(dst + kTile * D + (uint32_t)(q * box_rows) * 4u, sc, (uint32_t)box_rows * 4u, bar);
-            } else {
+        if (lane < boxes) {  // a lane for each page
+          if (C::codes) {
+            tma_4d(dst + (uint32_t)(lane * box_rows) * D, kv ? vm : km, 0, y0, z0, page, bar);
+            const float* sc = (kv ? p.vs : p.ks) + ((((int64_t)page * p.n_kv_heads + w.h) << p.shift) + y0);
+            bulk_g2s(dst + kTile * D + (uint32_t)(lane * box_rows) * 4u, sc, (uint32_t)box_rows * 4u, bar);
+          } else {
 #pragma unroll
-              for (int a = 0; a < D / 64; ++a)
-                tma_4d(dst + a * 16384u + (uint32_t)(q * box_rows) * 128u, kv ? vm : km, x0 + 64 * a, y0, z0, pg, bar);
-            }
+            for (int a = 0; a < D / 64; ++a)
+              tma_4d(dst + a * 16384u + (uint32_t)(lane * box_rows) * 128u, kv ? vm : km, x0 + 64 * a, y0, z0, page, bar);
           }
         }
+        __syncwarp();
         if (tail) {  // the piece's last V tile: zero the rows that hold no key of it
           ok = __all_sync(0xffffffffu, mbar_wait(bar, tails & 1, p.status));
           if (!ok) break;
@@ -407,7 +379,7 @@ template <int D, int TYPE>
 __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr int kChunks = D / 8, kStep = kQThreads / kChunks;  // 16-byte chunks of a row, rows between a thread's copies
-  const int tid = threadIdx.x & (kQThreads - 1);               // of warps 18, 19
+  const int tid = threadIdx.x & (kQThreads - 1);               // of warps 10, 11
   const int ch = tid % kChunks, r_first = tid / kChunks;
   const int step_tok = kStep / p.group, step_head = kStep % p.group;
   uint32_t uses0 = 0, uses1 = 0;
@@ -510,7 +482,7 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
     const uint64_t b = v_desc + (uint64_t)(slot * (C::tile >> 4));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = 2 * half + (i & 1) + 4 * (i >> 1);
+      const int k = 4 * half + i;
       mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
     }
   };
@@ -643,25 +615,21 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
 }
 
 // ---------------------------------------------------------------------------
-// softmax and output: four warps for a half of the CTA and 64 of the columns (g),
-// a row a thread
+// softmax and output (four warps for a half of the CTA, a row a thread)
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, int g, float sl, uint32_t base,
+__device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, float sl, uint32_t base,
                                              const uint8_t* gbase, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
-  constexpr int kCols = kTile / 2, kOut = D / 2;  // score and output columns of a thread
   const int tid = threadIdx.x & 127;
   const bool lead = (tid & 31) == 0;
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;
-  const uint32_t t_s = tmem + 128u * t + 64u * g + lanes, t_p = tmem + 128u * t + 32u * g + lanes;
-  const uint32_t t_o = tmem + 256u + (uint32_t)D * t + (uint32_t)kOut * g + lanes;
-  auto at = [&](uint32_t off, int i) { return base + off + (uint32_t)i * (kTile * 4) + 4u * tid; };  // row's word of array i
-  const uint32_t my_top = at(C::top_off, 2 * t + g), other_top = at(C::top_off, 2 * t + (g ^ 1));
+  const uint32_t t_s = tmem + 128u * t + lanes, t_o = tmem + 256u + (uint32_t)D * t + lanes;
   const float2 sl2 = make_float2(sl, sl);
-  uint32_t steps = 0, pieces = 0, sums = 0, duals = 0, tiles = 0;
+  uint32_t steps = 0, pieces = 0, duals = 0, tiles = 0;
   auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, p.status)); };
   auto arrive = [&](uint32_t bar) {  // for the warp
+    tc_fence_before();
     __syncwarp();
     if (lead) mbar_arrive(bar);
   };
@@ -676,88 +644,70 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     const int lim0 = __shfl_sync(0xffffffffu, lim, 0);  // the warp's smallest: limits grow with the row
     float m = -INFINITY, l = 0.f;
     for (int k = 0; k < n; ++k, ++steps) {
-      const int kb = w.k0 + kTile * w.tile_of(t, k) + kCols * g;
+      const int kb = w.k0 + kTile * w.tile_of(t, k);
       const uint32_t ti = tiles + w.tile_of(t, k);
-      const float* sc = reinterpret_cast<const float*>(gbase + C::scale_off) + (ti % kScaleRing) * 2 * kTile + kCols * g;
+      const float* sc = reinterpret_cast<const float*>(gbase + C::scale_off) + (ti % kScaleRing) * 2 * kTile;
       if (!wait(bars.s_full(t), steps & 1)) return;
       if (C::codes && !wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1)) return;
       tc_fence_after();
-      float x[kCols];
-      tmem_ld32(t_s, x);
-      tmem_ld32(t_s + 32u, x + 32);
+      float x[kTile];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
       tmem_ld_wait();
       if (C::codes) {
 #pragma unroll
-        for (int q = 0; q < kCols; q += 2) {
+        for (int q = 0; q < kTile; q += 2) {
           const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
           x[q] = y.x;
           x[q + 1] = y.y;
         }
       }
-      const int seen = lim - kb;  // this row's keys among the columns
-      const bool masked = kb + kCols > lim0;
-      if (masked) {
+      if (kb + kTile > lim0) {
+        const int seen = lim - kb;  // this row's keys in the tile
 #pragma unroll
-        for (int q = 0; q < kCols; ++q) x[q] = q < seen ? x[q] : -INFINITY;
+        for (int q = 0; q < kTile; ++q) x[q] = q < seen ? x[q] : -INFINITY;
       }
-      float mx[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
-#pragma unroll
-      for (int q = 8; q < kCols; q += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[q + 2 * e], x[q + 2 * e + 1]);
-      float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl;
-      const uint32_t buf = (steps & 1) * (4 * kTile * 4);
-      sts32(my_top + buf, __float_as_uint(top));
-      tc_fence_before();
-      arrive(bars.top_full(t));
-
-      // weights of 32 keys; every kPoly-th pair goes without the exp2 unit,
-      // which alone would take as long as the tensor core's part of the step
+      // weights of 32 keys into tensor memory (over scores that are in
+      // registers by now), and their sums
+      float2 sum[2];
       auto weights = [&](int q, float ref, uint32_t(&pk)[16]) {
         const float2 ref2 = make_float2(ref, ref);
-        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int c = 32 * q + 2 * e;
           float2 y = fma2(make_float2(x[c], x[c + 1]), sl2, ref2);
-          if (e % kPoly == kPoly - 1) {
-            const float2 z = y;
-            y = poly_ex2(z);
-            if (masked) {  // the cubic's smallest weight is not zero
-              y.x = z.x == -INFINITY ? 0.f : y.x;
-              y.y = z.y == -INFINITY ? 0.f : y.y;
-            }
-          } else {
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-          }
-          if (e & 1) sum_b = add2(sum_b, y); else sum = add2(sum, y);
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum[e & 1] = add2(sum[e & 1], y);
           if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + c));
           pk[e] = dev::float2_to_bf16x2(y.x, y.y);
         }
-        sum = add2(sum, sum_b);
-        return sum.x + sum.y;
       };
-      // The first 32 columns' weights need no new reference in most steps: they
-      // are computed while the other group's maximum is on its way.
-      uint32_t pk[16];
-      float sum = weights(0, m == -INFINITY ? 0.f : -m, pk);
-      if (!wait(bars.top_full(t), steps & 1)) return;
-      tc_fence_after();
-      top = max3(top, __uint_as_float(lds32(other_top + buf)), top);
+      // The first 64 keys' weights need no new reference in most steps: they are
+      // computed together with the maximum, and again if that has grown.
+      uint32_t pa[16], pb[16];
+      sum[0] = sum[1] = make_float2(0.f, 0.f);
+      float ref = m == -INFINITY ? 0.f : -m;
+      weights(0, ref, pa);
+      weights(1, ref, pb);
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
+#pragma unroll
+      for (int q = 8; q < kTile; q += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[q + 2 * e], x[q + 2 * e + 1]);
+      const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * sl;
       const bool grow = !(top <= m + kLazy);
       if (__any_sync(0xffffffffu, grow)) {
-        // a NaN or +inf among the scores makes the row NaN, and m says so: the
-        // cubic would not carry it
+        // a NaN or +inf among the scores makes the row NaN
         const float mn = !grow ? m : top < INFINITY ? top : __int_as_float(0x7FC00000);
         const float f = grow ? ex2(m - mn) : 1.f;  // 0 for a row that had no key yet
         m = mn;
         l *= f;
         if (k > 0) {
 #pragma unroll 1
-          for (int q = 0; q < kOut / 16; ++q) {
+          for (int q = 0; q < D / 16; ++q) {
             uint32_t o[16];
             tmem_ld16(t_o + 16u * q, o);
             tmem_ld_wait();
@@ -766,19 +716,24 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
             tmem_st16(t_o + 16u * q, o);
           }
         }
-        sum = weights(0, m == -INFINITY ? 0.f : -m, pk);
+        ref = m == -INFINITY ? 0.f : -m;
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+        weights(0, ref, pa);
+        weights(1, ref, pb);
       }
-      tmem_st16(t_p, pk);  // over scores: both groups have read theirs
+      tmem_st16(t_s, pa);
+      tmem_st16(t_s + 16u, pb);
       tmem_st_wait();
-      tc_fence_before();
       arrive(bars.p_half(t));
-      l += sum;
-      l += weights(1, m == -INFINITY ? 0.f : -m, pk);
-      tmem_st16(t_p + 16u, pk);
+      weights(2, ref, pa);
+      tmem_st16(t_s + 32u, pa);
+      weights(3, ref, pb);
+      tmem_st16(t_s + 48u, pb);
       tmem_st_wait();
-      tc_fence_before();
       arrive(bars.p_full(t));
-      if (C::codes && lead) {  // sixteen arrivals free the scales: one of a warp, two where one half alone reads them
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
+      if (C::codes && lead) {  // eight arrivals free the scales: one of a warp, two where one half alone reads them
         mbar_arrive(bars.sc_empty(ti % kScaleRing));
         if (w.dual || w.rows <= kTile) mbar_arrive(bars.sc_empty(ti % kScaleRing));
       }
@@ -790,31 +745,25 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
     float f = 1.f, f1 = 0.f;  // factors of this half's and the other half's sums
     if (n > 0) {
-      if (!wait(bars.o_done(t), pieces & 1)) return;
+      if (!wait(bars.o_done(t), pieces++ & 1)) return;
       tc_fence_after();
-      sts32(at(C::sum_off, 2 * t + g), __float_as_uint(l));
-      if (g == 0) sts32(at(C::ref_off, t), __float_as_uint(m));
-      ++pieces;
-      if (w.dual && t == 1) {  // half 0 takes it from here
-        tc_fence_before();
+    }
+    if (w.dual) {
+      const uint32_t ml = base + C::ml_off + 8u * tid;
+      if (t == 1) {  // half 0 takes it from here
+        sts64(ml, make_uint2(__float_as_uint(m), __float_as_uint(l)));
         arrive(bars.join());
         if (!wait(bars.o1_free(), duals++ & 1)) return;
         continue;
       }
-      arrive(bars.sum_full(t));
-      if (!wait(bars.sum_full(t), sums++ & 1)) return;
-      l += __uint_as_float(lds32(at(C::sum_off, 2 * t + (g ^ 1))));
-      if (w.dual) {
-        if (!wait(bars.join(), duals++ & 1)) return;
-        tc_fence_after();
-        const float l1 = __uint_as_float(lds32(at(C::sum_off, 2))) + __uint_as_float(lds32(at(C::sum_off, 3)));
-        const float m1 = __uint_as_float(lds32(at(C::ref_off, 1)));
-        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
-        f = ex2(m - ref);
-        f1 = ex2(m1 - ref);
-        m = mm;
-        l = l * f + l1 * f1;
-      }
+      if (!wait(bars.join(), duals++ & 1)) return;
+      tc_fence_after();
+      const uint2 u = lds64(ml);
+      const float m1 = __uint_as_float(u.x), l1 = __uint_as_float(u.y), mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
+      f = ex2(m - ref);
+      f1 = ex2(m1 - ref);
+      m = mm;
+      l = l * f + l1 * f1;
     }
     const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
     const bool partial = p.n_split > 1;
@@ -822,7 +771,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     bool nan = false;
     const int64_t pr = (int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
 #pragma unroll
-    for (int q = 0; q < kOut / 32; ++q) {
+    for (int q = 0; q < D / 32; ++q) {
       float o[32];
       if (n > 0) {
         tmem_ld32(t_o + 32u * q, o);
@@ -832,17 +781,14 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
       }
       if (w.dual) {
+        float o1[32];
+        tmem_ld32(t_o + (uint32_t)D + 32u * q, o1);
+        tmem_ld_wait();
 #pragma unroll
-        for (int e0 = 0; e0 < 2; ++e0) {
-          uint32_t o1[16];
-          tmem_ld16(t_o + (uint32_t)D + 32u * q + 16u * e0, o1);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[16 * e0 + e] = o[16 * e0 + e] * f + __uint_as_float(o1[e]) * f1;
-        }
+        for (int e = 0; e < 32; ++e) o[e] = o[e] * f + o1[e] * f1;
       }
       if (live && partial) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + kOut * g + 32 * q);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       } else if (live) {
@@ -853,18 +799,15 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
           nan |= a != a || b != b;
           u[e] = dev::float2_to_bf16x2(a, b);
         }
-        uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + kOut * g + 32 * q);
+        uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + 32 * q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dst[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
       }
       __syncwarp();
     }
-    if (w.dual) {
-      tc_fence_before();
-      arrive(bars.o1_free());
-    }
+    if (w.dual) arrive(bars.o1_free());
     if (partial) {
-      if (live && g == 0) p.part_ml[pr] = make_float2(m, l);
+      if (live) p.part_ml[pr] = make_float2(m, l);
       continue;
     }
     // a key that the row does not see may have made it NaN
@@ -900,27 +843,25 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       }
       for (int i = 0; i < kScaleRing; ++i) {
         mbar_init(bars.sc_full(i), 128);
-        mbar_init(bars.sc_empty(i), 16);
+        mbar_init(bars.sc_empty(i), 8);
       }
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars.q_full(t), kQThreads);
       mbar_init(bars.q_empty(t), 1);
       mbar_init(bars.s_full(t), 1);
-      mbar_init(bars.p_full(t), 8);
-      mbar_init(bars.p_half(t), 8);
-      mbar_init(bars.top_full(t), 8);
-      mbar_init(bars.sum_full(t), 8);
+      mbar_init(bars.p_full(t), 4);
+      mbar_init(bars.p_half(t), 4);
       mbar_init(bars.o_done(t), 1);
     }
-    mbar_init(bars.join(), 8);
-    mbar_init(bars.o1_free(), 8);
+    mbar_init(bars.join(), 4);
+    mbar_init(bars.o1_free(), 4);
     mbar_init(bars.v_tail(), 1);
     mbar_init(bars.drained(), 1);
     mbar_init_fence();
     shape[0] = shape[1] = shape[2] = 0;
   }
-  if (warp == 16) {
+  if (warp == 8) {
     tmem_alloc(bars.tmem_slot(), 512);
     tmem_relinquish();
   }
@@ -949,16 +890,16 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   }
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
-  if (warp < 16) {
+  if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
-    softmax_rows<D, TYPE>(p, sched, warp >> 3, (warp >> 2) & 1, sl, base, gbase, tmem, bars);
+    softmax_rows<D, TYPE>(p, sched, warp >> 2, sl, base, gbase, tmem, bars);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
-    if (warp == 16) {
+    if (warp == 8) {
       issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
-    } else if (warp == 17) {
+    } else if (warp == 9) {
       load_tiles<D, TYPE>(p, sched, &km, &vm, base, bars);
-    } else if (warp < 20) {
+    } else if (warp < 12) {
       load_q<D, TYPE>(p, sched, base, bars);
     } else {
       convert_tiles<D, TYPE>(p, sched, base, bars);
@@ -967,7 +908,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
