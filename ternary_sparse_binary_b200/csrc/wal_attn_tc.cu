@@ -654,42 +654,50 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
       tmem_ld_wait();
-      if (C::codes) {
+      const int seen = lim - kb;  // this row's keys in the tile
+      const bool masked = kb + kTile > lim0;
+      // scores of n keys from the q-th on: the keys' K scales, and -inf for keys
+      // that the row does not see
+      auto prepare = [&](float* v, int q, int n) {
+        if (C::codes) {
 #pragma unroll
-        for (int q = 0; q < kTile; q += 2) {
-          const float2 y = mul2(make_float2(x[q], x[q + 1]), *reinterpret_cast<const float2*>(sc + q));
-          x[q] = y.x;
-          x[q + 1] = y.y;
+          for (int e = 0; e < n; e += 2) {
+            const float2 y = mul2(make_float2(v[e], v[e + 1]), *reinterpret_cast<const float2*>(sc + q + e));
+            v[e] = y.x;
+            v[e + 1] = y.y;
+          }
         }
-      }
-      if (kb + kTile > lim0) {
-        const int seen = lim - kb;  // this row's keys in the tile
+        if (masked) {
 #pragma unroll
-        for (int q = 0; q < kTile; ++q) x[q] = q < seen ? x[q] : -INFINITY;
-      }
-      // weights of 32 keys into tensor memory (over scores that are in
-      // registers by now), and their sums
+          for (int e = 0; e < n; ++e) v[e] = q + e < seen ? v[e] : -INFINITY;
+        }
+      };
+      prepare(x, 0, kTile);
+      // weights of 32 keys, as bf16 pairs, and their sums
       float2 sum[2];
-      auto weights = [&](int q, float ref, uint32_t(&pk)[16]) {
+      auto weights = [&](int q, const float* v, float ref, uint32_t(&pk)[16]) {
         const float2 ref2 = make_float2(ref, ref);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int c = 32 * q + 2 * e;
-          float2 y = fma2(make_float2(x[c], x[c + 1]), sl2, ref2);
+          float2 y = fma2(make_float2(v[2 * e], v[2 * e + 1]), sl2, ref2);
           y.x = ex2(y.x);
           y.y = ex2(y.y);
           sum[e & 1] = add2(sum[e & 1], y);
-          if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + c));
+          if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + 32 * q + 2 * e));
           pk[e] = dev::float2_to_bf16x2(y.x, y.y);
         }
       };
       // The first 64 keys' weights need no new reference in most steps: they are
-      // computed together with the maximum, and again if that has grown.
+      // computed together with the maximum, and again if that has grown.  With
+      // codes there are not the registers for that: the scores are read again
+      // from tensor memory once the maximum is known.
       uint32_t pa[16], pb[16];
       sum[0] = sum[1] = make_float2(0.f, 0.f);
       float ref = m == -INFINITY ? 0.f : -m;
-      weights(0, ref, pa);
-      weights(1, ref, pb);
+      if (!C::codes) {
+        weights(0, x, ref, pa);
+        weights(1, x + 32, ref, pb);
+      }
       float mx[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
@@ -717,20 +725,40 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
           }
         }
         ref = m == -INFINITY ? 0.f : -m;
-        sum[0] = sum[1] = make_float2(0.f, 0.f);
-        weights(0, ref, pa);
-        weights(1, ref, pb);
+        if (!C::codes) {
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          weights(0, x, ref, pa);
+          weights(1, x + 32, ref, pb);
+        }
       }
-      tmem_st16(t_s, pa);
-      tmem_st16(t_s + 16u, pb);
-      tmem_st_wait();
-      arrive(bars.p_half(t));
-      weights(2, ref, pa);
-      tmem_st16(t_s + 32u, pa);
-      weights(3, ref, pb);
-      tmem_st16(t_s + 48u, pb);
-      tmem_st_wait();
-      arrive(bars.p_full(t));
+      // the weights go over scores that have been read
+      if (!C::codes) {
+        tmem_st16(t_s, pa);
+        tmem_st16(t_s + 16u, pb);
+        tmem_st_wait();
+        arrive(bars.p_half(t));
+        weights(2, x + 64, ref, pa);
+        tmem_st16(t_s + 32u, pa);
+        weights(3, x + 96, ref, pb);
+        tmem_st16(t_s + 48u, pb);
+        tmem_st_wait();
+        arrive(bars.p_full(t));
+      } else {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float v[64];
+          tmem_ld32(t_s + 64u * half, v);
+          tmem_ld32(t_s + 64u * half + 32u, v + 32);
+          tmem_ld_wait();
+          prepare(v, 64 * half, 64);
+          weights(2 * half, v, ref, pa);
+          tmem_st16(t_s + 32u * half, pa);
+          weights(2 * half + 1, v + 32, ref, pb);
+          tmem_st16(t_s + 32u * half + 16u, pb);
+          tmem_st_wait();
+          arrive(half ? bars.p_full(t) : bars.p_half(t));
+        }
+      }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
       if (C::codes && lead) {  // eight arrivals free the scales: one of a warp, two where one half alone reads them
