@@ -94,6 +94,7 @@ __device__ __noinline__ void attend_row(const AttnParams& p, const AttnSeq& s, i
     acc[i] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
+#pragma unroll 1
   for (int j = 0; j < lim; ++j) {
     float k[VPL], v[VPL];
     if (p.table && p.type != WAL_KV_BF16) {

@@ -82,19 +82,27 @@ struct Cfg {
 __device__ __forceinline__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
-// MN-major operand in the 128-byte swizzle: rows of 64 elements along MN, one
-// row per k, groups of eight rows 1024 bytes apart, the next 64 elements along
-// MN `mn_stride` bytes on.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn_stride >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
-}
-// D[tmem] (+)= A[tmem] * B[smem]^T
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// Shared-memory descriptors in the 128-byte swizzle, as two words: the start
+// address in 16-byte units (and, for V, the byte offset of the next 64 columns),
+// and what all tiles share: groups of eight rows 1024 bytes apart, version 1,
+// the swizzle.  Q and K are K-major; V is MN-major: rows of 64 elements along
+// the columns, one row per key, the next 64 columns 16 KB on.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescK = 1u << 16, kDescV = (16384u >> 4) << 16;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t offset_bits) { return ((saddr & 0x3FFFFu) >> 4) | offset_bits; }
+// D[tmem] (+)= A[smem] * B[smem]^T, and A[tmem] * B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
@@ -126,6 +134,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// mbar_wait with its loop rolled: the kernel has many waits, and its code must
+// stay small (see softmax_rows).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t* status) {
+#pragma unroll 1
+  for (uint32_t it = 0; it < kSpinLimit; ++it)
+    if (mbar_try_wait(bar, parity)) return true;
+  atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
+  return false;
+}
+// 32 bytes to a 32-byte aligned address: a whole sector, where two 16-byte
+// stores of lanes with rows of their own would send two halves.
+__device__ __forceinline__ void stg256(void* dst, const uint32_t* u) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+               "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one of them is
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -183,14 +207,6 @@ struct Bars {
   __device__ uint32_t tmem_slot() const { return base + 400u; }
 };
 
-// The pieces of work of a launch: (query tile pair, split of the keys,
-// sequence, K/V head), the pairs that see most keys first, so that the CTAs,
-// which take every gridDim.x-th piece, get about the same.
-struct Sched {
-  int tiles, splits;  // as many as the longest sequence has
-  __device__ int64_t total(const AttnParams& p) const { return (int64_t)tiles * splits * p.B * p.n_kv_heads; }
-};
-
 // A piece.  With more than one tile of rows, query tile t walks n_t[t] key
 // tiles.  With one (dual), both halves of the CTA walk its keys, half t the key
 // tiles t, t + 2, ..., and their sums are joined at the end.
@@ -205,37 +221,70 @@ struct Work {
   __device__ int tile_of(int t, int k) const { return dual ? 2 * k + t : k; }
 };
 
-// Piece i; false where there are no rows.
+// The pieces of a launch are (query tile pair, split of the keys, sequence, K/V
+// head), the pairs that see most keys first, so that the CTAs, which take every
+// gridDim.x-th piece, get about the same.  Each role walks its CTA's pieces by
+// itself; 32-bit numbers do (a launch with several splits has fewer than
+// kGrid pairs).
+struct Sched {
+  int tiles, splits;  // as many as the longest sequence has
+};
 template <int TYPE>
-__device__ __forceinline__ bool get_work(const AttnParams& p, const Sched& sc, int64_t i, Work& w, AttnSeq& s) {
-  const int64_t per = (int64_t)p.B * p.n_kv_heads, ts = i / per;
-  const int r = (int)(i - ts * per);
-  w.b = r / p.n_kv_heads;
-  w.h = r - w.b * p.n_kv_heads;
-  w.split = (int)(ts % sc.splits);
-  s = attn_seq(p, w.b);
-  const int rows_all = s.n_q * p.group;
-  w.r0 = (sc.tiles - 1 - (int)(ts / sc.splits)) * kTcAttnRows;
-  w.rows = min(kTcAttnRows, rows_all - w.r0);
-  if (w.rows <= 0) return false;
-  w.k0 = w.split * p.split_keys;
-  if (w.split > 0 && w.k0 >= s.len) return false;  // not a split of this sequence
-  w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
-  w.n = w.k1 > w.k0 ? (w.k1 - w.k0 + kTile - 1) / kTile : 0;
-  w.dual = w.rows <= kTile && w.n > 1;
-  if (w.dual) {
-    w.n0 = (w.n + 1) / 2;
-    w.n1 = w.n / 2;
-  } else {
-    w.n0 = w.n;
-    w.n1 = w.rows > kTile ? w.n : 0;
-    if (TYPE == WAL_KV_BF16 && w.rows > kTile) {  // the first tile's rows may see fewer keys
-      const int end = min(w.k1, attn_limit(s, (w.r0 + kTile - 1) / p.group));
-      w.n0 = end > w.k0 ? (end - w.k0 + kTile - 1) / kTile : 0;
+struct Walk {
+  const AttnParams& p;
+  const Sched sched;
+  int per, ts, r;  // (sequence, head) pairs, (tile pair, split), (sequence, head)
+  __device__ __forceinline__ Walk(const AttnParams& p_, const Sched& s_) : p(p_), sched(s_) {
+    per = p.B * p.n_kv_heads;
+    ts = (int)blockIdx.x / per;
+    r = (int)blockIdx.x - ts * per;
+  }
+  // The next piece that has rows.
+  __device__ __forceinline__ bool next(Work& w, AttnSeq& s) {
+#pragma unroll 1
+    for (; ts < sched.tiles * sched.splits; step()) {
+      int tile = ts;
+      w.split = 0;
+      if (sched.splits > 1) {
+        tile = ts / sched.splits;
+        w.split = ts - tile * sched.splits;
+      }
+      w.b = r / p.n_kv_heads;
+      w.h = r - w.b * p.n_kv_heads;
+      s = attn_seq(p, w.b);
+      w.r0 = (sched.tiles - 1 - tile) * kTcAttnRows;
+      w.rows = min(kTcAttnRows, s.n_q * p.group - w.r0);
+      if (w.rows <= 0) continue;
+      w.k0 = w.split * p.split_keys;
+      if (w.split > 0 && w.k0 >= s.len) continue;  // not a split of this sequence
+      w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
+      w.n = w.k1 > w.k0 ? (w.k1 - w.k0 + kTile - 1) / kTile : 0;
+      w.dual = w.rows <= kTile && w.n > 1;
+      if (w.dual) {
+        w.n0 = (w.n + 1) / 2;
+        w.n1 = w.n / 2;
+      } else {
+        w.n0 = w.n;
+        w.n1 = w.rows > kTile ? w.n : 0;
+        if (TYPE == WAL_KV_BF16 && w.rows > kTile) {  // the first tile's rows may see fewer keys
+          const int end = min(w.k1, attn_limit(s, (w.r0 + kTile - 1) / p.group));
+          w.n0 = end > w.k0 ? (end - w.k0 + kTile - 1) / kTile : 0;
+        }
+      }
+      step();
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ void step() {
+    r += (int)gridDim.x;
+    if (r >= per) {
+      const int q = r / per;
+      r -= q * per;
+      ts += q;
     }
   }
-  return true;
-}
+};
 
 // ---------------------------------------------------------------------------
 // K/V tiles by TMA (one warp): bf16 tiles as the MMAs want them, or codes and
@@ -253,11 +302,12 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
   auto empty = [&](int s) { return C::codes ? bars.raw_empty(s) : bars.empty(s); };
   uint32_t item = 0, tails = 0;
   bool ok = true, tail = false;
-  const int64_t total = sched.total(p);
-  for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-    Work w;
-    AttnSeq s;
-    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+  Walk<TYPE> walk(p, sched);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  while (ok && walk.next(w, s)) {
+#pragma unroll 1
     for (int j = 0; j < w.n && ok; ++j) {
       const int kb = w.k0 + kTile * j, cnt = min(kTile, w.k1 - kb);
       // this tile's boxes: lane i's page (paged) or the packed rows
@@ -269,9 +319,10 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
       }
       const int x0 = p.table ? 0 : w.h * D, z0 = p.table ? w.h : 0;
       const int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int slot = item % kSlots;
-        if (item >= kSlots) ok = mbar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
+        if (item >= kSlots) ok = bar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tail = !C::codes && kv == 1 && cnt < kTile;
@@ -292,9 +343,10 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
         }
         __syncwarp();
         if (tail) {  // the piece's last V tile: zero the rows that hold no key of it
-          ok = __all_sync(0xffffffffu, mbar_wait(bar, tails & 1, p.status));
+          ok = __all_sync(0xffffffffu, bar_wait(bar, tails & 1, p.status));
           if (!ok) break;
           ++tails;
+#pragma unroll 1
           for (int r8 = lane; r8 < (kTile - cnt) * (D / 8); r8 += 32) {
             const int r = cnt + r8 / (D / 8), ch = r8 % (D / 8);
             sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7), make_uint4(0, 0, 0, 0));
@@ -308,6 +360,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
   }
   // nothing of this warp's stays in flight, whatever its readers waited for
   if (!ok && tail) mbar_drain(bars.v_tail(), tails & 1, p.status);
+#pragma unroll 1
   for (uint32_t i = item > kSlots ? item - kSlots : 0; i < item; ++i) mbar_drain(full(i % kSlots), (i / kSlots) & 1, p.status);
 }
 
@@ -319,19 +372,21 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
   using C = Cfg<D, TYPE>;
   const int tid = threadIdx.x & 127;
   uint32_t item = 0, tiles = 0;
-  const int64_t total = sched.total(p);
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-    Work w;
-    AttnSeq s;
-    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+  Walk<TYPE> walk(p, sched);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  while (walk.next(w, s)) {
+#pragma unroll 1
     for (int j = 0; j < w.n; ++j, ++tiles) {
       const int cnt = min(kTile, w.k1 - w.k0 - kTile * j);
       const int si = tiles % kScaleRing;
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int rs = item % C::raws, slot = item % C::slots;
-        bool ok = mbar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
-        if (ok && kv == 0 && tiles >= kScaleRing) ok = mbar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
-        if (ok && item >= C::slots) ok = mbar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
+        bool ok = bar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
+        if (ok && kv == 0 && tiles >= kScaleRing) ok = bar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
+        if (ok && item >= C::slots) ok = bar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
         if (!ok) return;
         const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
         // keys that are not there get codes and scales of zero
@@ -383,17 +438,17 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
   const int ch = tid % kChunks, r_first = tid / kChunks;
   const int step_tok = kStep / p.group, step_head = kStep % p.group;
   uint32_t uses0 = 0, uses1 = 0;
-  const int64_t total = sched.total(p);
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-    Work w;
-    AttnSeq s;
-    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+  Walk<TYPE> walk(p, sched);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  while (walk.next(w, s)) {
     const bool both = w.has_q(0) && w.has_q(1);
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {  // both tiles' copies, then what is left to do for each
       if (!w.has_q(t)) continue;
       uint32_t& uses = t ? uses1 : uses0;
-      if (uses > 0 && !mbar_wait(bars.q_empty(t), (uses - 1) & 1, p.status)) {
+      if (uses > 0 && !bar_wait(bars.q_empty(t), (uses - 1) & 1, p.status)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
@@ -450,12 +505,8 @@ template <int D, int TYPE>
 __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sched, uint32_t base, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
-  const uint64_t q_desc = sdesc_sw128(base), k_desc = sdesc_sw128(base + C::ring_off);
-  const uint64_t v_desc = sdesc_mn_sw128(base + C::ring_off, 16384u);
-  uint32_t quse0 = 0, quse1 = 0, ph0 = 0, ph1 = 0;  // parities: of the Q tiles' uses, of the halves' weights
-  // Ring position of the next K or V tile.  The loop is on the path of every
-  // step, with few instructions between two waits: votes only after a group of
-  // them, no divisions, one elected region per group of MMAs.
+  const uint32_t q_lo = desc_lo(base, kDescK), k_lo = desc_lo(base + C::ring_off, kDescK), v_lo = desc_lo(base + C::ring_off, kDescV);
+  // Ring position of a K or V tile.
   struct Pos {
     uint32_t slot, parity;
     __device__ void next() {
@@ -464,34 +515,38 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
         parity ^= 1;
       }
     }
-  } pos = {0, 0};
-  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, p.status); };
-  auto kv_wait = [&](const Pos& at) { return mbar_wait(bars.full(at.slot), at.parity, p.status); };
+    __device__ void next2() {
+      next();
+      next();
+    }
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.status); };
+  auto kv_wait = [&](const Pos& at) { return bar_wait(bars.full(at.slot), at.parity, p.status); };
   auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
   // the functions below run in the elected lane
   auto scores = [&](int t, int qt, uint32_t slot) {  // S_t = Q_qt K^T
-    const uint64_t a = q_desc + (uint64_t)(qt * (C::tile >> 4)), b = k_desc + (uint64_t)(slot * (C::tile >> 4));
+    const uint32_t a = q_lo + qt * (C::tile >> 4), b = k_lo + slot * (C::tile >> 4), d = tmem + 128u * t;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = ((k >> 2) * 16384u + (k & 3) * 32u) >> 4;
-      mma_f16(tmem + 128u * t, a + off, b + off, id_s, k > 0);
+      mma_ss(d, a + off, b + off, id_s, k > 0);
     }
     mma_commit(bars.s_full(t));
   };
-  auto weigh = [&](int t, int half, uint32_t slot, bool more) {  // O_t (+)= P_t V over the keys of p_half or the others
-    const uint64_t b = v_desc + (uint64_t)(slot * (C::tile >> 4));
+  auto weigh = [&](int t, int half, uint32_t slot, bool more) {  // O_t (+)= P_t V over the first or last 64 keys
+    const uint32_t a = tmem + 128u * t + 32u * half, b = v_lo + slot * (C::tile >> 4) + half * (8192u >> 4), d = tmem + 256u + (uint32_t)D * t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 4 * half + i;
-      mma_f16_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
-    }
+    for (int k = 0; k < 4; ++k) mma_ts(d, a + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
   };
+  Pos pos = {0, 0};                                  // the piece's next K tile
+  uint32_t quse0 = 0, quse1 = 0, ph0 = 0, ph1 = 0;  // parities: of the Q tiles' uses, of the halves' weights
   bool ok = true;
-  const int64_t total = sched.total(p);
-  for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-    Work w;
-    AttnSeq s;
-    if (!get_work<TYPE>(p, sched, i, w, s) || w.n == 0) continue;
+  Walk<TYPE> walk(p, sched);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  while (ok && walk.next(w, s)) {
+    if (w.n == 0) continue;
     if (w.has_q(0)) {
       ok = wait(bars.q_full(0), quse0);
       quse0 ^= 1;
@@ -500,113 +555,64 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
       ok = wait(bars.q_full(1), quse1);
       quse1 ^= 1;
     }
-    Pos v = pos;  // V_j; `pos` itself runs over the K tiles
+    const int ahead = w.dual ? 2 : 1;  // K tiles that S runs ahead of the weights
+    Pos v = pos;                        // V_j
     v.next();
-    ok = all(ok && kv_wait(pos));
-    if (!ok) break;
-    tc_fence_after();
-    if (!w.dual) {
-      if (elect_one()) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (w.n_t(t) > 0) {
-            scores(t, t, pos.slot);
-            if (w.n_t(t) == 1) mma_commit(bars.q_empty(t));
-          }
-        mma_commit(bars.empty(pos.slot));
-      }
-      __syncwarp();
-      for (int j = 0; j < w.n; ++j) {
-        pos.next();
-        pos.next();
-        const bool last = j + 1 == w.n;
-        ok = kv_wait(v) && (last || kv_wait(pos));
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j >= w.n_t(t)) continue;
-          uint32_t& ph = t ? ph1 : ph0;
-          ok = all(ok && wait(bars.p_half(t), ph));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) weigh(t, 0, v.slot, j > 0);
-          __syncwarp();
-          ok = all(wait(bars.p_full(t), ph));
-          if (!ok) break;
-          ph ^= 1;
-          tc_fence_after();
-          if (elect_one()) {
-            weigh(t, 1, v.slot, true);
-            if (j + 1 < w.n_t(t)) {
-              scores(t, t, pos.slot);
-              if (j + 2 == w.n_t(t)) mma_commit(bars.q_empty(t));
-            } else {
-              mma_commit(bars.o_done(t));
-            }
-            if (t == 1 || w.n1 == 0) {  // the step's last products
-              mma_commit(bars.empty(v.slot));
-              if (!last) mma_commit(bars.empty(pos.slot));
-            }
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        v.next();
-        v.next();
-      }
-    } else {
-      Pos k1 = pos;
-      k1.next();
-      k1.next();
-      if (elect_one()) {
-        scores(0, 0, pos.slot);
-        mma_commit(bars.empty(pos.slot));
-      }
-      __syncwarp();
-      ok = all(kv_wait(k1));
+    // the first scores of both halves: of one K tile, or (dual) of two
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+      if (w.n_t(t) == 0) continue;
+      ok = all(ok && kv_wait(pos));
       if (!ok) break;
       tc_fence_after();
+      const bool last = w.dual || t == 1 || w.n1 == 0;  // of the K tile's readers
       if (elect_one()) {
-        scores(1, 0, k1.slot);
-        mma_commit(bars.empty(k1.slot));
-        if (w.n == 2) mma_commit(bars.q_empty(0));
+        scores(t, w.dual ? 0 : t, pos.slot);
+        if (w.dual ? t == 1 && w.n == 2 : w.n_t(t) == 1) mma_commit(bars.q_empty(w.dual ? 0 : t));
+        if (last) mma_commit(bars.empty(pos.slot));
       }
       __syncwarp();
-      Pos ahead = k1;  // K_{j + 2}
-      for (int j = 0; j < w.n; ++j) {
-        const int t = j & 1;
+      if (last) pos.next2();
+    }
+#pragma unroll 1
+    for (int j = 0; j < w.n && ok; ++j) {
+      const bool more_k = j + ahead < w.n;  // `pos` is there
+#pragma unroll 1
+      for (int t = w.dual ? j & 1 : 0; t < 2; ++t) {
+        if (!w.dual && j >= w.n_t(t)) continue;
         const uint32_t ph = t ? ph1 : ph0;
         ok = all(kv_wait(v) && wait(bars.p_half(t), ph));
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) weigh(t, 0, v.slot, j > 1);
+        if (elect_one()) weigh(t, 0, v.slot, j >= ahead);
         __syncwarp();
+        const bool again = j + ahead < (w.dual ? w.n : w.n_t(t));  // this half has another tile
+        const bool last = w.dual || t == 1 || w.n1 == 0;            // of the step's products
         ok = all(wait(bars.p_full(t), ph));
         if (!ok) break;
         if (t) ph1 ^= 1; else ph0 ^= 1;
         tc_fence_after();
         if (elect_one()) {
           weigh(t, 1, v.slot, true);
-          if (j + 2 >= w.n) mma_commit(bars.o_done(t));
-          mma_commit(bars.empty(v.slot));
+          if (last) mma_commit(bars.empty(v.slot));
+          if (!again) mma_commit(bars.o_done(t));
         }
         __syncwarp();
-        v.next();
-        v.next();
-        pos.next();
-        pos.next();
-        if (j + 2 >= w.n) continue;
-        ahead.next();
-        ahead.next();
-        ok = all(kv_wait(ahead));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          scores(t, 0, ahead.slot);
-          mma_commit(bars.empty(ahead.slot));
-          if (j + 3 == w.n) mma_commit(bars.q_empty(0));
+        if (again) {  // while the tensor core weighs; in a short ring this tile takes the place of V's
+          ok = all(kv_wait(pos));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            scores(t, w.dual ? 0 : t, pos.slot);
+            if (j + ahead + 1 == (w.dual ? w.n : w.n_t(t))) mma_commit(bars.q_empty(w.dual ? 0 : t));
+            if (last) mma_commit(bars.empty(pos.slot));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (w.dual) break;
       }
+      v.next2();
+      if (more_k) pos.next2();
     }
   }
   if (elect_one()) mma_commit(bars.drained());
@@ -617,6 +623,10 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
 // ---------------------------------------------------------------------------
 // softmax and output (four warps for a half of the CTA, a row a thread)
 // ---------------------------------------------------------------------------
+// The loops over steps and pieces are kept rolled here and in the other roles:
+// the schedulers' instruction caches are small, and code that is fetched anew
+// in every step costs the MMA warp, which runs each of its instructions once a
+// step, several times what the instructions do.
 template <int D, int TYPE>
 __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, float sl, uint32_t base,
                                              const uint8_t* gbase, uint32_t tmem, const Bars& bars) {
@@ -626,23 +636,25 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
   const uint32_t lanes = (uint32_t)(tid & 96) << 16;
   const uint32_t t_s = tmem + 128u * t + lanes, t_o = tmem + 256u + (uint32_t)D * t + lanes;
   const float2 sl2 = make_float2(sl, sl);
+  const bool sectors = (((uintptr_t)p.O | (uintptr_t)(p.ldo * 2)) & 31) == 0;  // every row of O starts on 32 bytes
   uint32_t steps = 0, pieces = 0, duals = 0, tiles = 0;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, p.status)); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, bar_wait(bar, parity, p.status)); };
   auto arrive = [&](uint32_t bar) {  // for the warp
     tc_fence_before();
     __syncwarp();
     if (lead) mbar_arrive(bar);
   };
-  const int64_t total = sched.total(p);
-  for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-    Work w;
-    AttnSeq s;
-    if (!get_work<TYPE>(p, sched, i, w, s)) continue;
+  Walk<TYPE> walk(p, sched);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  while (walk.next(w, s)) {
     const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
     const int n = w.n_t(t);
     const int lim = row < w.r0 + w.rows ? min(w.k1, attn_limit(s, row / p.group)) : w.k1;
     const int lim0 = __shfl_sync(0xffffffffu, lim, 0);  // the warp's smallest: limits grow with the row
     float m = -INFINITY, l = 0.f;
+#pragma unroll 1
     for (int k = 0; k < n; ++k, ++steps) {
       const int kb = w.k0 + kTile * w.tile_of(t, k);
       const uint32_t ti = tiles + w.tile_of(t, k);
@@ -687,17 +699,6 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
           pk[e] = dev::float2_to_bf16x2(y.x, y.y);
         }
       };
-      // The first 64 keys' weights need no new reference in most steps: they are
-      // computed together with the maximum, and again if that has grown.  With
-      // codes there are not the registers for that: the scores are read again
-      // from tensor memory once the maximum is known.
-      uint32_t pa[16], pb[16];
-      sum[0] = sum[1] = make_float2(0.f, 0.f);
-      float ref = m == -INFINITY ? 0.f : -m;
-      if (!C::codes) {
-        weights(0, x, ref, pa);
-        weights(1, x + 32, ref, pb);
-      }
       float mx[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) mx[q] = max3(x[2 * q], x[2 * q + 1], x[2 * q]);
@@ -724,16 +725,16 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
             tmem_st16(t_o + 16u * q, o);
           }
         }
-        ref = m == -INFINITY ? 0.f : -m;
-        if (!C::codes) {
-          sum[0] = sum[1] = make_float2(0.f, 0.f);
-          weights(0, x, ref, pa);
-          weights(1, x + 32, ref, pb);
-        }
       }
-      // the weights go over scores that have been read
+      const float ref = m == -INFINITY ? 0.f : -m;
+      sum[0] = sum[1] = make_float2(0.f, 0.f);
+      uint32_t pa[16], pb[16];
+      // The weights go over scores that have been read.  With codes there are
+      // not the registers to keep 128 of them: they are read again.
       if (!C::codes) {
+        weights(0, x, ref, pa);
         tmem_st16(t_s, pa);
+        weights(1, x + 32, ref, pb);
         tmem_st16(t_s + 16u, pb);
         tmem_st_wait();
         arrive(bars.p_half(t));
@@ -798,7 +799,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     const float inv = lim == 0 ? 0.f : 1.f / l;
     bool nan = false;
     const int64_t pr = (int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       float o[32];
       if (n > 0) {
@@ -816,9 +817,8 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
         for (int e = 0; e < 32; ++e) o[e] = o[e] * f + o1[e] * f1;
       }
       if (live && partial) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * q);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int e = 0; e < 4; ++e) stg256(p.part_o + pr * D + 32 * q + 8 * e, reinterpret_cast<const uint32_t*>(o) + 8 * e);
       } else if (live) {
         uint32_t u[16];
 #pragma unroll
@@ -827,9 +827,15 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
           nan |= a != a || b != b;
           u[e] = dev::float2_to_bf16x2(a, b);
         }
-        uint4* dst = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D + 32 * q);
+        uint16_t* dst = p.O + (s.q0 + tok) * p.ldo + head * D + 32 * q;
+        if (sectors) {
+          stg256(dst, u);
+          stg256(dst + 16, u + 8);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+          for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint4*>(dst)[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+        }
       }
       __syncwarp();
     }
@@ -840,6 +846,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     }
     // a key that the row does not see may have made it NaN
     uint32_t again = __ballot_sync(0xffffffffu, live && nan && lim < w.k1);
+#pragma unroll 1
     while (again) {
       const int src = __ffs(again) - 1;
       again &= again - 1;
@@ -860,6 +867,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   int* shape = reinterpret_cast<int*>(gbase + C::bar_off + 404);  // most tiles, most splits of a sequence, any out of range
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(bars.full(i), C::codes ? 128 : 1);
       mbar_init(bars.empty(i), 1);
@@ -900,6 +908,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   // how far the pieces reach, and which sequences are out of range
   {
     int tiles = 0, splits = 1, bad = 0;
+#pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += C::threads) {
       const AttnSeq s = attn_seq(p, b);
       bad |= s.bad;

@@ -261,6 +261,40 @@ def test_extreme_scores(n_q):
         assert np.all(np.abs(got[i] - ref) <= 2.0 ** -8 * (size + np.abs(ref)) * 1.01)
 
 
+@pytest.mark.parametrize("n_q,L,typ", [(200, 700, "bf16"), (20, 700, "bf16"), (20, 700, "int8"), (20, 9000, "bf16"), (1, 900, "int8"), (300, 300, "bf16")])
+def test_scores_that_jump(n_q, L, typ):
+    """One key among the later ones tops all before it by hundreds of nats, for
+    every other column of the batch's rows: its value alone remains."""
+    w = wal()
+    rng = np.random.default_rng(L + n_q)
+    D, page = 64, 16
+    (k, v, ks, vs), table, kv, vv = random_cache(rng, [L], page, 1, D, typ)
+    jump = L - n_q // 2 - 1 if n_q > 1 else L - 5
+    scale = 1.0 / D
+    kv, vv = kv[0].copy(), vv[0]
+    pg, off = table[0, jump // page], jump % page
+    if typ == "bf16":
+        k[pg, 0, off] = 1000.0
+        kv[jump] = 1000.0
+    else:
+        k[pg, 0, off] = 100
+        ks[pg, 0, off] = 10.0
+        kv[jump] = 1000.0
+    q = bf16(np.ones((n_q, 2 * D)) * np.where(np.arange(2 * D) < D, 1.0, -1.0) + 0.25 * rng.normal(size=(n_q, 2 * D)))
+    Q = torch.from_numpy(q).bfloat16().cuda()
+    O = torch.empty_like(Q)
+    w.KvCache(*[dev(t) for t in (k, v, ks, vs)]).attend(Q, i32([0, n_q]), i32([L]), torch.from_numpy(table).cuda(), O,
+                                                        max_q=n_q, max_kv=L, scale=scale)
+    qb = q.reshape(n_q, 2, D)
+    o, a = ao.attend(qb, kv, vv, scale, 2)
+    assert_close(O.cpu().double().numpy().reshape(o.shape), o, attention_tolerance(o, a, qb, kv, scale))
+    if n_q == L:
+        O2 = torch.empty_like(Q)
+        dense = [torch.from_numpy(x.reshape(L, D)).bfloat16().cuda() for x in (kv, vv)]
+        w.attn_prompt(Q, *dense, i32([0, L]), O2, head_dim=D, max_len=L, scale=scale)
+        assert_close(O2.cpu().double().numpy().reshape(o.shape), o, attention_tolerance(o, a, qb, kv, scale))
+
+
 # ---- bad indexes -----------------------------------------------------------------
 
 @pytest.mark.parametrize("n_q", [1, 40])
