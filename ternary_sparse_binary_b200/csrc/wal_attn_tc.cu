@@ -13,11 +13,12 @@
 // the CTA's pieces by itself, so the loads and the first products of a piece run
 // under the end of the one before.
 //   warps 0-3, 4-7   softmax, rescaling and output of half 0 and 1
-//   warps 8, 9       issue the MMAs of half 0 and 1
-//   warp 10          K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
+//   warp 8           issues the MMAs
+//   warp 9           K/V by TMA, boxes of whole pages or packed rows: bf16 tiles
 //                    into a ring in the 128-byte swizzle, 8-bit codes and their
 //                    scales into a ring as they lie
-//   warps 12-15      Q; for 8-bit caches warp 11 loads Q, and these turn codes to bf16 tiles, exact; scales go to a ring of
+//   warps 10, 11     Q
+//   warps 12-15      (8-bit) codes to bf16 tiles, exact; scales go to a ring of
 //                    their own and meet S and P in fp32
 // The MMAs of one thread run in order, so S_t of the next keys may overwrite
 // P_t once P_t V has been issued, and a softmax that sees its S_t finished knows
@@ -52,18 +53,19 @@ namespace {
 
 constexpr int kTile = 128;      // query rows of a tile, keys of a step
 constexpr int kScaleRing = 4;   // key tiles whose scales are held at once
-constexpr uint32_t kAheadNs = 100;
+constexpr int kQThreads = 64;   // threads that load Q
 constexpr float kLazy = 16.f;   // growth of the maximum, in log2, that O is rescaled for
 constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobody, so any number is right
 
-// Shared memory and registers.  The 512 threads are launched with 128 registers,
-// which setmaxnreg shares out again as 256 x 176 + 256 x 80.
-constexpr int kThreads = 512, kSoftRegs = 176, kOtherRegs = 80;
+// Shared memory and registers.  Launched registers are shared out again by
+// setmaxnreg: 384 threads of 168 as 256 x 208 + 128 x 88, 512 threads of 128 as
+// 256 x 176 + 256 x 80.
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool codes = TYPE != WAL_KV_BF16;
+  static constexpr int threads = codes ? 512 : 384;
+  static constexpr int soft_regs = codes ? 176 : 208, other_regs = codes ? 80 : 88;
   static constexpr uint32_t tile = kTile * D * 2;                    // a Q, K or V tile in bf16
-  static constexpr int q_threads = codes ? 32 : 128;                 // threads that load Q
   static constexpr int slots = D == 64 ? (codes ? 6 : 8) : (codes ? 3 : 5);
   static constexpr uint32_t raw = codes ? kTile * D + kTile * 4 : 0;  // a tile as it lies in the cache, and its scales
   static constexpr int raws = D == 64 ? 6 : 3;
@@ -141,17 +143,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t*
   atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
   return false;
 }
-// The same for roles that run ahead: they poll now and then, and leave the
-// barrier unit and the issue slots to the others.
-__device__ __forceinline__ bool bar_wait_ahead(uint32_t bar, uint32_t parity, int32_t* status) {
-#pragma unroll 1
-  for (uint32_t it = 0; it < kSpinLimit; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    __nanosleep(kAheadNs);
-  }
-  atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
-  return false;
-}
 // 32 bytes to a 32-byte aligned address: a whole sector, where two 16-byte
 // stores of lanes with rows of their own would send two halves.
 __device__ __forceinline__ void stg256(void* dst, const uint32_t* u) {
@@ -212,7 +203,7 @@ struct Bars {
   __device__ uint32_t join() const { return base + 456u; }                // dual: half 1's sums are there
   __device__ uint32_t o1_free() const { return base + 448u; }                   // dual: and have been joined
   __device__ uint32_t v_tail() const { return base + 384u; }
-  __device__ uint32_t drained(int t) const { return base + 464u + 8u * t; }
+  __device__ uint32_t drained() const { return base + 392u; }
   __device__ uint32_t tmem_slot() const { return base + 400u; }
 };
 
@@ -331,7 +322,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int slot = item % kSlots;
-        if (item >= kSlots) ok = bar_wait_ahead(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
+        if (item >= kSlots) ok = bar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tail = !C::codes && kv == 1 && cnt < kTile;
@@ -435,15 +426,15 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
 }
 
 // ---------------------------------------------------------------------------
-// Q tiles (one warp, or four that have no codes to widen)
+// Q tiles (two warps)
 // ---------------------------------------------------------------------------
 // 16-byte asynchronous copies, all of a tile in flight at once: a row may be any
 // (token, head), so no box fits every group.
 template <int D, int TYPE>
 __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
-  constexpr int kChunks = D / 8, kStep = C::q_threads / kChunks;  // 16-byte chunks of a row, rows between a thread's copies
-  const int tid = threadIdx.x & (C::q_threads - 1);
+  constexpr int kChunks = D / 8, kStep = kQThreads / kChunks;  // 16-byte chunks of a row, rows between a thread's copies
+  const int tid = threadIdx.x & (kQThreads - 1);               // of warps 10, 11
   const int ch = tid % kChunks, r_first = tid / kChunks;
   const int step_tok = kStep / p.group, step_head = kStep % p.group;
   uint32_t uses0 = 0, uses1 = 0;
@@ -457,7 +448,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
     for (int t = 0; t < 2; ++t) {  // both tiles' copies, then what is left to do for each
       if (!w.has_q(t)) continue;
       uint32_t& uses = t ? uses1 : uses0;
-      if (uses > 0 && !bar_wait_ahead(bars.q_empty(t), (uses - 1) & 1, p.status)) {
+      if (uses > 0 && !bar_wait(bars.q_empty(t), (uses - 1) & 1, p.status)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
@@ -505,113 +496,128 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
 }
 
 // ---------------------------------------------------------------------------
-// MMA issue (a warp for each half; the same elected lane issues everything)
+// MMA issue (one warp; the same elected lane issues everything)
 // ---------------------------------------------------------------------------
-// A wait, a vote and a commit cost this warp 50 to 200 cycles each, and a step
-// has several: one warp for both halves took longer over them than the tensor
-// core over the products.  The whole warp walks the loop: with one lane alone in
-// it the operands are not known to be uniform, and issuing an MMA took about
-// 200 cycles.
-//
-// A tile's ring slot and a Q tile are free after two commits: one of each half
-// that reads it, or both of the one.
+// The whole warp walks the loop: with one lane alone in it the operands are not
+// known to be uniform, and an MMA took about 200 cycles to issue instead of the
+// 64 that it runs.
 template <int D, int TYPE>
-__device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sched, int t, uint32_t base, uint32_t tmem, const Bars& bars) {
+__device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sched, uint32_t base, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
-  const uint32_t k_lo = desc_lo(base + C::ring_off, kDescK), v_lo = desc_lo(base + C::ring_off, kDescV);
-  const uint32_t t_s = tmem + 128u * t, t_o = tmem + 256u + (uint32_t)D * t;
-  auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
-  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.status); };
-  auto kv_wait = [&](uint32_t item) { return wait(bars.full(item % C::slots), (item / C::slots) & 1); };
-  // the functions below run in the elected lane
-  auto commit = [&](uint32_t bar, bool twice) {
-    mma_commit(bar);
-    if (twice) mma_commit(bar);
+  const uint32_t q_lo = desc_lo(base, kDescK), k_lo = desc_lo(base + C::ring_off, kDescK), v_lo = desc_lo(base + C::ring_off, kDescV);
+  // Ring position of a K or V tile.
+  struct Pos {
+    uint32_t slot, parity;
+    __device__ void next() {
+      if (++slot == C::slots) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+    __device__ void next2() {
+      next();
+      next();
+    }
   };
-  auto scores = [&](uint32_t q_lo, uint32_t item) {  // S = Q K^T
-    const uint32_t b = k_lo + (item % C::slots) * (C::tile >> 4);
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.status); };
+  auto kv_wait = [&](const Pos& at) { return bar_wait(bars.full(at.slot), at.parity, p.status); };
+  auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
+  // the functions below run in the elected lane
+  auto scores = [&](int t, int qt, uint32_t slot) {  // S_t = Q_qt K^T
+    const uint32_t a = q_lo + qt * (C::tile >> 4), b = k_lo + slot * (C::tile >> 4), d = tmem + 128u * t;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = ((k >> 2) * 16384u + (k & 3) * 32u) >> 4;
-      mma_ss(t_s, q_lo + off, b + off, id_s, k > 0);
+      mma_ss(d, a + off, b + off, id_s, k > 0);
     }
     mma_commit(bars.s_full(t));
   };
-  auto weigh = [&](int half, uint32_t item, bool more) {  // O (+)= P V over the first or last 64 keys
-    const uint32_t a = t_s + 32u * half, b = v_lo + (item % C::slots) * (C::tile >> 4) + half * (8192u >> 4);
+  auto weigh = [&](int t, int half, uint32_t slot, bool more) {  // O_t (+)= P_t V over the first or last 64 keys
+    const uint32_t a = tmem + 128u * t + 32u * half, b = v_lo + slot * (C::tile >> 4) + half * (8192u >> 4), d = tmem + 256u + (uint32_t)D * t;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_ts(t_o, a + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
+    for (int k = 0; k < 4; ++k) mma_ts(d, a + 8u * k, b + k * (2048u >> 4), id_o, more || k > 0);
   };
-  uint32_t first = 0;                   // ring item of the piece's first K tile
-  uint32_t quse0 = 0, quse1 = 0, ph = 0;  // parities: of the Q tiles' uses, of this half's weights
+  Pos pos = {0, 0};                                  // the piece's next K tile
+  uint32_t quse0 = 0, quse1 = 0, ph0 = 0, ph1 = 0;  // parities: of the Q tiles' uses, of the halves' weights
   bool ok = true;
   Walk<TYPE> walk(p, sched);
   Work w;
   AttnSeq s;
 #pragma unroll 1
   while (ok && walk.next(w, s)) {
-    const int n = w.n_t(t), qt = w.dual ? 0 : t;
-    const uint32_t q_parity = qt ? quse1 : quse0;
-    if (w.has_q(0)) quse0 ^= 1;
-    if (w.has_q(1)) quse1 ^= 1;
-    if (n > 0) {
-      const uint32_t q_lo = desc_lo(base + qt * C::tile, kDescK);
-      const int stride = w.dual ? 2 : 1, other = w.n_t(t ^ 1);  // key tiles between this half's, and of the other half
-      uint32_t ki = first + (w.dual ? 2 * t : 0);
-      ok = all(wait(bars.q_full(qt), q_parity) && kv_wait(ki));
+    if (w.n == 0) continue;
+    if (w.has_q(0)) {
+      ok = wait(bars.q_full(0), quse0);
+      quse0 ^= 1;
+    }
+    if (ok && w.has_q(1)) {
+      ok = wait(bars.q_full(1), quse1);
+      quse1 ^= 1;
+    }
+    const int ahead = w.dual ? 2 : 1;  // K tiles that S runs ahead of the weights
+    Pos v = pos;                        // V_j
+    v.next();
+    // the first scores of both halves: of one K tile, or (dual) of two
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+      if (w.n_t(t) == 0) continue;
+      ok = all(ok && kv_wait(pos));
       if (!ok) break;
       tc_fence_after();
+      const bool last = w.dual || t == 1 || w.n1 == 0;  // of the K tile's readers
       if (elect_one()) {
-        scores(q_lo, ki);
-        commit(bars.empty(ki % C::slots), w.dual || other == 0);
-        if (n == 1) commit(bars.q_empty(qt), !w.dual);
+        scores(t, w.dual ? 0 : t, pos.slot);
+        if (w.dual ? t == 1 && w.n == 2 : w.n_t(t) == 1) mma_commit(bars.q_empty(w.dual ? 0 : t));
+        if (last) mma_commit(bars.empty(pos.slot));
       }
       __syncwarp();
+      if (last) pos.next2();
+    }
 #pragma unroll 1
-      for (int k = 0; k < n; ++k) {
-        const uint32_t vi = ki + 1;
-        const bool again = k + 1 < n, v_alone = w.dual || k >= other;
-        ok = all(kv_wait(vi) && wait(bars.p_half(t), ph));
+    for (int j = 0; j < w.n && ok; ++j) {
+      const bool more_k = j + ahead < w.n;  // `pos` is there
+#pragma unroll 1
+      for (int t = w.dual ? j & 1 : 0; t < 2; ++t) {
+        if (!w.dual && j >= w.n_t(t)) continue;
+        const uint32_t ph = t ? ph1 : ph0;
+        ok = all(kv_wait(v) && wait(bars.p_half(t), ph));
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) weigh(0, vi, k > 0);
+        if (elect_one()) weigh(t, 0, v.slot, j >= ahead);
         __syncwarp();
-        // the next K tile is waited for here, before the rest of the weights --
-        // unless it may have to take the place of this V tile
-        ki += 2 * stride;
-        const bool early = again && C::slots > 2 * stride + 1;
-        ok = all((!early || kv_wait(ki)) && wait(bars.p_full(t), ph));
+        const bool again = j + ahead < (w.dual ? w.n : w.n_t(t));  // this half has another tile
+        const bool last = w.dual || t == 1 || w.n1 == 0;            // of the step's products
+        ok = all(wait(bars.p_full(t), ph));
         if (!ok) break;
-        ph ^= 1;
+        if (t) ph1 ^= 1; else ph0 ^= 1;
         tc_fence_after();
-        if (!early) {
-          if (elect_one()) {
-            weigh(1, vi, true);
-            commit(bars.empty(vi % C::slots), v_alone);
-            if (!again) mma_commit(bars.o_done(t));
-          }
-          __syncwarp();
-          if (!again) break;
-          ok = all(kv_wait(ki));
+        if (elect_one()) {
+          weigh(t, 1, v.slot, true);
+          if (last) mma_commit(bars.empty(v.slot));
+          if (!again) mma_commit(bars.o_done(t));
+        }
+        __syncwarp();
+        if (again) {  // while the tensor core weighs; in a short ring this tile takes the place of V's
+          ok = all(kv_wait(pos));
           if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {
+            scores(t, w.dual ? 0 : t, pos.slot);
+            if (j + ahead + 1 == (w.dual ? w.n : w.n_t(t))) mma_commit(bars.q_empty(w.dual ? 0 : t));
+            if (last) mma_commit(bars.empty(pos.slot));
+          }
+          __syncwarp();
         }
-        if (elect_one()) {
-          if (early) weigh(1, vi, true);
-          scores(q_lo, ki);
-          if (early) commit(bars.empty(vi % C::slots), v_alone);
-          commit(bars.empty(ki % C::slots), w.dual || k + 1 >= other);
-          if (k + 2 == n) commit(bars.q_empty(qt), !w.dual);
-        }
-        __syncwarp();
+        if (w.dual) break;
       }
+      v.next2();
+      if (more_k) pos.next2();
     }
-    first += 2 * w.n;
   }
-  if (elect_one()) mma_commit(bars.drained(t));
+  if (elect_one()) mma_commit(bars.drained());
   __syncwarp();
-  mbar_drain(bars.drained(t), 0, p.status);
+  mbar_drain(bars.drained(), 0, p.status);
 }
 
 // ---------------------------------------------------------------------------
@@ -850,7 +856,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
 }
 
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, TYPE>::threads, 1)
 attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
   using C = Cfg<D, TYPE>;
   extern __shared__ uint8_t smem_raw[];
@@ -864,7 +870,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
 #pragma unroll 1
     for (int i = 0; i < C::slots; ++i) {
       mbar_init(bars.full(i), C::codes ? 128 : 1);
-      mbar_init(bars.empty(i), 2);
+      mbar_init(bars.empty(i), 1);
     }
     if (C::codes) {
       for (int i = 0; i < C::raws; ++i) {
@@ -877,8 +883,8 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       }
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bars.q_full(t), C::q_threads);
-      mbar_init(bars.q_empty(t), 2);
+      mbar_init(bars.q_full(t), kQThreads);
+      mbar_init(bars.q_empty(t), 1);
       mbar_init(bars.s_full(t), 1);
       mbar_init(bars.p_full(t), 4);
       mbar_init(bars.p_half(t), 4);
@@ -887,8 +893,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     mbar_init(bars.join(), 4);
     mbar_init(bars.o1_free(), 4);
     mbar_init(bars.v_tail(), 1);
-    mbar_init(bars.drained(0), 1);
-    mbar_init(bars.drained(1), 1);
+    mbar_init(bars.drained(), 1);
     mbar_init_fence();
     shape[0] = shape[1] = shape[2] = 0;
   }
@@ -904,7 +909,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   {
     int tiles = 0, splits = 1, bad = 0;
 #pragma unroll 1
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+    for (int b = threadIdx.x; b < p.B; b += C::threads) {
       const AttnSeq s = attn_seq(p, b);
       bad |= s.bad;
       tiles = max(tiles, (int)(((int64_t)s.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows));
@@ -923,17 +928,17 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
     softmax_rows<D, TYPE>(p, sched, warp >> 2, sl, base, gbase, tmem, bars);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < 10) {
-      issue_mmas<D, TYPE>(p, sched, warp - 8, base, tmem, bars);
-    } else if (warp == 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
+    if (warp == 8) {
+      issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
+    } else if (warp == 9) {
       load_tiles<D, TYPE>(p, sched, &km, &vm, base, bars);
-    } else if (C::codes ? warp == 11 : warp >= 12) {
+    } else if (warp < 12) {
       load_q<D, TYPE>(p, sched, base, bars);
-    } else if (C::codes) {
+    } else {
       convert_tiles<D, TYPE>(p, sched, base, bars);
     }
   }
@@ -1001,7 +1006,7 @@ int launch_one(const AttnParams& p, cudaStream_t stream) {
   if (e == cudaSuccess) {
     const int64_t tiles = ((int64_t)p.max_q * p.group + kTcAttnRows - 1) / kTcAttnRows;
     const int64_t pieces = tiles * p.n_split * p.n_kv_heads * p.B;
-    attn_tc_kernel<D, TYPE><<<(unsigned)(pieces < kGrid ? pieces : kGrid), kThreads, Cfg<D, TYPE>::smem, stream>>>(p, km, vm);
+    attn_tc_kernel<D, TYPE><<<(unsigned)(pieces < kGrid ? pieces : kGrid), Cfg<D, TYPE>::threads, Cfg<D, TYPE>::smem, stream>>>(p, km, vm);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string("attn_tc_kernel launch: ") + cudaGetErrorString(e));
