@@ -222,8 +222,8 @@ struct Work {
 };
 
 // The pieces of a launch are (query tile pair, split of the keys, sequence, K/V
-// head), the pairs that see most keys first, so that the CTAs, which take every
-// gridDim.x-th piece, get about the same.  Each role walks its CTA's pieces by
+// head), the pairs that see most keys first.  The CTAs take one each, then one
+// each in the opposite order, and so on, so that they get about the same.  Each role walks its CTA's pieces by
 // itself; 32-bit numbers do (a launch with several splits has fewer than
 // kGrid pairs).
 struct Sched {
@@ -233,9 +233,12 @@ template <int TYPE>
 struct Walk {
   const AttnParams& p;
   const Sched sched;
-  int per, ts, r;  // (sequence, head) pairs, (tile pair, split), (sequence, head)
+  int per, ts, r;    // (sequence, head) pairs, (tile pair, split), (sequence, head)
+  int stride, back;  // pieces to the next one, and to the one after that
   __device__ __forceinline__ Walk(const AttnParams& p_, const Sched& s_) : p(p_), sched(s_) {
     per = p.B * p.n_kv_heads;
+    stride = 2 * ((int)gridDim.x - (int)blockIdx.x) - 1;
+    back = 2 * (int)blockIdx.x + 1;
     ts = (int)blockIdx.x / per;
     r = (int)blockIdx.x - ts * per;
   }
@@ -277,7 +280,10 @@ struct Walk {
     return false;
   }
   __device__ __forceinline__ void step() {
-    r += (int)gridDim.x;
+    r += stride;
+    const int s = stride;
+    stride = back;
+    back = s;
     if (r >= per) {
       const int q = r / per;
       r -= q * per;
