@@ -400,6 +400,7 @@ int check_attn(int n_heads, int n_kv_heads, int head_dim, int T, int B, int max_
   if (T < 0 || B < 1 || B > 65535 || max_q < 1 || max_kv < 1)
     return fail(WAL_ERR_SHAPE, "T >= 0, 1 <= B <= 65535 and the length bounds >= 1");
   if ((int64_t)max_q * (n_heads / n_kv_heads) > 0x7FFFFF00) return fail(WAL_ERR_UNSUPPORTED, "max_q * group must be below 2^31 - 256");
+  if (((int64_t)T * n_heads / kTcAttnRows + (int64_t)B * n_kv_heads) > 0x7FFFFFFF / 128) return fail(WAL_ERR_UNSUPPORTED, "T * n_heads and B * n_kv_heads must stay below 2^32 and 2^24");
   if (!std::isfinite(scale)) return fail(WAL_ERR_ARG, "scale must be finite");
   return WAL_OK;
 }
@@ -442,22 +443,47 @@ int launch_combine(const AttnParams& p, cudaStream_t s) {
 
 constexpr int kPlanSms = 148;  // SMs the splits are planned for: a constant, so that a workspace size holds on any device
 
-// How the keys are split.  A CTA of the decode kernel holds a quarter to a half
-// of an SM, so `slots` of them run at once; about `waves` times as many pieces
-// even out ragged lengths, and a piece has at least `least` keys.
-void plan_split(int64_t ctas, int max_kv, bool tc, int* n_split, int* split_keys) {
-  const int64_t slots = tc ? kPlanSms : 2 * kPlanSms, waves = tc ? 3 : 6;
-  const int least = tc ? 512 : 128;
-  const int64_t even = (max_kv * ctas + slots * waves - 1) / (slots * waves);
-  int64_t keys = std::max<int64_t>(least, (even + 127) / 128 * 128);
-  if (tc && ctas >= slots) keys = std::max<int64_t>(keys, max_kv);
-  *split_keys = (int)std::min<int64_t>(keys, (max_kv + 127) / 128 * 128);
-  *n_split = (max_kv + *split_keys - 1) / *split_keys;
+// How the keys are split.
+// Decode: a CTA holds a quarter to a half of an SM, so two an SM run at once;
+// about six times as many pieces even out ragged lengths, and a piece has at
+// least 128 keys.
+// Tensor-core kernel: the split with the least estimated time, in steps of 128
+// keys (about 1.8 us).  A piece costs three steps more than it has; pieces that
+// more than fill the SMs leave about 1.2 pieces' time unused at the end, the
+// more so as only bounds of the lengths are known here; a split writes and
+// reads fp32 partial results at about 5.7 TB/s, and adds a launch.  Measured,
+// without and with the split it takes: 2 x 1024 tokens over up to 16384 keys
+// 368 and 159 us; 2 x 2048 over 4096 (none) 220, with three 321 us.
+void plan_split(int64_t pieces, int64_t part_bytes, int max_kv, bool tc, int* n_split, int* split_keys) {
+  const int64_t tiles = ((int64_t)max_kv + 127) / 128;
+  int64_t best = 1;
+  if (tc) {
+    double best_cost = 0;
+    for (int64_t s = 1; s <= 128 && s <= (tiles + 1) / 2; ++s) {
+      const double r = (double)(pieces * s) / kPlanSms, steps = (double)((tiles + s - 1) / s) + 3;
+      double cost = (r <= 1 ? 1 : r + 1.2) * steps;
+      if (s > 1) cost += 3 + (double)part_bytes * s * 2 / (5.7e6 * 1.8);
+      if (s == 1 || cost < best_cost) {
+        best = s;
+        best_cost = cost;
+      }
+    }
+  } else {
+    const int64_t even = (max_kv * pieces + 12 * kPlanSms - 1) / (12 * kPlanSms);
+    best = std::max<int64_t>(1, tiles / std::max<int64_t>(1, (even + 127) / 128));
+  }
+  const int64_t keys = (tiles + best - 1) / best * 128;
+  *split_keys = (int)std::min<int64_t>(keys, 0x7FFFFF80);
+  *n_split = (int)((max_kv + keys - 1) / keys);
 }
 
-int64_t attn_ctas(int B, int n_kv_heads, int64_t rows) {
-  const int64_t per = rows <= kDecMaxRows ? 1 : (rows + kTcAttnRows - 1) / kTcAttnRows;
-  return (int64_t)B * n_kv_heads * per;
+// Pieces of a call whose keys are not split: decode, one a (sequence, K/V head);
+// else as many row tiles as T rows of B sequences can have.
+int64_t attn_pieces(int B, int n_kv_heads, int group, int T, int max_q) {
+  const int64_t rows = (int64_t)max_q * group;
+  if (rows <= kDecMaxRows) return (int64_t)B * n_kv_heads;
+  const int64_t most = B * ((rows + kTcAttnRows - 1) / kTcAttnRows);
+  return n_kv_heads * std::min<int64_t>(most, (int64_t)T * group / kTcAttnRows + B);
 }
 
 int launch_attn(const AttnParams& p, cudaStream_t stream) {
@@ -488,7 +514,7 @@ extern "C" size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int 
   if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, 1.f) != WAL_OK) return 0;
   int n_split, split_keys;
   const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
-  plan_split(attn_ctas(B, cache->n_heads, rows), max_kv, rows > kDecMaxRows, &n_split, &split_keys);
+  plan_split(attn_pieces(B, cache->n_heads, n_heads / cache->n_heads, T, std::max(1, std::min(max_q, T))), (int64_t)T * n_heads * cache->head_dim * 4, max_kv, rows > kDecMaxRows, &n_split, &split_keys);
   if (n_split == 1) return kStatusWs;
   const size_t pr = (size_t)n_split * T * n_heads;
   return kStatusWs + align_up(pr * 8, 256) + pr * cache->head_dim * 4;
@@ -513,7 +539,7 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
-  plan_split(attn_ctas(B, cache->n_heads, rows), max_kv, rows > kDecMaxRows, &p.n_split, &p.split_keys);
+  plan_split(attn_pieces(B, cache->n_heads, n_heads / cache->n_heads, T, std::max(1, std::min(max_q, T))), (int64_t)T * n_heads * cache->head_dim * 4, max_kv, rows > kDecMaxRows, &p.n_split, &p.split_keys);
   p.clear = T > 0 && p.n_split > 1;
   p.status = status_word(ws);
   if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;

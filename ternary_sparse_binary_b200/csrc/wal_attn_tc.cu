@@ -221,45 +221,84 @@ struct Work {
   __device__ int tile_of(int t, int k) const { return dual ? 2 * k + t : k; }
 };
 
-// The pieces of a launch are (query tile pair, split of the keys, sequence, K/V
-// head), the pairs that see most keys first.  The CTAs take one each, then one
-// each in the opposite order, and so on, so that they get about the same.  Each role walks its CTA's pieces by
-// itself; 32-bit numbers do (a launch with several splits has fewer than
-// kGrid pairs).
-struct Sched {
-  int tiles, splits;  // as many as the longest sequence has
-};
+// The pieces of a launch: (query tile pair, sequence, split of its keys, K/V
+// head), without those that have no rows, the tile pairs that see most keys
+// first.  The CTAs take one each, then one each in the opposite order, and so
+// on, so that they get about the same.  Each role walks its CTA's pieces by
+// itself, whole warps at a time: a lane looks at a sequence.
 template <int TYPE>
 struct Walk {
   const AttnParams& p;
-  const Sched sched;
-  int per, ts, r;    // (sequence, head) pairs, (tile pair, split), (sequence, head)
-  int stride, back;  // pieces to the next one, and to the one after that
-  __device__ __forceinline__ Walk(const AttnParams& p_, const Sched& s_) : p(p_), sched(s_) {
-    per = p.B * p.n_kv_heads;
+  int tile, at;            // tile pair, and the next piece's place among those from there on
+  int stride, back;        // pieces to the next one, and to the one after that
+  AttnSeq mine;            // this lane's sequence, and how many tile pairs and splits it has
+  int tiles, splits;
+  __device__ __forceinline__ Walk(const AttnParams& p_, int most) : p(p_), tile(most - 1), at(blockIdx.x) {
     stride = 2 * ((int)gridDim.x - (int)blockIdx.x) - 1;
     back = 2 * (int)blockIdx.x + 1;
-    ts = (int)blockIdx.x / per;
-    r = (int)blockIdx.x - ts * per;
+    look(0);
   }
-  // The next piece that has rows.
+  __device__ __forceinline__ void look(int b0) {  // at sequences b0 .. b0 + 31
+    const int b = b0 + (threadIdx.x & 31);
+    tiles = 0;
+    splits = 1;
+    if (b >= p.B) return;
+    mine = attn_seq(p, b);
+    tiles = (mine.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows;
+    if (p.n_split > 1) splits = max(1, (mine.len + p.split_keys - 1) / p.split_keys);
+  }
+  // The next piece.
   __device__ __forceinline__ bool next(Work& w, AttnSeq& s) {
 #pragma unroll 1
-    for (; ts < sched.tiles * sched.splits; step()) {
-      int tile = ts;
-      w.split = 0;
-      if (sched.splits > 1) {
-        tile = ts / sched.splits;
-        w.split = ts - tile * sched.splits;
+    while (tile >= 0) {
+      // pieces of one head in this tile pair, and the last pair with the same ones
+      int each = 0, same = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        if (p.B > 32) look(b0);
+        each += __reduce_add_sync(0xffffffffu, tiles > tile ? splits : 0);
+        same = max(same, __reduce_max_sync(0xffffffffu, tiles > tile ? 0 : tiles));
       }
-      w.b = r / p.n_kv_heads;
-      w.h = r - w.b * p.n_kv_heads;
-      s = attn_seq(p, w.b);
-      w.r0 = (sched.tiles - 1 - tile) * kTcAttnRows;
+      const int per = each * p.n_kv_heads, pairs = tile - same + 1;
+      if (at >= per * pairs) {
+        at -= per * pairs;
+        tile = same - 1;
+        continue;
+      }
+      const int down = at / per, place = at - down * per;
+      const int of = place / p.n_kv_heads;  // of `each`
+      w.h = place - of * p.n_kv_heads;
+      int before = 0, b0 = 0, mask = 0;
+#pragma unroll 1
+      for (;; b0 += 32) {  // the sequence with the of-th piece
+        if (p.B > 32) look(b0);
+        const int v = tiles > tile ? splits : 0;
+        int sum = v;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int up = __shfl_up_sync(0xffffffffu, sum, o);
+          if ((int)(threadIdx.x & 31) >= o) sum += up;
+        }
+        mask = __ballot_sync(0xffffffffu, before + sum > of);
+        if (mask) {
+          const int src = __ffs(mask) - 1;
+          w.b = b0 + src;
+          w.split = of - before - __shfl_sync(0xffffffffu, sum - v, src);
+          s.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+          s.n_q = __shfl_sync(0xffffffffu, mine.n_q, src);
+          s.len = __shfl_sync(0xffffffffu, mine.len, src);
+          s.bad = false;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      w.r0 = (tile - down) * kTcAttnRows;
+      at += stride;
+      const int other = stride;
+      stride = back;
+      back = other;
       w.rows = min(kTcAttnRows, s.n_q * p.group - w.r0);
-      if (w.rows <= 0) continue;
       w.k0 = w.split * p.split_keys;
-      if (w.split > 0 && w.k0 >= s.len) continue;  // not a split of this sequence
       w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
       w.n = w.k1 > w.k0 ? (w.k1 - w.k0 + kTile - 1) / kTile : 0;
       w.dual = w.rows <= kTile && w.n > 1;
@@ -274,21 +313,9 @@ struct Walk {
           w.n0 = end > w.k0 ? (end - w.k0 + kTile - 1) / kTile : 0;
         }
       }
-      step();
       return true;
     }
     return false;
-  }
-  __device__ __forceinline__ void step() {
-    r += stride;
-    const int s = stride;
-    stride = back;
-    back = s;
-    if (r >= per) {
-      const int q = r / per;
-      r -= q * per;
-      ts += q;
-    }
   }
 };
 
@@ -297,7 +324,7 @@ struct Walk {
 // scales for the converters
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sched, const CUtensorMap* km, const CUtensorMap* vm,
+__device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const CUtensorMap* km, const CUtensorMap* vm,
                                            uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr int kSlots = C::codes ? C::raws : C::slots;
@@ -308,7 +335,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
   auto empty = [&](int s) { return C::codes ? bars.raw_empty(s) : bars.empty(s); };
   uint32_t item = 0, tails = 0;
   bool ok = true, tail = false;
-  Walk<TYPE> walk(p, sched);
+  Walk<TYPE> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -374,11 +401,11 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, const Sched& sch
 // codes to bf16 tiles (four warps)
 // ---------------------------------------------------------------------------
 template <int D, int TYPE>
-__device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
+__device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   const int tid = threadIdx.x & 127;
   uint32_t item = 0, tiles = 0;
-  Walk<TYPE> walk(p, sched);
+  Walk<TYPE> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -393,7 +420,7 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
         bool ok = bar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
         if (ok && kv == 0 && tiles >= kScaleRing) ok = bar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
         if (ok && item >= C::slots) ok = bar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
-        if (!ok) return;
+        if (!__all_sync(0xffffffffu, ok)) return;
         const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
         // keys that are not there get codes and scales of zero
         sts32(base + C::scale_off + (uint32_t)(si * 2 + kv) * (kTile * 4) + 4u * tid,
@@ -437,14 +464,14 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, const Sched& 
 // 16-byte asynchronous copies, all of a tile in flight at once: a row may be any
 // (token, head), so no box fits every group.
 template <int D, int TYPE>
-__device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, uint32_t base, const Bars& bars) {
+__device__ __forceinline__ void load_q(const AttnParams& p, int most, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr int kChunks = D / 8, kStep = kQThreads / kChunks;  // 16-byte chunks of a row, rows between a thread's copies
   const int tid = threadIdx.x & (kQThreads - 1);               // of warps 10, 11
   const int ch = tid % kChunks, r_first = tid / kChunks;
   const int step_tok = kStep / p.group, step_head = kStep % p.group;
   uint32_t uses0 = 0, uses1 = 0;
-  Walk<TYPE> walk(p, sched);
+  Walk<TYPE> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -454,7 +481,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
     for (int t = 0; t < 2; ++t) {  // both tiles' copies, then what is left to do for each
       if (!w.has_q(t)) continue;
       uint32_t& uses = t ? uses1 : uses0;
-      if (uses > 0 && !bar_wait(bars.q_empty(t), (uses - 1) & 1, p.status)) {
+      if (!__all_sync(0xffffffffu, uses == 0 || bar_wait(bars.q_empty(t), (uses - 1) & 1, p.status))) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
@@ -508,7 +535,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, const Sched& sched, 
 // known to be uniform, and an MMA took about 200 cycles to issue instead of the
 // 64 that it runs.
 template <int D, int TYPE>
-__device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sched, uint32_t base, uint32_t tmem, const Bars& bars) {
+__device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32_t base, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
   const uint32_t q_lo = desc_lo(base, kDescK), k_lo = desc_lo(base + C::ring_off, kDescK), v_lo = desc_lo(base + C::ring_off, kDescV);
@@ -547,7 +574,7 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
   Pos pos = {0, 0};                                  // the piece's next K tile
   uint32_t quse0 = 0, quse1 = 0, ph0 = 0, ph1 = 0;  // parities: of the Q tiles' uses, of the halves' weights
   bool ok = true;
-  Walk<TYPE> walk(p, sched);
+  Walk<TYPE> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -634,7 +661,7 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, const Sched& sch
 // in every step costs the MMA warp, which runs each of its instructions once a
 // step, several times what the instructions do.
 template <int D, int TYPE>
-__device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& sched, int t, float sl, uint32_t base,
+__device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int t, float sl, uint32_t base,
                                              const uint8_t* gbase, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   const int tid = threadIdx.x & 127;
@@ -650,7 +677,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, const Sched& s
     __syncwarp();
     if (lead) mbar_arrive(bar);
   };
-  Walk<TYPE> walk(p, sched);
+  Walk<TYPE> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -870,7 +897,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
   const Bars bars = {base + C::bar_off};
-  int* shape = reinterpret_cast<int*>(gbase + C::bar_off + 404);  // most tiles, most splits of a sequence, any out of range
+  int* shape = reinterpret_cast<int*>(gbase + C::bar_off + 404);  // most tile pairs of a sequence, any out of range
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
 #pragma unroll 1
@@ -901,7 +928,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     mbar_init(bars.v_tail(), 1);
     mbar_init(bars.drained(), 1);
     mbar_init_fence();
-    shape[0] = shape[1] = shape[2] = 0;
+    shape[0] = shape[1] = 0;
   }
   if (warp == 8) {
     tmem_alloc(bars.tmem_slot(), 512);
@@ -913,39 +940,37 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   const uint32_t tmem = __shfl_sync(0xffffffffu, lds32(bars.tmem_slot()), 0);
   // how far the pieces reach, and which sequences are out of range
   {
-    int tiles = 0, splits = 1, bad = 0;
+    int tiles = 0, bad = 0;
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += C::threads) {
       const AttnSeq s = attn_seq(p, b);
       bad |= s.bad;
-      tiles = max(tiles, (int)(((int64_t)s.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows));
-      if (s.n_q > 0) splits = max(splits, (int)(((int64_t)s.len + p.split_keys - 1) / p.split_keys));
+      tiles = max(tiles, (s.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows);
     }
     atomicMax(&shape[0], tiles);
-    atomicMax(&shape[1], splits);
-    if (bad) shape[2] = 1;
+    if (bad) shape[1] = 1;
   }
   __syncthreads();
-  const Sched sched = {shape[0], shape[1]};
+  const int most = shape[0];
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (p.clear) *p.status = p.n_split == 1 && shape[2] ? (int32_t)WAL_ERR_ARG : 0;
-    else if (shape[2]) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+    if (p.clear) *p.status = p.n_split == 1 && shape[1] ? (int32_t)WAL_ERR_ARG : 0;
+    else if (shape[1]) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   }
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
-    softmax_rows<D, TYPE>(p, sched, warp >> 2, sl, base, gbase, tmem, bars);
+    softmax_rows<D, TYPE>(p, most, warp >> 2, sl, base, gbase, tmem, bars);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
     if (warp == 8) {
-      issue_mmas<D, TYPE>(p, sched, base, tmem, bars);
+      issue_mmas<D, TYPE>(p, most, base, tmem, bars);
     } else if (warp == 9) {
-      load_tiles<D, TYPE>(p, sched, &km, &vm, base, bars);
+      load_tiles<D, TYPE>(p, most, &km, &vm, base, bars);
     } else if (warp < 12) {
-      load_q<D, TYPE>(p, sched, base, bars);
+      load_q<D, TYPE>(p, most, base, bars);
     } else {
-      convert_tiles<D, TYPE>(p, sched, base, bars);
+      convert_tiles<D, TYPE>(p, most, base, bars);
     }
   }
   tc_fence_before();
