@@ -391,7 +391,8 @@ int wal_int3_embed(const wal_int3_table* t, const int32_t* ids, int M, float* ou
  * Index values are checked on the device: one that is out of range never
  * causes an access outside the caller's buffers.  It records WAL_ERR_ARG in
  * the workspace status word (wal_device_status), as wal_int3_embed does, and
- * each entry point says what happens to the rows concerned. */
+ * each entry point says what happens to the rows concerned.  A call that needs
+ * no scratch takes NULL for ws: the same happens, and nothing is recorded. */
 enum { WAL_F32 = 0, WAL_BF16 = 1 };                       /* element types of activations */
 enum { WAL_ROPE_HALF = 0, WAL_ROPE_INTERLEAVED = 1 };     /* which columns make a pair */
 enum { WAL_SCALING_NONE = 0, WAL_SCALING_LINEAR = 1, WAL_SCALING_PARTS = 2 };
@@ -462,7 +463,7 @@ int wal_kv_cache_sizes(int n_pages, int page_size, int n_heads, int head_dim, in
  * or an infinity gets codes 0 and the scale NaN: it reads back as NaN.
  * slots[t] = -1 skips the row (a padded batch); any other value outside
  * [0, n_pages * page_size) is skipped and records WAL_ERR_ARG.  Two rows of a
- * call must not name the same slot.  ws: at least 512 bytes.  Asynchronous. */
+ * call must not name the same slot.  ws: NULL, or at least 512 bytes.  Asynchronous. */
 int wal_kv_append(const wal_kv_cache* cache, const void* K, const void* V, int in_type, int T, int ldk, int ldv,
                   const int32_t* slots, const int32_t* positions, const wal_rope_plan* rope, void* ws,
                   size_t ws_bytes, wal_stream_t stream);
@@ -474,13 +475,14 @@ int wal_kv_append(const wal_kv_cache* cache, const void* K, const void* V, int i
  * ceil(max_len / page_size) <= ld_table; T is the number of rows in K and V.
  * A sequence whose start values do not increase, leave [0, T] or span more than
  * max_len tokens writes nothing, a page id outside [0, n_pages) gives zero
- * rows; both record WAL_ERR_ARG.  ws: at least 512 bytes.  Asynchronous. */
+ * rows; both record WAL_ERR_ARG.  ws: NULL, or at least 512 bytes.  Asynchronous. */
 int wal_kv_read(const wal_kv_cache* cache, const int32_t* table, int ld_table, const int32_t* start, int B,
                 int max_len, void* K, void* V, int out_type, int T, int ldk, int ldv, void* ws, size_t ws_bytes,
                 wal_stream_t stream);
 
 /* Scratch bytes of wal_attn_paged: the 256-byte header, and partial results
- * where the keys of a sequence are split over CTAs.  0 on a bad argument. */
+ * where the keys of a sequence are split over CTAs; 512 where they are not (ws
+ * may then be NULL).  0 on a bad argument. */
 size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q, int max_kv);
 
 /* Attention of new tokens over the cache that holds them already.  Rows
@@ -508,7 +510,7 @@ int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, in
  * start[b] .. start[b + 1] - 1 of Q, K, V and O (bf16) are sequence b, and its
  * token i sees its tokens 0 .. i.  Formula, types, bounds and reports as in
  * wal_attn_paged with max_len in the place of max_q.  head_dim 64 or 128.
- * ws: at least 512 bytes.  Asynchronous. */
+ * ws: NULL, or at least 512 bytes.  Asynchronous. */
 int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
                     int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B, int max_len,
                     float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes, wal_stream_t stream);

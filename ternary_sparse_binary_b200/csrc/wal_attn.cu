@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
   const AttnSeq s = attn_seq(p, b);
   if (p.clear) {
     if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
-  } else if (s.bad && h == 0 && threadIdx.x == 0) {
+  } else if (s.bad && h == 0 && threadIdx.x == 0 && p.status) {
     atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   }
   if (s.bad) return;
@@ -412,6 +412,12 @@ int check_bf16_rows(const void* X, int64_t ld, int64_t width, bool needed, const
   return WAL_OK;
 }
 
+size_t attn_ws_bytes(int n_split, int T, int n_heads, int head_dim) {
+  if (n_split == 1) return kStatusWs;
+  const size_t pr = (size_t)n_split * T * n_heads;
+  return kStatusWs + align_up(pr * 8, 256) + pr * head_dim * 4;
+}
+
 int launched(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
   return WAL_OK;
@@ -515,9 +521,7 @@ extern "C" size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int 
   int n_split, split_keys;
   const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
   plan_split(attn_pieces(B, cache->n_heads, n_heads / cache->n_heads, T, std::max(1, std::min(max_q, T))), (int64_t)T * n_heads * cache->head_dim * 4, max_kv, rows > kDecMaxRows, &n_split, &split_keys);
-  if (n_split == 1) return kStatusWs;
-  const size_t pr = (size_t)n_split * T * n_heads;
-  return kStatusWs + align_up(pr * 8, 256) + pr * cache->head_dim * 4;
+  return attn_ws_bytes(n_split, T, n_heads, cache->head_dim);
 }
 
 extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
@@ -532,14 +536,14 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   if (!q_start || !kv_len || !table || misaligned(q_start, 4) || misaligned(kv_len, 4) || misaligned(table, 4))
     return fail(WAL_ERR_ARG, "q_start, kv_len and table are required, 4-byte aligned");
   if ((int64_t)ld_table * cache->page_size < max_kv) return fail(WAL_ERR_ARG, "ld_table pages must cover max_kv tokens");
-  if (!ws || ws_bytes < wal_attn_paged_workspace_bytes(cache, n_heads, T, B, max_q, max_kv))
-    return fail(WAL_ERR_WORKSPACE, "workspace too small");
   int dev = 0;
-  if ((st = current_device(&dev))) return st;
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
   plan_split(attn_pieces(B, cache->n_heads, n_heads / cache->n_heads, T, std::max(1, std::min(max_q, T))), (int64_t)T * n_heads * cache->head_dim * 4, max_kv, rows > kDecMaxRows, &p.n_split, &p.split_keys);
+  if ((ws || p.n_split > 1) && (!ws || ws_bytes < attn_ws_bytes(p.n_split, T, n_heads, cache->head_dim)))
+    return fail(WAL_ERR_WORKSPACE, "workspace too small");
+  if ((st = current_device(&dev))) return st;
   p.clear = T > 0 && p.n_split > 1;
   p.status = status_word(ws);
   if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
@@ -571,13 +575,13 @@ extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint1
       (st = check_bf16_rows(V, ldv, kv_width, T > 0, "V")) || (st = check_bf16_rows(O, ldo, width, T > 0, "O")))
     return st;
   if (!start || misaligned(start, 4)) return fail(WAL_ERR_ARG, "start is required, 4-byte aligned");
-  if (!ws || ws_bytes < kStatusWs) return fail(WAL_ERR_WORKSPACE, "prompt attention needs a 512-byte workspace");
+  if (ws && ws_bytes < kStatusWs) return fail(WAL_ERR_WORKSPACE, "a workspace has at least 512 bytes");
   int dev = 0;
   if ((st = current_device(&dev))) return st;
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
   if (T == 0) return clear_status(ws, s, &p.status);
-  p.clear = true;
+  p.clear = ws != nullptr;
   p.status = status_word(ws);
   p.Q = Q; p.O = O;
   p.k = K; p.v = V;

@@ -23,7 +23,7 @@ struct AttnParams {
   int shift, n_pages;        // log2(page_size)
   int T, B, max_q, max_kv;
   float scale_log2;          // scale * log2(e)
-  int32_t* status;
+  int32_t* status;           // NULL: nothing is recorded
   // A call that splits its keys clears the status word in its first kernel and
   // reports index values in its second, a prompt does both in its one kernel,
   // another call after a memset.
@@ -62,7 +62,7 @@ __device__ __forceinline__ int attn_limit(const AttnSeq& s, int i) { return max(
 __device__ __forceinline__ int attn_page(const AttnParams& p, int b, int j) {
   const int page = __ldg(p.table + b * p.ld_table + (j >> p.shift));
   if ((uint32_t)page < (uint32_t)p.n_pages) return page;
-  if (!p.clear) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+  if (!p.clear && p.status) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   return 0;
 }
 // Row of key j in the cache (in units of head_dim elements).

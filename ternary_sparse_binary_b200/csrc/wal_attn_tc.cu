@@ -140,7 +140,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t*
 #pragma unroll 1
   for (uint32_t it = 0; it < kSpinLimit; ++it)
     if (mbar_try_wait(bar, parity)) return true;
-  atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
+  if (status) atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
   return false;
 }
 // 32 bytes to a 32-byte aligned address: a whole sector, where two 16-byte
@@ -952,7 +952,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   }
   __syncthreads();
   const int most = shape[0];
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) {
     if (p.clear) *p.status = p.n_split == 1 && shape[1] ? (int32_t)WAL_ERR_ARG : 0;
     else if (shape[1]) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   }

@@ -32,6 +32,7 @@ int check_cache(const wal_kv_cache* c) {
 
 int clear_status(void* ws, cudaStream_t stream, int32_t** status) {
   *status = status_word(ws);
+  if (!ws) return WAL_OK;
   const cudaError_t e = cudaMemsetAsync(*status, 0, 4, stream);
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string("status clear: ") + cudaGetErrorString(e));
   return WAL_OK;
@@ -97,24 +98,6 @@ __device__ __forceinline__ ItemCols item_cols(const Rope& r, int it) {
   return c;
 }
 
-template <int XT>
-__device__ __forceinline__ void load8(const void* row, int col, float* v) {
-  if (XT == WAL_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + col);
-    const float4 x = p[0], y = p[1];
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + col);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = dev::bf16x2_to_float2(w[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(dev::float2_to_bf16x2(v[0], v[1]), dev::float2_to_bf16x2(v[2], v[3]),
                     dev::float2_to_bf16x2(v[4], v[5]), dev::float2_to_bf16x2(v[6], v[7]));
@@ -143,26 +126,101 @@ __device__ __forceinline__ void rotate16(float (&v)[16], const Rope& r, int it, 
 // ---------------------------------------------------------------------------
 // rotate
 // ---------------------------------------------------------------------------
+// A CTA takes kTokens tokens (one where there are few: latency), and a thread
+// kBatch items at a time, whose loads are on their way while the angles are
+// computed.  16384 tokens of 40 heads of 128, half of each turned, bf16 (336 MB):
+// 70 us with one token a CTA and its loads after the angles, see the notes at the
+// launch for what it takes now.
+constexpr int kBatch = 4;
+
 template <int XT>
+struct Raw16 {  // 16 elements as they lie in memory
+  uint4 v[XT == WAL_F32 ? 4 : 2];
+};
+template <int XT>
+__device__ __forceinline__ void load16(const void* row, int a, int b, Raw16<XT>& r) {
+  const char* p = static_cast<const char*>(row);
+  constexpr int S = XT == WAL_F32 ? 4 : 2, H = S / 2;
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    r.v[i] = *reinterpret_cast<const uint4*>(p + (size_t)a * S + 16 * i);
+    r.v[H + i] = *reinterpret_cast<const uint4*>(p + (size_t)b * S + 16 * i);
+  }
+}
+template <int XT>
+__device__ __forceinline__ void unpack16(const Raw16<XT>& r, float (&v)[16]) {
+  if (XT == WAL_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 u = r.v[i < (XT == WAL_F32 ? 4 : 2) ? i : 0];
+      v[4 * i] = __uint_as_float(u.x); v[4 * i + 1] = __uint_as_float(u.y);
+      v[4 * i + 2] = __uint_as_float(u.z); v[4 * i + 3] = __uint_as_float(u.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = dev::bf16x2_to_float2(w[k]);
+        v[8 * i + 2 * k] = f.x;
+        v[8 * i + 2 * k + 1] = f.y;
+      }
+    }
+  }
+}
+// Cosines and sines of tokens t0 .. t0 + n - 1 into cs[token][pair].
+__device__ __forceinline__ void angles(const Rope& r, const int32_t* __restrict__ positions, int64_t t0, int n, float2* cs) {
+  for (int q = threadIdx.x; q < n * r.pairs; q += blockDim.x) {
+    const int t = q / r.pairs, i = q - t * r.pairs;
+    cs[t * kMaxPairs + i] = rope_angle(r, __ldg(positions + t0 + t), i);
+  }
+}
+
+template <int XT, int kTokens>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const void* X, uint16_t* Y, const int32_t* __restrict__ positions,
-                                                         Rope r, int n_heads, int items, int64_t ldx, int64_t ldy) {
-  __shared__ float2 cs[kMaxPairs];
-  const int64_t t = blockIdx.x;
-  const int pos = positions[t];
-  for (int i = threadIdx.x; i < r.pairs; i += kThreads) cs[i] = rope_angle(r, pos, i);
-  __syncthreads();
-  const void* x = static_cast<const char*>(X) + t * ldx * (XT == WAL_F32 ? 4 : 2);
-  uint16_t* y = Y + t * ldy;
-  for (int q = threadIdx.x; q < n_heads * items; q += kThreads) {
-    const int h = q / items, it = q - h * items;
-    const ItemCols c = item_cols(r, it);
-    const int col = h * items * 16;
-    float v[16];
-    load8<XT>(x, col + c.a, v);
-    load8<XT>(x, col + c.b, v + 8);
-    if (c.rot) rotate16(v, r, it, cs);
-    *reinterpret_cast<uint4*>(y + col + c.a) = pack8(v);
-    *reinterpret_cast<uint4*>(y + col + c.b) = pack8(v + 8);
+                                                         Rope r, int n_heads, int items, int64_t ldx, int64_t ldy, int T) {
+  __shared__ float2 cs[kTokens * kMaxPairs];
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int n = min(kTokens, (int)(T - t0)), per = n_heads * items, all = n * per;
+  auto place = [&](int q, int& t, int& it, int& col) {
+    t = q / per;
+    const int e = q - t * per, h = e / items;
+    it = e - h * items;
+    col = h * items * 16;
+  };
+  for (int q0 = threadIdx.x, first = 1; first || q0 - (int)threadIdx.x < all; q0 += kBatch * kThreads) {
+    Raw16<XT> raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int q = q0 + u * kThreads;
+      if (q < all) {
+        int t, it, col;
+        place(q, t, it, col);
+        const ItemCols c = item_cols(r, it);
+        load16<XT>(static_cast<const char*>(X) + (t0 + t) * ldx * (XT == WAL_F32 ? 4 : 2), col + c.a, col + c.b, raw[u]);
+      }
+    }
+    if (first) {
+      first = 0;
+      angles(r, positions, t0, n, cs);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int q = q0 + u * kThreads;
+      if (q < all) {
+        int t, it, col;
+        place(q, t, it, col);
+        const ItemCols c = item_cols(r, it);
+        float v[16];
+        unpack16<XT>(raw[u], v);
+        if (c.rot) rotate16(v, r, it, cs + t * kMaxPairs);
+        uint16_t* y = Y + (t0 + t) * ldy + col;
+        *reinterpret_cast<uint4*>(y + c.a) = pack8(v);
+        *reinterpret_cast<uint4*>(y + c.b) = pack8(v + 8);
+      }
+    }
   }
 }
 
@@ -177,85 +235,147 @@ struct AppendParams {
   const int32_t* slots;
   const int32_t* positions;
   Rope rope;
-  int n_heads, head_dim, shift;
+  int n_heads, head_dim, shift, T;
   uint32_t n_slots;
-  int32_t* status;
+  int32_t* status;  // NULL: nothing is recorded
 };
 
-// One CTA per token; a head row (head_dim / 16 items of neighbouring threads,
-// 4 or 8) is reduced by shuffles.  The division is the IEEE one, so that a
-// code is round(x / scale) and not off by one where a reciprocal's product
-// falls on the other side of a tie.
-template <int XT, int TYPE>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
-  __shared__ float2 cs[kMaxPairs];
-  const int64_t t = blockIdx.x;
-  const int slot = p.slots[t];
-  if ((uint32_t)slot >= p.n_slots) {
-    if (slot != -1 && threadIdx.x == 0) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
-    return;
+// round(x / scale) for a code, x / scale being the IEEE quotient: the product
+// with the reciprocal decides unless it lies next to a border between two codes
+// (within 2^-20 of itself, where its error is below 2^-22), where the division
+// is done.
+template <int TYPE>
+__device__ __forceinline__ uint32_t quantise(float x, float scale, float inv) {
+  float y = x * inv;
+  if (TYPE == WAL_KV_INT8) {
+    const float off = fabsf(y - rintf(y));
+    if (off > 0.5f - 128.f * 0x1p-20f) y = __fdiv_rn(x, scale);
+    return (uint32_t)__float2int_rn(y) & 0xFFu;
   }
-  if (p.rope.pairs) {
-    const int pos = p.positions[t];
-    for (int i = threadIdx.x; i < p.rope.pairs; i += kThreads) cs[i] = rope_angle(p.rope, pos, i);
-    __syncthreads();
-  }
-  const int items = p.head_dim / 16;
-  const int64_t page = slot >> p.shift;
-  const int off = slot & ((1 << p.shift) - 1);
-  const int rows = 2 * p.n_heads;
-  for (int q0 = 0; q0 < rows * items; q0 += kThreads) {
-    const int q = q0 + threadIdx.x;
-    const bool live = q < rows * items;
-    const int row = live ? q / items : 0, it = live ? q - row * items : 0;
-    const int which = row >= p.n_heads, h = row - which * p.n_heads;
-    Rope r = p.rope;
-    if (which) r.pairs = 0;
-    const ItemCols c = item_cols(r, it);
-    const void* x = static_cast<const char*>(p.x[which]) + t * p.ld[which] * (XT == WAL_F32 ? 4 : 2);
-    float v[16];
-    load8<XT>(x, h * p.head_dim + c.a, v);
-    load8<XT>(x, h * p.head_dim + c.b, v + 8);
-    if (c.rot) rotate16(v, r, it, cs);
-    const int64_t crow = (((page * p.n_heads + h) << p.shift) + off);
-    if (TYPE == WAL_KV_BF16) {
-      uint16_t* d = static_cast<uint16_t*>(p.cache[which]) + crow * p.head_dim;
-      if (live) {
-        *reinterpret_cast<uint4*>(d + c.a) = pack8(v);
-        *reinterpret_cast<uint4*>(d + c.b) = pack8(v + 8);
-      }
-      continue;
-    }
-    float amax = 0.f;
+  // borders: half way between codes, i.e. four mantissa bits and no more; below
+  // the smallest normal code they are multiples of 2^-10
+  const uint32_t low = (__float_as_uint(y) + 8u) & 0xFFFFFu;
+  if ((low - 0x80000u < 16u) || (fabsf(y) < 0x1p-6f && y != 0.f)) y = __fdiv_rn(x, scale);
+  return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+}
+
+// A CTA takes kTokens tokens; a head row (head_dim / 16 items of neighbouring
+// threads, 4 or 8) is reduced by shuffles.
+template <int XT, int TYPE, int kTokens>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ float2 cs[kTokens * kMaxPairs];
+  __shared__ int slots[kTokens];
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int n = min(kTokens, (int)(p.T - t0));
+  if (blockIdx.x == 0 && p.status) {  // the first CTA looks at every slot: no CTA has to wait for a cleared word
     bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      amax = fmaxf(amax, fabsf(v[i]));
-      bad |= !(fabsf(v[i]) <= 3.4028234663852886e38f);
+    for (int t = threadIdx.x; t < p.T; t += kThreads) {
+      const int s = __ldg(p.slots + t);
+      bad |= (uint32_t)s >= p.n_slots && s != -1;
     }
-    if (bad) amax = __int_as_float(0x7F800000);
-    for (int o = items >> 1; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    bad = isinf(amax);
-    const float scale = fmaxf(__fdiv_rn(amax, TYPE == WAL_KV_INT8 ? 127.f : 448.f), 1.1754943508222875e-38f);
-    uint32_t w[4];
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *p.status = bad ? (int32_t)WAL_ERR_ARG : 0;
+  }
+  const int items = p.head_dim / 16, per = 2 * p.n_heads * items, all = n * per;
+  struct Place {
+    int t, which, h, it;
+  };
+  auto place = [&](int q) {
+    Place x;
+    x.t = q / per;
+    const int e = q - x.t * per, row = e / items;
+    x.it = e - row * items;
+    x.which = row >= p.n_heads;
+    x.h = row - x.which * p.n_heads;
+    return x;
+  };
+  auto cols = [&](const Place& x) {
+    Rope r = p.rope;
+    if (x.which) r.pairs = 0;
+    return item_cols(r, x.it);
+  };
+  for (int q0 = threadIdx.x, first = 1; first || q0 - (int)threadIdx.x < all; q0 += kBatch * kThreads) {
+    Raw16<XT> raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = 0;
+    for (int u = 0; u < kBatch; ++u) {
+      const int q = q0 + u * kThreads;
+      const Place x = place(q < all ? q : 0);  // lanes past the end go along for the shuffles
+      const ItemCols c = cols(x);
+      load16<XT>(static_cast<const char*>(p.x[x.which]) + (t0 + x.t) * p.ld[x.which] * (XT == WAL_F32 ? 4 : 2), x.h * p.head_dim + c.a,
+                 x.h * p.head_dim + c.b, raw[u]);
+    }
+    if (first) {
+      first = 0;
+      if ((int)threadIdx.x < n) slots[threadIdx.x] = p.slots[t0 + threadIdx.x];
+      if (p.rope.pairs) angles(p.rope, p.positions, t0, n, cs);
+      __syncthreads();
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float y = bad ? 0.f : __fdiv_rn(v[4 * i + j], scale);
-        const uint32_t b = TYPE == WAL_KV_INT8 ? (uint32_t)__float2int_rn(y) & 0xFFu
-                                               : (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-        w[i] |= b << (8 * j);
+    for (int u = 0; u < kBatch; ++u) {
+      const int q = q0 + u * kThreads;
+      if (q - (int)(threadIdx.x & 31) >= all) break;  // whole warps
+      const Place x = place(q < all ? q : 0);
+      const ItemCols c = cols(x);
+      const int slot = slots[x.t];
+      const bool live = q < all && (uint32_t)slot < p.n_slots;
+      float v[16];
+      unpack16<XT>(raw[u], v);
+      if (c.rot) rotate16(v, p.rope, x.it, cs + x.t * kMaxPairs);
+      const int64_t crow = (((int64_t)(slot >> p.shift) * p.n_heads + x.h) << p.shift) + (slot & ((1 << p.shift) - 1));
+      if (TYPE == WAL_KV_BF16) {
+        uint16_t* d = static_cast<uint16_t*>(p.cache[x.which]) + crow * p.head_dim;
+        if (live) {
+          *reinterpret_cast<uint4*>(d + c.a) = pack8(v);
+          *reinterpret_cast<uint4*>(d + c.b) = pack8(v + 8);
+        }
+        continue;
+      }
+      float amax = 0.f;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        amax = fmaxf(amax, fabsf(v[i]));
+        bad |= !(fabsf(v[i]) <= 3.4028234663852886e38f);
+      }
+      if (bad) amax = __int_as_float(0x7F800000);
+      for (int o = items >> 1; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      bad = isinf(amax);
+      const float scale = fmaxf(__fdiv_rn(amax, TYPE == WAL_KV_INT8 ? 127.f : 448.f), 1.1754943508222875e-38f);
+      const float inv = __frcp_rn(scale);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i] |= (bad ? 0u : quantise<TYPE>(v[4 * i + j], scale, inv)) << (8 * j);
+      }
+      if (live) {
+        uint8_t* d = static_cast<uint8_t*>(p.cache[x.which]) + crow * p.head_dim;
+        *reinterpret_cast<uint2*>(d + c.a) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(d + c.b) = make_uint2(w[2], w[3]);
+        if (x.it == 0) p.scale[x.which][crow] = bad ? __int_as_float(0x7FC00000) : scale;
       }
     }
-    if (live) {
-      uint8_t* d = static_cast<uint8_t*>(p.cache[which]) + crow * p.head_dim;
-      *reinterpret_cast<uint2*>(d + c.a) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(d + c.b) = make_uint2(w[2], w[3]);
-      if (it == 0) p.scale[which][crow] = bad ? __int_as_float(0x7FC00000) : scale;
-    }
   }
+}
+
+// Tokens of a CTA: one while the CTAs do not fill the SMs several times.
+constexpr int kManyTokens = 4, kFewTokens = 148 * 8;
+
+template <int XT, int TYPE>
+void launch_append(const AppendParams& p, cudaStream_t s) {
+  if (p.T <= kFewTokens)
+    append_kernel<XT, TYPE, 1><<<p.T, kThreads, 0, s>>>(p);
+  else
+    append_kernel<XT, TYPE, kManyTokens><<<(p.T + kManyTokens - 1) / kManyTokens, kThreads, 0, s>>>(p);
+}
+template <int XT>
+void launch_rope(const void* X, uint16_t* Y, const int32_t* positions, const Rope& r, int n_heads, int items, int ldx, int ldy, int T,
+                 cudaStream_t s) {
+  if (T <= kFewTokens)
+    rope_kernel<XT, 1><<<T, kThreads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy, T);
+  else
+    rope_kernel<XT, kManyTokens><<<(T + kManyTokens - 1) / kManyTokens, kThreads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy, T);
 }
 
 // ---------------------------------------------------------------------------
@@ -274,59 +394,90 @@ struct ReadParams {
 };
 constexpr int kReadTokens = 16;  // tokens of one CTA: a divisor of every page size, so one page
 
+// Neighbouring threads take items of a row, then heads of a token (the output's
+// rows are contiguous over both), then tokens, then K and V; four items a thread
+// at a time, all loaded before the first is stored.
 template <int TYPE, int OT>
-__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadParams p) {
   const int b = blockIdx.y, j0 = blockIdx.x * kReadTokens;
   const int64_t s0 = p.start[b], s1 = p.start[b + 1];
   if (s0 < 0 || s1 < s0 || s1 > p.T || s1 - s0 > p.max_len) {
-    if (j0 == 0 && threadIdx.x == 0) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+    if (j0 == 0 && threadIdx.x == 0 && p.status) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
     return;
   }
   const int n = min((int)(s1 - s0) - j0, kReadTokens);
   if (n <= 0) return;
   const int page = p.table[b * p.ld_table + (j0 >> p.shift)];
   const bool bad = (uint32_t)page >= (uint32_t)p.n_pages;
-  if (bad && threadIdx.x == 0) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+  if (bad && threadIdx.x == 0 && p.status) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   const int off = j0 & ((1 << p.shift) - 1);
-  const int items = p.head_dim / 16;
-  // neighbouring threads: items of a row, then heads of a token (rows of the
-  // output are contiguous over both), then tokens, then K and V
-  const int per_token = p.n_heads * items;
-  for (int q = threadIdx.x; q < 2 * n * per_token; q += kThreads) {
-    const int which = q >= n * per_token, r = q - which * n * per_token;
-    const int j = r / per_token, e = r - j * per_token;
-    const int h = e / items, it = e - h * items;
-    if (!p.out[which]) continue;
-    const int64_t crow = ((((int64_t)(bad ? 0 : page) * p.n_heads + h) << p.shift) + off + j);
-    const int64_t dst = (s0 + j0 + j) * p.ld[which] + h * p.head_dim + 16 * it;
-    float v[16];
-    if (TYPE == WAL_KV_BF16) {
-      const uint16_t* s = static_cast<const uint16_t*>(p.cache[which]) + crow * p.head_dim + 16 * it;
-      load8<WAL_BF16>(s, 0, v);
-      load8<WAL_BF16>(s, 8, v + 8);
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.cache[which]) + crow * p.head_dim + 16 * it);
-      const float sc = p.scale[which][crow];
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  const int items = p.head_dim / 16, per = p.n_heads * items, all = 2 * n * per;
+  const int64_t row0 = (((int64_t)(bad ? 0 : page) * p.n_heads) << p.shift) + off;  // head 0, token j0
+  struct Place {
+    int which, j, h, it;
+  };
+  auto place = [&](int q) {
+    Place x;
+    x.which = q >= n * per;
+    const int r = q - x.which * n * per;
+    x.j = r / per;
+    const int e = r - x.j * per;
+    x.h = e / items;
+    x.it = e - x.h * items;
+    return x;
+  };
+  for (int q0 = threadIdx.x; q0 < all; q0 += kBatch * kThreads) {
+    uint4 raw[kBatch][TYPE == WAL_KV_BF16 ? 2 : 1];
+    float sc[kBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[4];
-        dev::codes4_to_float<TYPE>(ww[i], f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[4 * i + k] = f[k] * sc;
+    for (int u = 0; u < kBatch; ++u) {
+      const Place x = place(min(q0 + u * kThreads, all - 1));
+      const int64_t crow = row0 + ((int64_t)x.h << p.shift) + x.j;
+      const char* cache = static_cast<const char*>(x.which ? p.cache[1] : p.cache[0]);
+      if (TYPE == WAL_KV_BF16) {
+        const uint4* src = reinterpret_cast<const uint4*>(cache + (crow * p.head_dim + 16 * x.it) * 2);
+        raw[u][0] = src[0];
+        raw[u][TYPE == WAL_KV_BF16 ? 1 : 0] = src[1];
+      } else {
+        raw[u][0] = *reinterpret_cast<const uint4*>(cache + crow * p.head_dim + 16 * x.it);
+        sc[u] = (x.which ? p.scale[1] : p.scale[0])[crow];
       }
     }
-    if (bad)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (OT == WAL_BF16) {
-      uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[which]) + dst);
-      d[0] = pack8(v);
-      d[1] = pack8(v + 8);
-    } else {
-      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out[which]) + dst);
+    for (int u = 0; u < kBatch; ++u) {
+      if (q0 + u * kThreads >= all) break;
+      const Place x = place(q0 + u * kThreads);
+      char* out = static_cast<char*>(x.which ? p.out[1] : p.out[0]);
+      if (!out) continue;
+      const int64_t dst = (s0 + j0 + x.j) * (x.which ? p.ld[1] : p.ld[0]) + x.h * p.head_dim + 16 * x.it;
+      float v[16];
+      if (TYPE == WAL_KV_BF16) {
+        Raw16<WAL_BF16> r;
+        r.v[0] = raw[u][0];
+        r.v[1] = raw[u][TYPE == WAL_KV_BF16 ? 1 : 0];
+        unpack16<WAL_BF16>(r, v);
+      } else {
+        const uint32_t w[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          float f[4];
+          dev::codes4_to_float<TYPE>(w[i], f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[4 * i + k] = f[k] * sc[u];
+        }
+      }
+      if (bad)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+      if (OT == WAL_BF16) {
+        uint4* d = reinterpret_cast<uint4*>(out + dst * 2);
+        d[0] = pack8(v);
+        d[1] = pack8(v + 8);
+      } else {
+        float4* d = reinterpret_cast<float4*>(out + dst * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
     }
   }
 }
@@ -390,9 +541,9 @@ extern "C" int wal_rope(const wal_rope_plan* rope, const void* X, int x_type, in
   const int items = rope->head_dim / 16;
   cudaStream_t s = (cudaStream_t)stream;
   if (x_type == WAL_F32)
-    rope_kernel<WAL_F32><<<T, kThreads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy);
+    launch_rope<WAL_F32>(X, Y, positions, r, n_heads, items, ldx, ldy, T, s);
   else
-    rope_kernel<WAL_BF16><<<T, kThreads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy);
+    launch_rope<WAL_BF16>(X, Y, positions, r, n_heads, items, ldx, ldy, T, s);
   return launched("rope_kernel");
 }
 
@@ -425,13 +576,14 @@ extern "C" int wal_kv_append(const wal_kv_cache* cache, const void* K, const voi
   if (misaligned(slots, 4) || misaligned(positions, 4)) return fail(WAL_ERR_ARG, "slots and positions must be 4-byte aligned");
   if (T > 0 && (!K || !V || !slots)) return fail(WAL_ERR_ARG, "K, V and slots are required");
   if (T > 0 && rope && !positions) return fail(WAL_ERR_ARG, "positions are required with a rope plan");
-  if (!ws || ws_bytes < kStatusWs) return fail(WAL_ERR_WORKSPACE, "the append needs a 512-byte workspace");
+  if (ws && ws_bytes < kStatusWs) return fail(WAL_ERR_WORKSPACE, "a workspace has at least 512 bytes");
   int dev = 0;
   if ((st = current_device(&dev))) return st;
   AppendParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
-  if ((st = clear_status(ws, s, &p.status))) return st;
-  if (T == 0) return WAL_OK;
+  if (T == 0) return clear_status(ws, s, &p.status);
+  p.status = status_word(ws);
+  p.T = T;
   p.x[0] = K; p.x[1] = V;
   p.ld[0] = ldk; p.ld[1] = ldv;
   p.cache[0] = cache->k; p.cache[1] = cache->v;
@@ -445,9 +597,9 @@ extern "C" int wal_kv_append(const wal_kv_cache* cache, const void* K, const voi
   p.n_slots = (uint32_t)(cache->n_pages * cache->page_size);
   const bool f = in_type == WAL_F32;
   switch (cache->type) {
-    case WAL_KV_BF16: f ? append_kernel<WAL_F32, WAL_KV_BF16><<<T, kThreads, 0, s>>>(p) : append_kernel<WAL_BF16, WAL_KV_BF16><<<T, kThreads, 0, s>>>(p); break;
-    case WAL_KV_INT8: f ? append_kernel<WAL_F32, WAL_KV_INT8><<<T, kThreads, 0, s>>>(p) : append_kernel<WAL_BF16, WAL_KV_INT8><<<T, kThreads, 0, s>>>(p); break;
-    default: f ? append_kernel<WAL_F32, WAL_KV_E4M3><<<T, kThreads, 0, s>>>(p) : append_kernel<WAL_BF16, WAL_KV_E4M3><<<T, kThreads, 0, s>>>(p); break;
+    case WAL_KV_BF16: f ? launch_append<WAL_F32, WAL_KV_BF16>(p, s) : launch_append<WAL_BF16, WAL_KV_BF16>(p, s); break;
+    case WAL_KV_INT8: f ? launch_append<WAL_F32, WAL_KV_INT8>(p, s) : launch_append<WAL_BF16, WAL_KV_INT8>(p, s); break;
+    default: f ? launch_append<WAL_F32, WAL_KV_E4M3>(p, s) : launch_append<WAL_BF16, WAL_KV_E4M3>(p, s); break;
   }
   return launched("append_kernel");
 }
@@ -464,7 +616,7 @@ extern "C" int wal_kv_read(const wal_kv_cache* cache, const int32_t* table, int 
   if (!table || !start || misaligned(table, 4) || misaligned(start, 4))
     return fail(WAL_ERR_ARG, "table and start are required, 4-byte aligned");
   if ((int64_t)ld_table * cache->page_size < max_len) return fail(WAL_ERR_ARG, "ld_table pages must cover max_len tokens");
-  if (!ws || ws_bytes < kStatusWs) return fail(WAL_ERR_WORKSPACE, "the read needs a 512-byte workspace");
+  if (ws && ws_bytes < kStatusWs) return fail(WAL_ERR_WORKSPACE, "a workspace has at least 512 bytes");
   int dev = 0;
   if ((st = current_device(&dev))) return st;
   ReadParams p = {};

@@ -14,8 +14,8 @@ namespace wal {
 constexpr size_t kStatusWs = 512;  // workspace that only holds the 256-byte aligned status word
 
 int check_cache(const wal_kv_cache* c);
-inline int32_t* status_word(void* ws) { return reinterpret_cast<int32_t*>(align_up((uintptr_t)ws, 256)); }
-// The status word of a workspace, cleared on `stream`.
+inline int32_t* status_word(void* ws) { return !ws ? nullptr : reinterpret_cast<int32_t*>(align_up((uintptr_t)ws, 256)); }
+// The status word of a workspace, cleared on `stream`; NULL without one.
 int clear_status(void* ws, cudaStream_t stream, int32_t** status);
 
 inline int log2_of(int v) {

@@ -66,7 +66,7 @@ APPEND = dict(cache=cache(), K=P, V=P, in_type=0, T=3, ldk=128, ldv=128, slots=P
     (dict(rope=rope(head_dim=128)), wal.WAL_ERR_SHAPE), (dict(in_type=5), wal.WAL_ERR_ARG), (dict(T=-1), wal.WAL_ERR_SHAPE),
     (dict(ldk=124), wal.WAL_ERR_ARG), (dict(ldv=129), wal.WAL_ERR_ARG), (dict(in_type=1, ldk=132), wal.WAL_ERR_ARG),
     (dict(K=None), wal.WAL_ERR_ARG), (dict(V=P + 1), wal.WAL_ERR_ARG), (dict(slots=None), wal.WAL_ERR_ARG),
-    (dict(positions=None), wal.WAL_ERR_ARG), (dict(ws=None), wal.WAL_ERR_WORKSPACE), (dict(ws_bytes=511), wal.WAL_ERR_WORKSPACE)])
+    (dict(positions=None), wal.WAL_ERR_ARG), (dict(ws_bytes=511), wal.WAL_ERR_WORKSPACE)])
 def test_append_refuses(kw, status):
     refuses(status, wal.wal_kv_append, *args(APPEND, kw))
 
@@ -94,8 +94,8 @@ PAGED = dict(cache=cache(), Q=P, n_heads=4, T=6, ldq=256, q_start=P, kv_len=P, t
     (dict(max_q=0), wal.WAL_ERR_SHAPE), (dict(max_kv=0), wal.WAL_ERR_SHAPE), (dict(ld_table=3), wal.WAL_ERR_ARG),
     (dict(ldq=248), wal.WAL_ERR_ARG), (dict(ldo=260), wal.WAL_ERR_ARG), (dict(Q=None), wal.WAL_ERR_ARG), (dict(O=P + 8), wal.WAL_ERR_ARG),
     (dict(q_start=None), wal.WAL_ERR_ARG), (dict(kv_len=P + 2), wal.WAL_ERR_ARG), (dict(table=None), wal.WAL_ERR_ARG),
-    (dict(scale=math.inf), wal.WAL_ERR_ARG), (dict(scale=math.nan), wal.WAL_ERR_ARG), (dict(ws=None), wal.WAL_ERR_WORKSPACE),
-    (dict(ws_bytes=256), wal.WAL_ERR_WORKSPACE)])
+    (dict(scale=math.inf), wal.WAL_ERR_ARG), (dict(scale=math.nan), wal.WAL_ERR_ARG), (dict(ws=None, max_kv=20000, ld_table=2000), wal.WAL_ERR_WORKSPACE),
+    (dict(ws_bytes=256), wal.WAL_ERR_WORKSPACE), (dict(ws_bytes=4096, max_kv=20000, ld_table=2000), wal.WAL_ERR_WORKSPACE)])
 def test_paged_refuses(kw, status):
     refuses(status, wal.wal_attn_paged, *args(PAGED, kw))
 
