@@ -437,8 +437,8 @@ int wal_rope(const wal_rope_plan* rope, const void* X, int x_type, int T, int n_
  *   k, v               [n_pages][n_heads][page_size][head_dim] of `type`;
  *   k_scale, v_scale   fp32 [n_pages][n_heads][page_size], NULL for bf16.
  * A value is its code, times the scale of its (slot, head) row in the 8-bit
- * types: int8 codes in [-127, 127], or e4m3 codes (finite ones; the two NaN
- * codes are never written and not read as NaN).  Buffers are 16-byte aligned.
+ * types: int8 codes in [-127, 127], or e4m3 codes (the two NaN codes are never
+ * written; what they read as is not specified), and finite scales.  Buffers are 16-byte aligned.
  * head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; n_pages * page_size
  * below 2^31.  K and V are the caller's; slots nobody wrote may hold anything,
  * and no entry point reads past a sequence's length. */

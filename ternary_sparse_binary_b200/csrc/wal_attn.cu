@@ -54,39 +54,60 @@ __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s
 //    undone when O is written;
 //  - P: an 8 x 8 transpose (movmatrix) turns S^T's accumulator layout into the
 //    B operand's.
-// 8-bit codes are exact in bf16 and go to the tensor cores unscaled: the score
-// gets the key's K scale, the weight its V scale, both in fp32.  Weights are
-// rounded to bf16 for the second product (the operand type; 2^-8 of a weight,
-// averaged over the keys); m, l, scores and O stay fp32.
+// 8-bit codes go to the tensor cores unscaled, as fp16 (exact, and half the
+// instructions of bf16); the score gets the key's K scale in fp32.  Q is then
+// fp16 too, each row brought to [1, 2) by a power of two: nothing is lost down to
+// 2^-14 of the row's largest, and 2^-25 of it below.  V's scale belongs to the
+// weight, and a small one must not cost an fp16 weight its digits: O has a
+// reference of its own, m2 = max(score + log2 |V scale|), so that its weights are
+// at most about 1 where they count.  bf16 caches stay bf16 (m2 = m).  Weights are
+// rounded for the second product (2^-8 or 2^-11 of a weight, averaged over the
+// keys); references, l, scores and O are fp32.
+// References are lazy: they follow the maximum when it has grown by more than
+// 2^4, which a vote finds; most steps have no reduction and leave O alone.
 constexpr int kDecWarps = 4;
 constexpr int kDecMaxRows = 16;
 
+template <bool HALF>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-      "%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if (HALF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-
-// The loads of one key row by one lane: D / 4 elements of K, the lane's part.
-template <int D, int TYPE>
-struct RowWords {
-  static constexpr int n = TYPE == WAL_KV_BF16 ? D / 8 : D / 16;  // 32-bit words of K (and of V) a lane holds per key
-};
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kDecLazy = 4.f;
 
 template <int D, int TYPE, int NT, int MT>
-__global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int KB = TYPE == WAL_KV_BF16 ? 2 : 1;       // bytes of a code
-  constexpr int W = RowWords<D, TYPE>::n;               // words of K per lane and key
-  constexpr int NW = D * KB / 32;                       // words of V per lane and key (of 8 lanes)
-  constexpr int DT = D / 16;                            // fragments along d
+__global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1 ? 3 : 2) attn_decode_kernel(const __grid_constant__ AttnParams p) {
+  constexpr bool CODES = TYPE != WAL_KV_BF16;
+  constexpr int KB = CODES ? 1 : 2;      // bytes of a code
+  constexpr int W = D * KB / 16;         // 32-bit words of K per lane and key (of 4 lanes)
+  constexpr int NW = D * KB / 32;        // words of V per lane and key (of 8 lanes)
+  constexpr int DT = D / 16;             // fragments along d
   constexpr int STEP = 16 * MT;
   __shared__ float s_o[kDecWarps][8 * NT][D + 4];
   __shared__ float2 s_ml[kDecWarps][8 * NT];
@@ -104,81 +125,41 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
   const int k0 = split * p.split_keys, k1 = min(s.len, k0 + p.split_keys);
   if (rows == 0 || (k0 >= k1 && split > 0)) return;  // split 0 also answers for a sequence without keys
 
-  // Q fragments: row g of tile t, the columns in the order of the K loads
-  uint32_t q[NT][DT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = 8 * t + g;
-    const bool live = r < rows;
-    const uint16_t* src = p.Q + (s.q0 + (live ? r / p.group : 0)) * p.ldq + (h * p.group + (live ? r % p.group : 0)) * D;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {  // 16 bytes of Q: two fragments along d
-      const int piece = TYPE == WAL_KV_BF16 ? 32 * i + 8 * c : 64 * (i >> 1) + 16 * c + 8 * (i & 1);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (live) v = __ldg(reinterpret_cast<const uint4*>(src + piece));
-      q[t][2 * i][0] = v.x;
-      q[t][2 * i][1] = v.y;
-      q[t][2 * i + 1][0] = v.z;
-      q[t][2 * i + 1][1] = v.w;
-    }
-  }
-  // this lane's columns of S^T: rows 8 t + 2 c + {0, 1}
-  int lim[NT][2];
-  float m[NT][2], l[NT][2];
-  int lim_min = s.len;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * t + 2 * c + e;
-      lim[t][e] = r < rows ? attn_limit(s, r / p.group) : s.len;
-      m[t][e] = -INFINITY;
-      l[t][e] = 0.f;
-    }
-  lim_min = attn_limit(s, 0);
-  float o[DT][NT][4];
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
-
-  const uint8_t* kbase = static_cast<const uint8_t*>(p.k);
-  const uint8_t* vbase = static_cast<const uint8_t*>(p.v);
-  for (int j0 = k0 + warp * STEP; j0 < k1; j0 += kDecWarps * STEP) {
-    // rows of the 16-key tiles: a tile lies in one page
-    int64_t row[MT];
+  // K and V of a step, and where they lie: a tile of 16 keys is in one page
+  uint32_t kw[MT][2][W], vw[MT][4][NW];
+  float ks[MT][2], vs[MT][2];
+  int64_t row[MT];
+  auto find = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < MT; ++u) row[u] = j0 + 16 * u < k1 ? attn_page_row(p, b, h, j0 + 16 * u) : 0;
-    uint32_t kw[MT][2][W], vw[MT][4][NW];
-    float ks[MT][2], vs[MT][2];
+  };
+  auto load_k = [&](int j0) {
+    const uint8_t* base = static_cast<const uint8_t*>(p.k);
 #pragma unroll
-    for (int u = 0; u < MT; ++u) {
+    for (int u = 0; u < MT; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = 16 * u + g + 8 * e;
-        const bool live = j0 + j < k1;
-        const uint8_t* src = kbase + (row[u] + g + 8 * e) * (D * KB) + 16 * c;
+        const int j = g + 8 * e;
+        const bool live = j0 + 16 * u + j < k1;
+        const uint8_t* src = base + (row[u] + j) * (D * KB) + 16 * c;
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (live) v = __ldg(reinterpret_cast<const uint4*>(src + 64 * i));
           kw[u][e][4 * i] = v.x; kw[u][e][4 * i + 1] = v.y; kw[u][e][4 * i + 2] = v.z; kw[u][e][4 * i + 3] = v.w;
         }
-        if (TYPE != WAL_KV_BF16) {
-          ks[u][e] = live ? __ldg(p.ks + row[u] + g + 8 * e) : 0.f;
-          vs[u][e] = live ? __ldg(p.vs + row[u] + g + 8 * e) : 0.f;
-        }
+        if (CODES) ks[u][e] = live ? __ldg(p.ks + row[u] + j) : 0.f;
       }
-    }
+  };
+  auto load_v = [&](int j0) {
+    const uint8_t* base = static_cast<const uint8_t*>(p.v);
 #pragma unroll
-    for (int u = 0; u < MT; ++u)
+    for (int u = 0; u < MT; ++u) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int jj = 2 * c + (e & 1) + 8 * (e >> 1);
-        const bool live = j0 + 16 * u + jj < k1;
-        const uint8_t* src = vbase + (row[u] + jj) * (D * KB);
+        const int j = 2 * c + (e & 1) + 8 * (e >> 1);
+        const bool live = j0 + 16 * u + j < k1;
+        const uint8_t* src = base + (row[u] + j) * (D * KB);
         if (NW >= 4) {
 #pragma unroll
           for (int i = 0; i < NW / 4; ++i) {
@@ -192,7 +173,76 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
           vw[u][e][0] = v.x; vw[u][e][1] = v.y;
         }
       }
+      if (CODES)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) vs[u][e] = j0 + 16 * u + g + 8 * e < k1 ? __ldg(p.vs + row[u] + g + 8 * e) : 0.f;
+    }
+  };
+  int j0 = k0 + warp * STEP;
+  find(j0);
+  load_k(j0);
+  load_v(j0);
 
+  // Q fragments: row g of tile t, the columns in the order of the K loads
+  uint32_t q[NT][DT][2];
+  float mult[NT][2];  // of the scores of this lane's columns of S^T: rows 8 t + 2 c + {0, 1}
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = 8 * t + g;
+    const bool live = r < rows;
+    const uint16_t* src = p.Q + (s.q0 + (live ? r / p.group : 0)) * p.ldq + (h * p.group + (live ? r % p.group : 0)) * D;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {  // 16 bytes of Q: two fragments along d
+      const int piece = CODES ? 64 * (i >> 1) + 16 * c + 8 * (i & 1) : 32 * i + 8 * c;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = __ldg(reinterpret_cast<const uint4*>(src + piece));
+      q[t][2 * i][0] = v.x;
+      q[t][2 * i][1] = v.y;
+      q[t][2 * i + 1][0] = v.z;
+      q[t][2 * i + 1][1] = v.w;
+      top = max(max(max(top, v.x & 0x7FFFu), (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+      top = max(max(max(top, v.z & 0x7FFFu), (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu));
+    }
+    mult[t][0] = mult[t][1] = p.scale_log2;
+    if (CODES) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t e = min(max(top >> 7, 1u), 253u);  // biased exponent of the row's largest
+      const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23) * p.scale_log2;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 f = dev::bf16x2_to_float2(q[t][i][k]);
+          q[t][i][k] = dev::float2_to_half2(f.x * down, f.y * down);
+        }
+      mult[t][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+      mult[t][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+    }
+  }
+  int lim[NT][2];
+  float m[NT][2], m2[NT][2], l[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * t + 2 * c + e;
+      lim[t][e] = r < rows ? attn_limit(s, r / p.group) : s.len;
+      m[t][e] = m2[t][e] = -INFINITY;
+      l[t][e] = 0.f;
+    }
+  const int lim_min = min(k1, attn_limit(s, 0));
+  float o[DT][NT][4];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
+
+#pragma unroll 1
+  for (; j0 < k1; j0 += kDecWarps * STEP) {
     // S^T = K Q^T
     float sc[MT][NT][4];
 #pragma unroll
@@ -204,28 +254,33 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         uint32_t a[4];
-        if (TYPE == WAL_KV_BF16) {
-          a[0] = kw[u][0][2 * d]; a[1] = kw[u][1][2 * d]; a[2] = kw[u][0][2 * d + 1]; a[3] = kw[u][1][2 * d + 1];
+        if (CODES) {
+          dev::codes4_to_half<TYPE>(kw[u][0][d], a[0], a[2]);
+          dev::codes4_to_half<TYPE>(kw[u][1][d], a[1], a[3]);
         } else {
-          dev::codes4_to_bf16<TYPE>(kw[u][0][d], a[0], a[2]);
-          dev::codes4_to_bf16<TYPE>(kw[u][1][d], a[1], a[3]);
+          a[0] = kw[u][0][2 * d]; a[1] = kw[u][1][2 * d]; a[2] = kw[u][0][2 * d + 1]; a[3] = kw[u][1][2 * d + 1];
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(sc[u][t], a[0], a[1], a[2], a[3], q[t][d][0], q[t][d][1]);
+        for (int t = 0; t < NT; ++t) mma16816<CODES>(sc[u][t], a[0], a[1], a[2], a[3], q[t][d][0], q[t][d][1]);
       }
     }
-    // scores in log2 units; keys a row does not see get -inf
+    // scores in log2 units, and (codes) what V's scale adds to them
+    float lv[MT][2];
 #pragma unroll
     for (int u = 0; u < MT; ++u)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int r = 0; r < 2; ++r) {
+        lv[u][r] = CODES ? lg2(fabsf(vs[u][r])) : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[u][t][e] * p.scale_log2;
-          if (TYPE != WAL_KV_BF16) x *= ks[u][e >> 1];
-          sc[u][t][e] = x;
-        }
-    if (j0 + STEP > lim_min || j0 + STEP > k1) {
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = sc[u][t][e + 2 * r];
+            x *= mult[t][e];
+            if (CODES) x *= ks[u][r];
+          }
+      }
+    if (j0 + STEP > lim_min) {  // keys a row does not see get -inf
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
@@ -236,68 +291,115 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
             if (j >= min(k1, lim[t][e & 1])) sc[u][t][e] = -INFINITY;
           }
     }
+    // the next step's K, in the registers of this one's
+    const int jn = j0 + kDecWarps * STEP;
+    find(jn);
+    load_k(jn);
+
+    float mx[NT][2], mx2[NT][2];
+    bool grow = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float corr[2];
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = m[t][e];
-#pragma unroll
-        for (int u = 0; u < MT; ++u) mx = fmaxf(mx, fmaxf(sc[u][t][e], sc[u][t][e + 2]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        corr[e] = exp2f(m[t][e] - ref);
-        m[t][e] = mx;
-        l[t][e] *= corr[e];
+        mx[t][e] = sc[0][t][e];
+        mx2[t][e] = sc[0][t][e] + lv[0][0];
 #pragma unroll
         for (int u = 0; u < MT; ++u)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float w = exp2f(sc[u][t][e + 2 * r] - ref);
+            mx[t][e] = fmaxf(mx[t][e], sc[u][t][e + 2 * r]);
+            if (CODES) mx2[t][e] = fmaxf(mx2[t][e], sc[u][t][e + 2 * r] + lv[u][r]);
+          }
+        grow |= mx[t][e] > m[t][e] + kDecLazy || (CODES && mx2[t][e] > m2[t][e] + kDecLazy);
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float corr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          auto join = [&](float x, float old) {
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            return fmaxf(fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)), old);
+          };
+          const float n = join(mx[t][e], m[t][e]);
+          const float f = m[t][e] == -INFINITY ? 0.f : ex2(m[t][e] - n);
+          m[t][e] = n;
+          l[t][e] *= f;
+          corr[e] = f;
+          if (CODES) {
+            const float n2 = join(mx2[t][e], m2[t][e]);
+            corr[e] = m2[t][e] == -INFINITY ? 0.f : ex2(m2[t][e] - n2);
+            m2[t][e] = n2;
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][t][e] *= corr[e & 1];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[t][e] == -INFINITY ? 0.f : m[t][e], ref2 = m2[t][e] == -INFINITY ? 0.f : m2[t][e];
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float& x = sc[u][t][e + 2 * r];
+            const float w = ex2(x - ref);
             l[t][e] += w;
-            sc[u][t][e + 2 * r] = TYPE == WAL_KV_BF16 ? w : w * vs[u][r];
+            x = CODES ? copysignf(ex2(x + lv[u][r] - ref2), vs[u][r]) : w;
           }
       }
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[d][t][e] *= corr[e & 1];
-    }
     // O^T += V^T P^T
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
       uint32_t pb[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        pb[t][0] = transpose8x8(dev::float2_to_bf16x2(sc[u][t][0], sc[u][t][1]));
-        pb[t][1] = transpose8x8(dev::float2_to_bf16x2(sc[u][t][2], sc[u][t][3]));
+        pb[t][0] = transpose8x8(CODES ? dev::float2_to_half2(sc[u][t][0], sc[u][t][1]) : dev::float2_to_bf16x2(sc[u][t][0], sc[u][t][1]));
+        pb[t][1] = transpose8x8(CODES ? dev::float2_to_half2(sc[u][t][2], sc[u][t][3]) : dev::float2_to_bf16x2(sc[u][t][2], sc[u][t][3]));
       }
-      if (TYPE == WAL_KV_BF16) {
+      if (!CODES) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {  // word d: columns 64 (d / 4) + 8 g + 2 (d % 4) + {0, 1}
           const uint32_t a0 = __byte_perm(vw[u][0][d], vw[u][1][d], 0x5410), a1 = __byte_perm(vw[u][0][d], vw[u][1][d], 0x7632);
           const uint32_t a2 = __byte_perm(vw[u][2][d], vw[u][3][d], 0x5410), a3 = __byte_perm(vw[u][2][d], vw[u][3][d], 0x7632);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816(o[d][t], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+          for (int t = 0; t < NT; ++t) mma16816<CODES>(o[d][t], a0, a1, a2, a3, pb[t][0], pb[t][1]);
         }
       } else {
 #pragma unroll
         for (int d = 0; d < DT; d += 2) {  // word d / 2: columns (D / 8) g + 2 d + {0 .. 3}
           uint32_t a[2][4];
           const uint32_t w0 = vw[u][0][d / 2], w1 = vw[u][1][d / 2], w2 = vw[u][2][d / 2], w3 = vw[u][3][d / 2];
-          dev::codes4_to_bf16<TYPE>(__byte_perm(w0, w1, 0x5140), a[0][0], a[0][1]);
-          dev::codes4_to_bf16<TYPE>(__byte_perm(w0, w1, 0x7362), a[1][0], a[1][1]);
-          dev::codes4_to_bf16<TYPE>(__byte_perm(w2, w3, 0x5140), a[0][2], a[0][3]);
-          dev::codes4_to_bf16<TYPE>(__byte_perm(w2, w3, 0x7362), a[1][2], a[1][3]);
+          dev::codes4_to_half<TYPE>(__byte_perm(w0, w1, 0x5140), a[0][0], a[0][1]);
+          dev::codes4_to_half<TYPE>(__byte_perm(w0, w1, 0x7362), a[1][0], a[1][1]);
+          dev::codes4_to_half<TYPE>(__byte_perm(w2, w3, 0x5140), a[0][2], a[0][3]);
+          dev::codes4_to_half<TYPE>(__byte_perm(w2, w3, 0x7362), a[1][2], a[1][3]);
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(o[d + x][t], a[x][0], a[x][1], a[x][2], a[x][3], pb[t][0], pb[t][1]);
+            for (int t = 0; t < NT; ++t) mma16816<CODES>(o[d + x][t], a[x][0], a[x][1], a[x][2], a[x][3], pb[t][0], pb[t][1]);
         }
       }
     }
+    load_v(jn);
+  }
+  if (CODES) {  // O in units of m, as l is
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = m2[t][e & 1] == -INFINITY ? 0.f : ex2(m2[t][e & 1] - m[t][e & 1]);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d][t][e] *= f;
+      }
   }
 
   // join the warps: each leaves its rows, then a warp takes a row
@@ -353,13 +455,17 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
   }
 }
 
-// Add the splits of a row in order, one warp a row, and report index values out
-// of range.
-template <int D>
+// Add the splits of a row, and report index values out of range.  PER warps of
+// the CTA share a row, each its splits in order, joined in order: one where
+// there are few splits, four where a warp alone would wait for one load after
+// the other.
+template <int D, int PER>
 __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __grid_constant__ AttnParams p) {
   constexpr int VPL = D / 32;
+  __shared__ float s_o[PER > 1 ? kRowWarps : 1][D];
+  __shared__ float s_l[PER > 1 ? kRowWarps : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.z, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnSeq s = attn_seq(p, b);
   if (blockIdx.x == 0) {  // the first kernel cleared the status word; what it skipped is reported here
     bool bad = s.bad;
@@ -367,8 +473,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
     for (int i = threadIdx.x; i < pages; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + b * p.ld_table + i) >= (uint32_t)p.n_pages;
     if (bad) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   }
-  const int row = blockIdx.x * kRowWarps + (threadIdx.x >> 5);  // (token, head)
-  if (s.bad || row >= s.n_q * p.n_heads) return;
+  const int row = blockIdx.x * (kRowWarps / PER) + warp / PER;  // (token, head)
+  if (s.bad || row >= s.n_q * p.n_heads) return;                // PER > 1: the whole CTA
   const int tok = row / p.n_heads, head = row - tok * p.n_heads;
   const int n = max(1, (s.len + p.split_keys - 1) / p.split_keys);
   const int64_t pr = attn_part_row(p, s, tok, head), stride = (int64_t)p.T * p.n_heads;
@@ -380,14 +486,34 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
   float acc[VPL], ll = 0.f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
-  for (int i = 0; i < n; ++i) {
+#pragma unroll 4
+  for (int i = warp % PER; i < n; i += PER) {
     const float2 ml = p.part_ml[pr + i * stride];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a split in which the row sees nothing
-    const float f = exp2f(ml.x - ref);
-    ll += f * ml.y;
     const float* src = p.part_o + (pr + i * stride) * D + lane * VPL;
+    float v[VPL];
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) acc[k] += f * src[k];
+    for (int k = 0; k < VPL; ++k) v[k] = src[k];
+    const bool none = ml.x == -INFINITY && ml.y == 0.f;  // the row sees nothing of this split
+    const float f = exp2f(ml.x - ref);
+    ll += none ? 0.f : f * ml.y;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) acc[k] += none ? 0.f : f * v[k];
+  }
+  if (PER > 1) {
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) s_o[warp][lane * VPL + k] = acc[k];
+    if (lane == 0) s_l[warp] = ll;
+    __syncthreads();
+    if (warp > 0) return;
+    ll = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) acc[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      ll += s_l[i];
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) acc[k] += s_o[i][lane * VPL + k];
+    }
   }
   finish_row<D>(p, s, b, head, tok, acc, ll);
 }
@@ -423,18 +549,24 @@ int launched(cudaError_t e, const char* what) {
   return WAL_OK;
 }
 
+// Tiles of 16 keys a step: bf16 takes one, its K and V being twice as wide, and
+// fits three CTAs on an SM (25 sequences, 16384 keys: 133 us against 136 with two
+// tiles and two CTAs); codes take two and fit two CTAs (int8, 32768 keys: 181 us,
+// 189 squeezed into three, 203 with one tile).
 template <int D, int TYPE>
 void launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
-  constexpr int MT2 = TYPE == WAL_KV_BF16 ? 1 : 2;  // sixteen rows: half the keys a step, to stay in registers
+  constexpr int MT = TYPE == WAL_KV_BF16 ? 1 : 2;
   if (p.max_q * p.group <= 8)
-    attn_decode_kernel<D, TYPE, 1, 2><<<grid, 32 * kDecWarps, 0, s>>>(p);
+    attn_decode_kernel<D, TYPE, 1, MT><<<grid, 32 * kDecWarps, 0, s>>>(p);
   else
-    attn_decode_kernel<D, TYPE, 2, MT2><<<grid, 32 * kDecWarps, 0, s>>>(p);
+    attn_decode_kernel<D, TYPE, 2, MT><<<grid, 32 * kDecWarps, 0, s>>>(p);
 }
 
 int launch_combine(const AttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)p.max_q * p.n_heads + kRowWarps - 1) / kRowWarps), 1, (unsigned)p.B);
+  const bool shared = p.n_split > 6;
+  const int rows = shared ? 1 : kRowWarps;  // of a CTA
+  cfg.gridDim = dim3((unsigned)(((int64_t)p.max_q * p.n_heads + rows - 1) / rows), 1, (unsigned)p.B);
   cfg.blockDim = dim3(32 * kRowWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -442,11 +574,15 @@ int launch_combine(const AttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64>, p)
-                                         : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128>, p);
+  cudaError_t e;
+  if (p.head_dim == 64)
+    e = shared ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4>, p) : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 1>, p);
+  else
+    e = shared ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4>, p) : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 1>, p);
   return launched(e, "attn_combine_kernel");
 }
 
+constexpr int kDecPieces = 12;
 constexpr int kPlanSms = 148;  // SMs the splits are planned for: a constant, so that a workspace size holds on any device
 
 // How the keys are split.
@@ -475,7 +611,7 @@ void plan_split(int64_t pieces, int64_t part_bytes, int max_kv, bool tc, int* n_
       }
     }
   } else {
-    const int64_t even = (max_kv * pieces + 12 * kPlanSms - 1) / (12 * kPlanSms);
+    const int64_t even = (max_kv * pieces + kDecPieces * kPlanSms - 1) / (kDecPieces * kPlanSms);
     best = std::max<int64_t>(1, tiles / std::max<int64_t>(1, (even + 127) / 128));
   }
   const int64_t keys = (tiles + best - 1) / best * 128;

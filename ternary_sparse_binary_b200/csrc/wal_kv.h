@@ -30,6 +30,11 @@ namespace dev {
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
+__device__ __forceinline__ uint32_t float2_to_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t float2_to_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -66,6 +71,20 @@ __device__ __forceinline__ void codes4_to_bf16(uint32_t w, uint32_t& lo, uint32_
     const uint32_t e = 0x7B807B80u;  // 2^120 as a bf16 pair
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"((t0 & 0x80008000u) | ((t0 >> 4) & 0x07F007F0u)), "r"(e));
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"((t1 & 0x80008000u) | ((t1 >> 4) & 0x07F007F0u)), "r"(e));
+  }
+}
+// And as fp16 pairs, in half the instructions: int8 as the low byte of 0x64xx
+// reads 1024 + (code + 128), e4m3 has a conversion of its own.
+template <int TYPE>
+__device__ __forceinline__ void codes4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (TYPE == WAL_KV_INT8) {
+    const uint32_t u = w ^ 0x80808080u, off = 0x64806480u;  // 1152
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(off));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(off));
+  } else {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 
