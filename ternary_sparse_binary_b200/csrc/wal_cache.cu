@@ -126,11 +126,9 @@ __device__ __forceinline__ void rotate16(float (&v)[16], const Rope& r, int it, 
 // ---------------------------------------------------------------------------
 // rotate
 // ---------------------------------------------------------------------------
-// A CTA takes kTokens tokens (one where there are few: latency), and a thread
-// kBatch items at a time, whose loads are on their way while the angles are
-// computed.  16384 tokens of 40 heads of 128, half of each turned, bf16 (336 MB):
-// 70 us with one token a CTA and its loads after the angles, see the notes at the
-// launch for what it takes now.
+// A CTA takes kTokens tokens (one where there are few: latency).  A thread has
+// the same item of each of them, so that its place is worked out once, and loads
+// all of them before the angles are computed.
 constexpr int kBatch = 4;
 
 template <int XT>
@@ -182,45 +180,32 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const void* X, uint16_t*
                                                          Rope r, int n_heads, int items, int64_t ldx, int64_t ldy, int T) {
   __shared__ float2 cs[kTokens * kMaxPairs];
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-  const int n = min(kTokens, (int)(T - t0)), per = n_heads * items, all = n * per;
-  auto place = [&](int q, int& t, int& it, int& col) {
-    t = q / per;
-    const int e = q - t * per, h = e / items;
-    it = e - h * items;
-    col = h * items * 16;
-  };
-  for (int q0 = threadIdx.x, first = 1; first || q0 - (int)threadIdx.x < all; q0 += kBatch * kThreads) {
-    Raw16<XT> raw[kBatch];
+  const int n = min(kTokens, (int)(T - t0)), per = n_heads * items;
+  bool first = true;
+  for (int q = threadIdx.x; first || q - (int)threadIdx.x < per; q += blockDim.x) {
+    const int h = q / items, it = q - h * items, col = h * items * 16;
+    const ItemCols c = item_cols(r, it);
+    Raw16<XT> raw[kTokens];
+    if (q < per)
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int q = q0 + u * kThreads;
-      if (q < all) {
-        int t, it, col;
-        place(q, t, it, col);
-        const ItemCols c = item_cols(r, it);
-        load16<XT>(static_cast<const char*>(X) + (t0 + t) * ldx * (XT == WAL_F32 ? 4 : 2), col + c.a, col + c.b, raw[u]);
-      }
-    }
+      for (int t = 0; t < kTokens; ++t)
+        if (t < n) load16<XT>(static_cast<const char*>(X) + (t0 + t) * ldx * (XT == WAL_F32 ? 4 : 2), col + c.a, col + c.b, raw[t]);
     if (first) {
-      first = 0;
+      first = false;
       angles(r, positions, t0, n, cs);
       __syncthreads();
     }
+    if (q < per)
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int q = q0 + u * kThreads;
-      if (q < all) {
-        int t, it, col;
-        place(q, t, it, col);
-        const ItemCols c = item_cols(r, it);
-        float v[16];
-        unpack16<XT>(raw[u], v);
-        if (c.rot) rotate16(v, r, it, cs + t * kMaxPairs);
-        uint16_t* y = Y + (t0 + t) * ldy + col;
-        *reinterpret_cast<uint4*>(y + c.a) = pack8(v);
-        *reinterpret_cast<uint4*>(y + c.b) = pack8(v + 8);
-      }
-    }
+      for (int t = 0; t < kTokens; ++t)
+        if (t < n) {
+          float v[16];
+          unpack16<XT>(raw[t], v);
+          if (c.rot) rotate16(v, r, it, cs + t * kMaxPairs);
+          uint16_t* y = Y + (t0 + t) * ldy + col;
+          *reinterpret_cast<uint4*>(y + c.a) = pack8(v);
+          *reinterpret_cast<uint4*>(y + c.b) = pack8(v + 8);
+        }
   }
 }
 
@@ -240,23 +225,21 @@ struct AppendParams {
   int32_t* status;  // NULL: nothing is recorded
 };
 
-// round(x / scale) for a code, x / scale being the IEEE quotient: the product
-// with the reciprocal decides unless it lies next to a border between two codes
-// (within 2^-20 of itself, where its error is below 2^-22), where the division
-// is done.
+// Whether y = x * (1 / scale) lies so near to a border between two codes that
+// x / scale, which decides, may lie on its other side.  y is within 2^-22 of the
+// quotient (relative); the margins are several times that.
 template <int TYPE>
-__device__ __forceinline__ uint32_t quantise(float x, float scale, float inv) {
-  float y = x * inv;
-  if (TYPE == WAL_KV_INT8) {
-    const float off = fabsf(y - rintf(y));
-    if (off > 0.5f - 128.f * 0x1p-20f) y = __fdiv_rn(x, scale);
-    return (uint32_t)__float2int_rn(y) & 0xFFu;
-  }
-  // borders: half way between codes, i.e. four mantissa bits and no more; below
-  // the smallest normal code they are multiples of 2^-10
-  const uint32_t low = (__float_as_uint(y) + 8u) & 0xFFFFFu;
-  if ((low - 0x80000u < 16u) || (fabsf(y) < 0x1p-6f && y != 0.f)) y = __fdiv_rn(x, scale);
-  return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ bool near_border(float y) {
+  if (TYPE == WAL_KV_INT8) return fabsf(y - rintf(y)) > 0.5f - 0x1p-13f;
+  // half way between codes: the fourth mantissa bit and no more; below the
+  // smallest normal code the borders lie elsewhere
+  return ((__float_as_uint(y) + 8u) & 0xFFFFFu) - 0x80000u < 16u || (fabsf(y) < 0x1p-6f && y != 0.f);
+}
+// Codes of a and b as bytes 0 and 1.
+template <int TYPE>
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+  if (TYPE == WAL_KV_INT8) return ((uint32_t)__float2int_rn(a) & 0xFFu) | (((uint32_t)__float2int_rn(b) & 0xFFu) << 8);
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // A CTA takes kTokens tokens; a head row (head_dim / 16 items of neighbouring
@@ -264,118 +247,124 @@ __device__ __forceinline__ uint32_t quantise(float x, float scale, float inv) {
 template <int XT, int TYPE, int kTokens>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ float2 cs[kTokens * kMaxPairs];
-  __shared__ int slots[kTokens];
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
   const int n = min(kTokens, (int)(p.T - t0));
   if (blockIdx.x == 0 && p.status) {  // the first CTA looks at every slot: no CTA has to wait for a cleared word
     bool bad = false;
-    for (int t = threadIdx.x; t < p.T; t += kThreads) {
+    for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
       const int s = __ldg(p.slots + t);
       bad |= (uint32_t)s >= p.n_slots && s != -1;
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *p.status = bad ? (int32_t)WAL_ERR_ARG : 0;
   }
-  const int items = p.head_dim / 16, per = 2 * p.n_heads * items, all = n * per;
-  struct Place {
-    int t, which, h, it;
-  };
-  auto place = [&](int q) {
-    Place x;
-    x.t = q / per;
-    const int e = q - x.t * per, row = e / items;
-    x.it = e - row * items;
-    x.which = row >= p.n_heads;
-    x.h = row - x.which * p.n_heads;
-    return x;
-  };
-  auto cols = [&](const Place& x) {
+  int slots[kTokens];
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) slots[t] = t < n ? __ldg(p.slots + t0 + t) : -1;
+  const int items = p.head_dim / 16, shift = items == 8 ? 3 : 2, rows = 2 * p.n_heads, per = rows << shift;
+  bool first = true;
+  for (int q = threadIdx.x; first || q - (int)threadIdx.x < per; q += blockDim.x) {
+    // whole warps go along for the shuffles
+    const int row = min(q >> shift, rows - 1), it = q & (items - 1), which = row >= p.n_heads, h = row - (which ? p.n_heads : 0);
     Rope r = p.rope;
-    if (x.which) r.pairs = 0;
-    return item_cols(r, x.it);
-  };
-  for (int q0 = threadIdx.x, first = 1; first || q0 - (int)threadIdx.x < all; q0 += kBatch * kThreads) {
-    Raw16<XT> raw[kBatch];
+    if (which) r.pairs = 0;
+    const ItemCols c = item_cols(r, it);
+    const char* x = static_cast<const char*>(which ? p.x[1] : p.x[0]);
+    const int64_t ld = which ? p.ld[1] : p.ld[0];
+    Raw16<XT> raw[kTokens];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int q = q0 + u * kThreads;
-      const Place x = place(q < all ? q : 0);  // lanes past the end go along for the shuffles
-      const ItemCols c = cols(x);
-      load16<XT>(static_cast<const char*>(p.x[x.which]) + (t0 + x.t) * p.ld[x.which] * (XT == WAL_F32 ? 4 : 2), x.h * p.head_dim + c.a,
-                 x.h * p.head_dim + c.b, raw[u]);
-    }
+    for (int t = 0; t < kTokens; ++t)
+      load16<XT>(x + (t0 + min(t, n - 1)) * ld * (XT == WAL_F32 ? 4 : 2), h * p.head_dim + c.a, h * p.head_dim + c.b, raw[t]);
     if (first) {
-      first = 0;
-      if ((int)threadIdx.x < n) slots[threadIdx.x] = p.slots[t0 + threadIdx.x];
-      if (p.rope.pairs) angles(p.rope, p.positions, t0, n, cs);
-      __syncthreads();
+      first = false;
+      if (p.rope.pairs) {
+        angles(p.rope, p.positions, t0, n, cs);
+        __syncthreads();
+      }
     }
+    char* cache = static_cast<char*>(which ? p.cache[1] : p.cache[0]);
+    float* scales = which ? p.scale[1] : p.scale[0];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int q = q0 + u * kThreads;
-      if (q - (int)(threadIdx.x & 31) >= all) break;  // whole warps
-      const Place x = place(q < all ? q : 0);
-      const ItemCols c = cols(x);
-      const int slot = slots[x.t];
-      const bool live = q < all && (uint32_t)slot < p.n_slots;
+    for (int t = 0; t < kTokens; ++t) {
+      const int slot = slots[t];
+      const bool live = q < per && (uint32_t)slot < p.n_slots;
       float v[16];
-      unpack16<XT>(raw[u], v);
-      if (c.rot) rotate16(v, p.rope, x.it, cs + x.t * kMaxPairs);
-      const int64_t crow = (((int64_t)(slot >> p.shift) * p.n_heads + x.h) << p.shift) + (slot & ((1 << p.shift) - 1));
+      unpack16<XT>(raw[t], v);
+      if (c.rot) rotate16(v, r, it, cs + t * kMaxPairs);
+      const int64_t crow = (((int64_t)(slot >> p.shift) * p.n_heads + h) << p.shift) + (slot & ((1 << p.shift) - 1));
       if (TYPE == WAL_KV_BF16) {
-        uint16_t* d = static_cast<uint16_t*>(p.cache[x.which]) + crow * p.head_dim;
+        uint16_t* d = reinterpret_cast<uint16_t*>(cache) + crow * p.head_dim;
         if (live) {
           *reinterpret_cast<uint4*>(d + c.a) = pack8(v);
           *reinterpret_cast<uint4*>(d + c.b) = pack8(v + 8);
         }
         continue;
       }
-      float amax = 0.f;
-      bool bad = false;
+      // the largest magnitude as bits: infinities and NaN come out on top
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      for (int o = items >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool bad = top >= 0x7F800000u;
+      const float scale = fmaxf(__fdiv_rn(__uint_as_float(bad ? 0u : top), TYPE == WAL_KV_INT8 ? 127.f : 448.f), 1.1754943508222875e-38f);
+      const float inv = __frcp_rn(scale);
+      bool border = false;
+      float y[16];
+      uint32_t low = ~0u, least = ~0u;  // e4m3: the nearest to half way, and the smallest
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        amax = fmaxf(amax, fabsf(v[i]));
-        bad |= !(fabsf(v[i]) <= 3.4028234663852886e38f);
+        y[i] = v[i] * inv;
+        if (TYPE == WAL_KV_INT8) {
+          border |= near_border<TYPE>(y[i]);
+        } else {
+          low = min(low, (__float_as_uint(y[i]) + 8u - 0x80000u) & 0xFFFFFu);
+          least = min(least, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+        }
       }
-      if (bad) amax = __int_as_float(0x7F800000);
-      for (int o = items >> 1; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      bad = isinf(amax);
-      const float scale = fmaxf(__fdiv_rn(amax, TYPE == WAL_KV_INT8 ? 127.f : 448.f), 1.1754943508222875e-38f);
-      const float inv = __frcp_rn(scale);
+      if (border || low < 16u || least < 0x3C800000u)  // a code is round(x / scale), the quotient being the IEEE one
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (near_border<TYPE>(y[i])) y[i] = __fdiv_rn(v[i], scale);
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[i] |= (bad ? 0u : quantise<TYPE>(v[4 * i + j], scale, inv)) << (8 * j);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = codes2<TYPE>(y[4 * i], y[4 * i + 1]) | (codes2<TYPE>(y[4 * i + 2], y[4 * i + 3]) << 16);
+      if (bad) w[0] = w[1] = w[2] = w[3] = 0;
       if (live) {
-        uint8_t* d = static_cast<uint8_t*>(p.cache[x.which]) + crow * p.head_dim;
+        uint8_t* d = reinterpret_cast<uint8_t*>(cache) + crow * p.head_dim;
         *reinterpret_cast<uint2*>(d + c.a) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2*>(d + c.b) = make_uint2(w[2], w[3]);
-        if (x.it == 0) p.scale[x.which][crow] = bad ? __int_as_float(0x7FC00000) : scale;
+        if (it == 0) scales[crow] = bad ? __int_as_float(0x7FC00000) : scale;
       }
     }
   }
 }
 
-// Tokens of a CTA: one while the CTAs do not fill the SMs several times.
-constexpr int kManyTokens = 4, kFewTokens = 148 * 8;
+// Tokens of a CTA: one while the CTAs do not fill the SMs several times.  Two
+// beat four and eight: 16381 tokens of 8 heads of 128 to e4m3 48, 62 and 82 us.
+constexpr int kManyTokens = 2, kFewTokens = 148 * 8;
+
+// Threads of a CTA that has `items` of them a token: whole warps, in equal rounds.
+int threads_for(int items) {
+  const int rounds = (items + kThreads - 1) / kThreads, each = (items + rounds - 1) / rounds;
+  return (each + 31) / 32 * 32;
+}
 
 template <int XT, int TYPE>
 void launch_append(const AppendParams& p, cudaStream_t s) {
+  const int threads = threads_for(2 * p.n_heads * (p.head_dim / 16));
   if (p.T <= kFewTokens)
-    append_kernel<XT, TYPE, 1><<<p.T, kThreads, 0, s>>>(p);
+    append_kernel<XT, TYPE, 1><<<p.T, threads, 0, s>>>(p);
   else
-    append_kernel<XT, TYPE, kManyTokens><<<(p.T + kManyTokens - 1) / kManyTokens, kThreads, 0, s>>>(p);
+    append_kernel<XT, TYPE, kManyTokens><<<(p.T + kManyTokens - 1) / kManyTokens, threads, 0, s>>>(p);
 }
 template <int XT>
 void launch_rope(const void* X, uint16_t* Y, const int32_t* positions, const Rope& r, int n_heads, int items, int ldx, int ldy, int T,
                  cudaStream_t s) {
+  const int threads = threads_for(n_heads * items);
   if (T <= kFewTokens)
-    rope_kernel<XT, 1><<<T, kThreads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy, T);
+    rope_kernel<XT, 1><<<T, threads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy, T);
   else
-    rope_kernel<XT, kManyTokens><<<(T + kManyTokens - 1) / kManyTokens, kThreads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy, T);
+    rope_kernel<XT, kManyTokens><<<(T + kManyTokens - 1) / kManyTokens, threads, 0, s>>>(X, Y, positions, r, n_heads, items, ldx, ldy, T);
 }
 
 // ---------------------------------------------------------------------------
