@@ -691,7 +691,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
     for (int k = 0; k < n; ++k, ++steps) {
       const int kb = w.k0 + kTile * w.tile_of(t, k);
       const uint32_t ti = tiles + w.tile_of(t, k);
-      const float* sc = reinterpret_cast<const float*>(gbase + C::scale_off) + (ti % kScaleRing) * 2 * kTile;
+      const uint32_t sc = base + C::scale_off + (ti % kScaleRing) * (2 * kTile * 4);  // K's scales of the tile, then V's
       if (!wait(bars.s_full(t), steps & 1)) return;
       if (C::codes && !wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1)) return;
       tc_fence_after();
@@ -706,10 +706,12 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       auto prepare = [&](float* v, int q, int n) {
         if (C::codes) {
 #pragma unroll
-          for (int e = 0; e < n; e += 2) {
-            const float2 y = mul2(make_float2(v[e], v[e + 1]), *reinterpret_cast<const float2*>(sc + q + e));
-            v[e] = y.x;
-            v[e + 1] = y.y;
+          for (int e = 0; e < n; e += 4) {
+            const uint4 k4 = lds128(sc + 4u * (q + e));
+            const float2 y = mul2(make_float2(v[e], v[e + 1]), make_float2(__uint_as_float(k4.x), __uint_as_float(k4.y)));
+            const float2 z = mul2(make_float2(v[e + 2], v[e + 3]), make_float2(__uint_as_float(k4.z), __uint_as_float(k4.w)));
+            v[e] = y.x; v[e + 1] = y.y;
+            v[e + 2] = z.x; v[e + 3] = z.y;
           }
         }
         if (masked) {
@@ -722,13 +724,18 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       float2 sum[2];
       auto weights = [&](int q, const float* v, float ref, uint32_t(&pk)[16]) {
         const float2 ref2 = make_float2(ref, ref);
+        uint4 v4;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 y = fma2(make_float2(v[2 * e], v[2 * e + 1]), sl2, ref2);
           y.x = ex2(y.x);
           y.y = ex2(y.y);
           sum[e & 1] = add2(sum[e & 1], y);
-          if (C::codes) y = mul2(y, *reinterpret_cast<const float2*>(sc + kTile + 32 * q + 2 * e));
+          if (C::codes) {
+            if (!(e & 1)) v4 = lds128(sc + kTile * 4 + 4u * (32 * q + 2 * e));
+            y = mul2(y, (e & 1) ? make_float2(__uint_as_float(v4.z), __uint_as_float(v4.w))
+                                : make_float2(__uint_as_float(v4.x), __uint_as_float(v4.y)));
+          }
           pk[e] = dev::float2_to_bf16x2(y.x, y.y);
         }
       };
@@ -762,9 +769,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       const float ref = m == -INFINITY ? 0.f : -m;
       sum[0] = sum[1] = make_float2(0.f, 0.f);
       uint32_t pa[16], pb[16];
-      // The weights go over scores that have been read.  With codes there are
-      // not the registers to keep 128 of them: they are read again.
-      if (!C::codes) {
+      {
         weights(0, x, ref, pa);
         tmem_st16(t_s, pa);
         weights(1, x + 32, ref, pb);
@@ -777,21 +782,6 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
         tmem_st16(t_s + 48u, pb);
         tmem_st_wait();
         arrive(bars.p_full(t));
-      } else {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          float v[64];
-          tmem_ld32(t_s + 64u * half, v);
-          tmem_ld32(t_s + 64u * half + 32u, v + 32);
-          tmem_ld_wait();
-          prepare(v, 64 * half, 64);
-          weights(2 * half, v, ref, pa);
-          tmem_st16(t_s + 32u * half, pa);
-          weights(2 * half + 1, v + 32, ref, pb);
-          tmem_st16(t_s + 32u * half + 16u, pb);
-          tmem_st_wait();
-          arrive(half ? bars.p_full(t) : bars.p_half(t));
-        }
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
