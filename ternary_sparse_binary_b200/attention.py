@@ -28,14 +28,15 @@ _HERE = contextlib.nullcontext()
 
 def _rows(x, what, dtypes=_X_TYPES):
     """(type, row stride, rows, columns) of an activation tensor."""
-    shape = x.shape
-    if len(shape) != 2 or x.dtype not in dtypes:
+    kind = dtypes.get(x.dtype)
+    if kind is None or x.dim() != 2:
         raise ValueError(f"{what}: a 2-D tensor of {' or '.join(str(d) for d in dtypes)}")
+    rows, cols = x.shape
     ld, one = x.stride()
-    if one != 1 and shape[1] > 1:
+    if one != 1 and cols > 1:
         raise ValueError(f"{what}: the last stride must be 1")
     # a one-row (or empty) tensor's row stride is arbitrary; its width serves
-    return dtypes[x.dtype], (ld if shape[0] > 1 else shape[1]), shape[0], shape[1]
+    return kind, (ld if rows > 1 else cols), rows, cols
 
 
 def _index(x, what, n=None):
@@ -116,6 +117,7 @@ class KvCache:
         self.k, self.v = k, v
         self.k_scale, self.v_scale = scales if scales else (None, None)
         self.n_pages, self.n_heads, self.page_size, self.head_dim = k.shape
+        self._scratch = {}  # workspace sizes of recent shapes
         self.desc = wal_kv_cache(self.n_pages, self.page_size, self.n_heads, self.head_dim, _KV_TYPES[k.dtype],
                                  k.data_ptr(), v.data_ptr(), *[s.data_ptr() for s in scales])
 
@@ -168,7 +170,13 @@ class KvCache:
                              v_out.data_ptr(), kt, T, ldk, ldv, wp, wn, s)
 
     def attend_workspace_bytes(self, n_heads, T, B, max_q, max_kv):
-        return _abi.wal_attn_paged_workspace_bytes(self.desc, n_heads, T, B, max_q, max_kv)
+        shape = (n_heads, T, B, max_q, max_kv)
+        n = self._scratch.get(shape)
+        if n is None:
+            if len(self._scratch) >= 256:
+                self._scratch.clear()
+            n = self._scratch[shape] = _abi.wal_attn_paged_workspace_bytes(self.desc, n_heads, T, B, max_q, max_kv)
+        return n
 
     def attend(self, q, q_start, kv_len, table, out, max_q, max_kv, scale=None, ws=None, stream=None):
         """out (bf16) = attention of the new tokens' q (bf16) [tokens, n_heads * head_dim] over the cache;
@@ -183,7 +191,7 @@ class KvCache:
         if ws is None:
             n = self.attend_workspace_bytes(n_heads, T, B, max_q, max_kv)  # 0: the call below says what is wrong
             if n > 512:
-                with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                with _HERE if stream is None else torch.cuda.stream(stream):
                     ws = torch.empty(n, dtype=torch.uint8, device=q.device)
         wp, wn = _ws(ws)
         with guard:
