@@ -61,16 +61,18 @@ def _enter(stream, *tensors):
     return guard, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
-def _ws(ws):
+def _ws(ws, like):
     if ws is None:
         return None, 0
-    if ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError("ws: a contiguous uint8 tensor")
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != like.get_device():
+        raise ValueError("ws: a contiguous uint8 tensor on the device of the others")
     return ws.data_ptr(), ws.numel()
 
 
 def status(ws, stream=None):
     """Raise WalError if the last call that was given this workspace recorded one (synchronises the stream)."""
+    if _ws(ws, ws)[1] < 512:
+        raise ValueError("ws: at least 512 bytes")
     guard, s = _enter(stream, ws)
     with guard:
         _abi.wal_device_status(ws.data_ptr(), s)
@@ -147,7 +149,7 @@ class KvCache:
             guard, s = _enter(stream, self.k, k, v, slots, positions, rope.freq)
         else:
             guard, s = _enter(stream, self.k, k, v, slots)
-        wp, wn = _ws(ws)
+        wp, wn = _ws(ws, k)
         with guard:
             _abi.wal_kv_append(self.desc, k.data_ptr(), v.data_ptr(), kt, T, ldk, ldv, _index(slots, "slots", T),
                                None if rope is None else _index(positions, "positions", T),
@@ -161,10 +163,10 @@ class KvCache:
         if vt != kt or shape != [T, width] or width != self.n_heads * self.head_dim:
             raise ValueError("k_out and v_out: [rows, heads * head_dim] of one type")
         tp, ldt = _table(table, B)
-        if T == 0:
+        if T == 0 and ws is None:
             return
         guard, s = _enter(stream, self.k, table, start, k_out, v_out)
-        wp, wn = _ws(ws)
+        wp, wn = _ws(ws, k_out)
         with guard:
             _abi.wal_kv_read(self.desc, tp, ldt, _index(start, "start"), B, max_len, k_out.data_ptr(),
                              v_out.data_ptr(), kt, T, ldk, ldv, wp, wn, s)
@@ -193,7 +195,7 @@ class KvCache:
             if n > 512:
                 with _HERE if stream is None else torch.cuda.stream(stream):
                     ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-        wp, wn = _ws(ws)
+        wp, wn = _ws(ws, q)
         with guard:
             _abi.wal_attn_paged(self.desc, q.data_ptr(), n_heads, T, ldq, _index(q_start, "q_start", B + 1),
                                 _index(kv_len, "kv_len"), tp, ldt, B, max_q, max_kv,
@@ -210,7 +212,7 @@ def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, str
     if shape != [T, width] or k_shape != v_shape or k_shape[0] != T or width % head_dim or k_shape[1] % head_dim:
         raise ValueError("q and out: [tokens, n_heads * head_dim]; k and v: [tokens, n_kv_heads * head_dim]")
     guard, s = _enter(stream, q, k, v, start, out)
-    wp, wn = _ws(ws)
+    wp, wn = _ws(ws, q)
     with guard:
         _abi.wal_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), width // head_dim, k_shape[1] // head_dim,
                              head_dim, T, ldq, ldk, ldv, _index(start, "start"), start.numel() - 1, max_len,

@@ -582,21 +582,31 @@ int launch_combine(const AttnParams& p, cudaStream_t s) {
   return launched(e, "attn_combine_kernel");
 }
 
-constexpr int kDecPieces = 12;
+constexpr int kDecMany = 12, kDecFew = 4;  // decode pieces an SM
+constexpr int kDecPieceBytes = 1 << 20;  // K and V of a piece, with kDecMany
 constexpr int kPlanSms = 148;  // SMs the splits are planned for: a constant, so that a workspace size holds on any device
 
 // How the keys are split.
-// Decode: a CTA holds a quarter to a half of an SM, so two an SM run at once;
-// about six times as many pieces even out ragged lengths, and a piece has at
-// least 128 keys.
+// Decode: a CTA holds a third to a half of an SM.  Four pieces an SM keep it busy
+// and cost the least beside the keys themselves (Q, the warps' join, the partial
+// results); ragged lengths even out with up to twelve, which is worth it while a
+// piece still has 1 MB of K and V.  Measured with four, this rule and twelve:
+// 25 ragged sequences of up to 32768 int8 keys, 8 heads, 220, 179 and 179 us;
+// 4 equal ones 67, 67 and 79; 64 ragged ones of up to 1024, twelve 32, else 27.
 // Tensor-core kernel: the split with the least estimated time, in steps of 128
 // keys (about 1.8 us).  A piece costs three steps more than it has; pieces that
 // more than fill the SMs leave about 1.2 pieces' time unused at the end, the
 // more so as only bounds of the lengths are known here; a split writes and
 // reads fp32 partial results at about 5.7 TB/s, and adds a launch.  Measured,
-// without and with the split it takes: 2 x 1024 tokens over up to 16384 keys
-// 368 and 159 us; 2 x 2048 over 4096 (none) 220, with three 321 us.
-void plan_split(int64_t pieces, int64_t part_bytes, int max_kv, bool tc, int* n_split, int* split_keys) {
+// without and with the split it takes: two sequences of up to 1024 tokens over
+// up to 16384 keys 223 and 134 us; 2 x 2048 over 4096 (none) 189, with three 333.
+void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int max_kv, int* n_split, int* split_keys) {
+  const int group = n_heads / c.n_heads;
+  const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * group;
+  const bool tc = rows > kDecMaxRows;
+  int64_t pieces = (int64_t)B * c.n_heads;  // without a split: one a (sequence, K/V head), or
+  if (tc)                                   // as many row tiles as T rows of B sequences can have
+    pieces = c.n_heads * std::min<int64_t>(B * ((rows + kTcAttnRows - 1) / kTcAttnRows), (int64_t)T * group / kTcAttnRows + B);
   const int64_t tiles = ((int64_t)max_kv + 127) / 128;
   int64_t best = 1;
   if (tc) {
@@ -604,28 +614,21 @@ void plan_split(int64_t pieces, int64_t part_bytes, int max_kv, bool tc, int* n_
     for (int64_t s = 1; s <= 128 && s <= (tiles + 1) / 2; ++s) {
       const double r = (double)(pieces * s) / kPlanSms, steps = (double)((tiles + s - 1) / s) + 3;
       double cost = (r <= 1 ? 1 : r + 1.2) * steps;
-      if (s > 1) cost += 3 + (double)part_bytes * s * 2 / (5.7e6 * 1.8);
+      if (s > 1) cost += 3 + (double)T * n_heads * c.head_dim * 4 * s * 2 / (5.7e6 * 1.8);
       if (s == 1 || cost < best_cost) {
         best = s;
         best_cost = cost;
       }
     }
   } else {
-    const int64_t even = (max_kv * pieces + kDecPieces * kPlanSms - 1) / (kDecPieces * kPlanSms);
-    best = std::max<int64_t>(1, tiles / std::max<int64_t>(1, (even + 127) / 128));
+    const int key_bytes = 2 * c.head_dim * (c.type == WAL_KV_BF16 ? 2 : 1);
+    auto even = [&](int n) { return (max_kv * pieces + n * kPlanSms - 1) / (n * kPlanSms); };
+    const int64_t keys = std::max(even(kDecMany), std::min<int64_t>(even(kDecFew), kDecPieceBytes / key_bytes));
+    best = std::max<int64_t>(1, tiles / std::max<int64_t>(1, (keys + 127) / 128));
   }
   const int64_t keys = (tiles + best - 1) / best * 128;
   *split_keys = (int)std::min<int64_t>(keys, 0x7FFFFF80);
   *n_split = (int)((max_kv + keys - 1) / keys);
-}
-
-// Pieces of a call whose keys are not split: decode, one a (sequence, K/V head);
-// else as many row tiles as T rows of B sequences can have.
-int64_t attn_pieces(int B, int n_kv_heads, int group, int T, int max_q) {
-  const int64_t rows = (int64_t)max_q * group;
-  if (rows <= kDecMaxRows) return (int64_t)B * n_kv_heads;
-  const int64_t most = B * ((rows + kTcAttnRows - 1) / kTcAttnRows);
-  return n_kv_heads * std::min<int64_t>(most, (int64_t)T * group / kTcAttnRows + B);
 }
 
 int launch_attn(const AttnParams& p, cudaStream_t stream) {
@@ -655,8 +658,7 @@ extern "C" size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int 
   if (check_cache(cache) != WAL_OK) return 0;
   if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, 1.f) != WAL_OK) return 0;
   int n_split, split_keys;
-  const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
-  plan_split(attn_pieces(B, cache->n_heads, n_heads / cache->n_heads, T, std::max(1, std::min(max_q, T))), (int64_t)T * n_heads * cache->head_dim * 4, max_kv, rows > kDecMaxRows, &n_split, &split_keys);
+  plan_split(*cache, n_heads, T, B, max_q, max_kv, &n_split, &split_keys);
   return attn_ws_bytes(n_split, T, n_heads, cache->head_dim);
 }
 
@@ -675,8 +677,7 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   int dev = 0;
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
-  const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / cache->n_heads);
-  plan_split(attn_pieces(B, cache->n_heads, n_heads / cache->n_heads, T, std::max(1, std::min(max_q, T))), (int64_t)T * n_heads * cache->head_dim * 4, max_kv, rows > kDecMaxRows, &p.n_split, &p.split_keys);
+  plan_split(*cache, n_heads, T, B, max_q, max_kv, &p.n_split, &p.split_keys);
   if ((ws || p.n_split > 1) && (!ws || ws_bytes < attn_ws_bytes(p.n_split, T, n_heads, cache->head_dim)))
     return fail(WAL_ERR_WORKSPACE, "workspace too small");
   if ((st = current_device(&dev))) return st;

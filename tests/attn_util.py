@@ -68,18 +68,18 @@ def random_cache(rng, lens, page, heads, D, typ, spread=1.0, garbage=True):
 
 def attention_tolerance(o, a, q, k, scale):
     """Largest error of one output.  Every softmax weight is rounded to bf16
-    (half a step, 2^-8) and carries the error of its score: D fp32 products and
-    sums (2^-23 each, the tensor core may truncate) of size sum |q||k|, a
-    product with the scale, and exp2 (2^-21 in all, or the cubic's 2^-13.7,
-    which may enter the weight and the sum that divides it: 2^-12); l and the
-    accumulator are fp32 sums over the keys (2^-23 each); the output is rounded
-    to bf16."""
+    (half a step, 2^-8; the fp16 weights of single tokens over codes are nearer)
+    and carries the error of its score: D fp32 products and sums (2^-23 each,
+    the tensor core may truncate) of size sum |q||k|, a product with the scale,
+    and exp2 (2^-21 in all); l and the accumulator are fp32 sums over the keys
+    (2^-23 each); the output is rounded to bf16.  Beside these nothing counts:
+    q as fp16 is exact but for values 2^-24 below its row's largest."""
     n, heads, D = q.shape
     L = k.shape[0]
     group = heads // k.shape[1]
     size = np.stack([(np.abs(q[:, h]) @ np.abs(k[:, h // group]).T).max(1) if L else np.zeros(n) for h in range(heads)], 1)
     ds = abs(scale) * size * (D + 8) * 2.0 ** -23
-    w = 2.0 ** -8 + 2 * ds[..., None] + 2.0 ** -12 + 2.0 ** -21 + 2 * L * 2.0 ** -23
+    w = 2.0 ** -8 + 2 * ds[..., None] + 2.0 ** -21 + 2 * L * 2.0 ** -23
     return (a * w) * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(o) + 1e-30
 
 
