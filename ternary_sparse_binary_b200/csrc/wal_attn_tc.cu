@@ -225,21 +225,25 @@ struct Work {
 // head), without those that have no rows, the tile pairs that see most keys
 // first.  The CTAs take one each, then one each in the opposite order, and so
 // on, so that they get about the same.  Each role walks its CTA's pieces by
-// itself, whole warps at a time: a lane looks at a sequence.
+// itself, whole warps at a time: a lane looks at a sequence, and the search for
+// a piece goes on where the last one ended.
 template <int TYPE>
 struct Walk {
   const AttnParams& p;
   int tile, at;            // tile pair, and the next piece's place among those from there on
   int stride, back;        // pieces to the next one, and to the one after that
   AttnSeq mine;            // this lane's sequence, and how many tile pairs and splits it has
-  int tiles, splits;
-  __device__ __forceinline__ Walk(const AttnParams& p_, int most) : p(p_), tile(most - 1), at(blockIdx.x) {
+  int tiles, splits, held; // (the first lane's sequence)
+  int each, same;          // of `tile`: pieces of one head, -1 if not counted yet, and the last pair with the same ones
+  int down, b0, before;    // where the search stands: the tile pair, the sequences, the pieces before them
+  __device__ __forceinline__ Walk(const AttnParams& p_, int most) : p(p_), tile(most - 1), at(blockIdx.x), held(-1), each(-1) {
     stride = 2 * ((int)gridDim.x - (int)blockIdx.x) - 1;
     back = 2 * (int)blockIdx.x + 1;
-    look(0);
   }
-  __device__ __forceinline__ void look(int b0) {  // at sequences b0 .. b0 + 31
-    const int b = b0 + (threadIdx.x & 31);
+  __device__ __forceinline__ void look(int first) {  // at 32 sequences
+    if (first == held) return;
+    held = first;
+    const int b = first + (threadIdx.x & 31);
     tiles = 0;
     splits = 1;
     if (b >= p.B) return;
@@ -251,27 +255,33 @@ struct Walk {
   __device__ __forceinline__ bool next(Work& w, AttnSeq& s) {
 #pragma unroll 1
     while (tile >= 0) {
-      // pieces of one head in this tile pair, and the last pair with the same ones
-      int each = 0, same = 0;
+      if (each < 0) {
+        each = same = 0;
+        down = -1;
 #pragma unroll 1
-      for (int b0 = 0; b0 < p.B; b0 += 32) {
-        if (p.B > 32) look(b0);
-        each += __reduce_add_sync(0xffffffffu, tiles > tile ? splits : 0);
-        same = max(same, __reduce_max_sync(0xffffffffu, tiles > tile ? 0 : tiles));
+        for (int b1 = 0; b1 < p.B; b1 += 32) {
+          look(b1);
+          each += __reduce_add_sync(0xffffffffu, tiles > tile ? splits : 0);
+          same = max(same, __reduce_max_sync(0xffffffffu, tiles > tile ? 0 : tiles));
+        }
       }
       const int per = each * p.n_kv_heads, pairs = tile - same + 1;
       if (at >= per * pairs) {
         at -= per * pairs;
         tile = same - 1;
+        each = -1;
         continue;
       }
-      const int down = at / per, place = at - down * per;
+      if (at / per != down) {
+        down = at / per;
+        b0 = before = 0;
+      }
+      const int place = at - down * per;
       const int of = place / p.n_kv_heads;  // of `each`
       w.h = place - of * p.n_kv_heads;
-      int before = 0, b0 = 0, mask = 0;
 #pragma unroll 1
-      for (;; b0 += 32) {  // the sequence with the of-th piece
-        if (p.B > 32) look(b0);
+      for (; b0 < p.B; b0 += 32) {  // the sequence with the of-th piece
+        look(b0);
         const int v = tiles > tile ? splits : 0;
         int sum = v;
 #pragma unroll
@@ -279,7 +289,7 @@ struct Walk {
           const int up = __shfl_up_sync(0xffffffffu, sum, o);
           if ((int)(threadIdx.x & 31) >= o) sum += up;
         }
-        mask = __ballot_sync(0xffffffffu, before + sum > of);
+        const int mask = __ballot_sync(0xffffffffu, before + sum > of);
         if (mask) {
           const int src = __ffs(mask) - 1;
           w.b = b0 + src;
@@ -292,6 +302,7 @@ struct Walk {
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
       }
+      if (b0 >= p.B) return false;  // the index arrays were changed meanwhile
       w.r0 = (tile - down) * kTcAttnRows;
       at += stride;
       const int other = stride;
@@ -671,6 +682,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
   const float2 sl2 = make_float2(sl, sl);
   const bool sectors = (((uintptr_t)p.O | (uintptr_t)(p.ldo * 2)) & 31) == 0;  // every row of O starts on 32 bytes
   uint32_t steps = 0, pieces = 0, duals = 0, tiles = 0;
+  bool redo = false;
   auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, bar_wait(bar, parity, p.status)); };
   auto arrive = [&](uint32_t bar) {  // for the warp
     tc_fence_before();
@@ -867,8 +879,24 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       if (live) p.part_ml[pr] = make_float2(m, l);
       continue;
     }
-    // a key that the row does not see may have made it NaN
-    uint32_t again = __ballot_sync(0xffffffffu, live && nan && lim < w.k1);
+    redo |= __any_sync(0xffffffffu, live && nan && lim < w.k1);
+  }
+  if (!redo) return;
+  // Rows that a key which they do not see may have made NaN.  This comes after
+  // the last piece, when nobody waits for this warp.
+  Walk<TYPE> once_more(p, most);
+#pragma unroll 1
+  while (once_more.next(w, s)) {
+    const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
+    const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
+    const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
+    bool nan = false;
+    if (live && attn_limit(s, tok) < w.k1) {
+      const uint16_t* o = p.O + (s.q0 + tok) * p.ldo + head * D;
+#pragma unroll 1
+      for (int i = 0; i < D; ++i) nan |= (o[i] & 0x7FFF) > 0x7F80;
+    }
+    uint32_t again = __ballot_sync(0xffffffffu, nan);
 #pragma unroll 1
     while (again) {
       const int src = __ffs(again) - 1;

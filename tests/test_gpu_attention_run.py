@@ -200,6 +200,31 @@ def test_decode_many_sequences(typ):
     run_paged(lens, [1] * 130, 4, 2, 128, 32, typ, seed=90, spread=2.0, bounds=(1, 4096))
 
 
+def test_many_short_chunks():
+    """Drafts of a few tokens for more sequences than the kernel has CTAs."""
+    rng = np.random.default_rng(300)
+    lens = [int(n) for n in rng.integers(0, 200, 300)]
+    run_paged(lens, [int(n) for n in rng.integers(0, 9, 300)], 8, 2, 64, 16, "int8", seed=300, spread=2.0)
+
+
+def test_long_prompt_with_a_nonfinite_last_value():
+    """Thousands of keys are gone through again for each row beside the bad one, and nobody gives up waiting."""
+    w = wal()
+    rng = np.random.default_rng(31)
+    T, D = 12000, 64
+    q, k, v = (torch.from_numpy(rng.normal(size=(T, h * D)).astype(np.float32)).bfloat16().cuda() for h in (4, 1, 1))
+    ref, out = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(512, dtype=torch.uint8, device="cuda")
+    w.attn_prompt(q, k, v, i32([0, T]), ref, head_dim=D, max_len=T, ws=ws)
+    v[T - 1] = float("nan")
+    w.attn_prompt(q, k, v, i32([0, T]), out, head_dim=D, max_len=T, ws=ws)
+    w.attention.status(ws)
+    assert torch.isnan(out[T - 1]).all()
+    # done again in fp32: the weights' rounding (2^-8 of at most max |v| < 6) and two of the output
+    r, o = ref[:T - 1].float(), out[:T - 1].float()
+    assert torch.all((o - r).abs() <= 2.0 ** -7 * r.abs() + 6 * 2.0 ** -8)
+
+
 def test_one_token_of_everything():
     """The smallest calls: one token, one head, one page."""
     for typ in TYPES:
