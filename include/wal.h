@@ -491,7 +491,7 @@ size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, in
  * token i sees the keys j <= kv_len[b] - (q_start[b + 1] - q_start[b]) + i.
  *   O[t][h] = sum_j softmax_j(scale * Q[t][h] . K[j]) V[j]       (bf16 [T][ldo])
  * with the maximum, the sum and the accumulators in fp32, and each softmax
- * weight rounded to bf16 for its product with V.  A row that sees no key gets
+ * weight rounded to bf16 (or fp16) for its product with V.  A row that sees no key gets
  * zeros.  Keys a row does not see never reach it, whatever they hold.
  * 1 <= B <= 65535; max_q >= 1 and max_kv >= 1 bound the lengths (they size the grid and
  * the workspace), ceil(max_kv / page_size) <= ld_table.  Rows of no sequence

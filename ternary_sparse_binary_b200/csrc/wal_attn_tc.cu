@@ -24,6 +24,12 @@
 // P_t once P_t V has been issued, and a softmax that sees its S_t finished knows
 // that its O_t is too.
 //
+// Bound by the chain of a step, softmax of one tile beside the products of the other:
+// about 3200 cycles where the MMAs take 2048.  A prompt of 8192 tokens, 32 q heads of
+// 128 on 8: 429 us, 1280 TFLOP/s of what the mask leaves.  One warp issues all MMAs:
+// two of them made the halves fall in step (552 us against 507 then); 16 softmax
+// warps, two to a row, were slower too (592).
+//
 // The maximum is lazy: m follows the row's running maximum only when that has
 // grown by more than 2^16, since weights up to 2^16 and sums of them keep their
 // relative precision in bf16 and fp32; O is then rescaled in tensor memory,
