@@ -604,6 +604,9 @@ constexpr int kPlanSms = 148;  // SMs the splits are planned for: a constant, so
 // without and with the split it takes: two sequences of up to 1024 tokens over
 // up to 16384 keys 223 and 128 us; 2 x 2048 over 4096 (none) 189, with three 333.
 void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int max_kv, int* n_split, int* split_keys) {
+  *n_split = 1;
+  *split_keys = max_kv;
+  if (T == 0) return;
   const int group = n_heads / c.n_heads;
   const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * group;
   const bool tc = rows > kDecMaxRows;
@@ -684,7 +687,7 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   if ((ws || p.n_split > 1) && (!ws || ws_bytes < attn_ws_bytes(p.n_split, T, n_heads, cache->head_dim)))
     return fail(WAL_ERR_WORKSPACE, "workspace too small");
   if ((st = current_device(&dev))) return st;
-  p.clear = T > 0 && p.n_split > 1;
+  p.clear = p.n_split > 1;
   p.status = status_word(ws);
   if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
   if (T == 0) return WAL_OK;

@@ -250,3 +250,23 @@ def test_workspaces_are_checked_and_cleared():
     none = x[:0]
     cache.read(i32([[0]]), i32([0, 0]), none, none, max_len=16, ws=ws)  # nothing to read: nothing recorded
     w.attention.status(ws)
+
+
+def test_calls_without_tokens():
+    """Empty batches change nothing, whatever the bounds."""
+    w = wal()
+    rope, cache = w.Rope(64), w.KvCache.empty(4, 16, 2, 64, dtype=torch.int8)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        t.zero_()
+    x, none = torch.zeros(0, 256, dtype=torch.bfloat16, device="cuda"), i32([])
+    kv, tab = x[:, :128], torch.zeros(3, 2048, dtype=torch.int32, device="cuda")
+    ws = torch.full((512,), 0xFF, dtype=torch.uint8, device="cuda")
+    for scratch in (None, ws):
+        rope.apply(x, none, x)
+        cache.append(kv, kv, none, positions=none, rope=rope, ws=scratch)
+        cache.read(tab, i32([0, 0, 0, 0]), kv, kv, max_len=32768, ws=scratch)
+        for max_q in (1, 500):
+            cache.attend(x, i32([0, 0, 0, 0]), i32([5, 0, 9]), tab, x, max_q=max_q, max_kv=32768, ws=scratch)
+        w.attn_prompt(x, kv, kv, i32([0, 0]), x, head_dim=64, max_len=100, ws=scratch)
+    w.attention.status(ws)
+    assert not cache.k.any() and not cache.k_scale.any()
