@@ -586,16 +586,19 @@ int launch_combine(const AttnParams& p, cudaStream_t s) {
 }
 
 constexpr int kDecMany = 12, kDecFew = 4;  // decode pieces an SM
-constexpr int kDecPieceBytes = 1 << 20;  // K and V of a piece, with kDecMany
+constexpr int kDecRowBytes = 128 << 10;  // K and V of a piece for each of its query rows, with more than kDecFew
 constexpr int kPlanSms = 148;  // SMs the splits are planned for: a constant, so that a workspace size holds on any device
 
 // How the keys are split.
 // Decode: a CTA holds a third to a half of an SM.  Four pieces an SM keep it busy
 // and cost the least beside the keys themselves (Q, the warps' join, the partial
-// results); ragged lengths even out with up to twelve, which is worth it while a
-// piece still has 1 MB of K and V.  Measured with four, this rule and twelve:
-// 25 ragged sequences of up to 32768 int8 keys, 8 heads, 220, 179 and 179 us;
-// 4 equal ones 67, 67 and 79; 64 ragged ones of up to 1024, twelve 32, else 27.
+// results of each query row); ragged lengths even out with up to twelve, which is
+// worth it while a piece has 128 KB of K and V for each of its rows.  Measured with
+// four an SM, this rule and twelve: 25 ragged sequences of up to 32768 int8 keys,
+// 8 heads for 32, 220, 179 and 179 us; 4 equal ones 67, 67 and 79.  With 1 MB in the
+// place of 128 KB a row, this rule: 25 of up to 16384 keys 116 and 100 us, 16 heads
+// of 64 each with 4 tokens over up to 8192 keys 93 and 71; the one that lost, 2 equal
+// bf16 sequences of 100000 keys, 138 and 154.
 // Tensor-core kernel: the split with the least estimated time, in steps of 128
 // keys (about 1.8 us).  A piece costs three steps more than it has; pieces that
 // more than fill the SMs leave about 1.2 pieces' time unused at the end, the
@@ -629,7 +632,7 @@ void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int
   } else {
     const int key_bytes = 2 * c.head_dim * (c.type == WAL_KV_BF16 ? 2 : 1);
     auto even = [&](int n) { return (max_kv * pieces + n * kPlanSms - 1) / (n * kPlanSms); };
-    const int64_t keys = std::max(even(kDecMany), std::min<int64_t>(even(kDecFew), kDecPieceBytes / key_bytes));
+    const int64_t keys = std::max(even(kDecMany), std::min<int64_t>(even(kDecFew), rows * kDecRowBytes / key_bytes));
     best = std::max<int64_t>(1, tiles / std::max<int64_t>(1, (keys + 127) / 128));
   }
   const int64_t keys = (tiles + best - 1) / best * 128;
