@@ -45,9 +45,12 @@ def _index(x, what, n=None):
     return x.data_ptr()
 
 
-def _table(x, B):
+def _table(x, B, most, page_size):
     if x.dtype != torch.int32 or x.dim() != 2 or x.shape[0] != B or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError(f"table: int32 [{B}, pages] with last stride 1")
+    # the library sees the row stride alone, which in a slice of a wider table says nothing of its columns
+    if x.shape[1] * page_size < most:
+        raise ValueError(f"table: {x.shape[1]} pages of {page_size} do not cover {most} tokens")
     return x.data_ptr(), (x.stride(0) if B > 1 else x.shape[1])
 
 
@@ -162,7 +165,7 @@ class KvCache:
         vt, ldv, *shape = _rows(v_out, "v_out")
         if vt != kt or shape != [T, width] or width != self.n_heads * self.head_dim:
             raise ValueError("k_out and v_out: [rows, heads * head_dim] of one type")
-        tp, ldt = _table(table, B)
+        tp, ldt = _table(table, B, max_len, self.page_size)
         if T == 0 and ws is None:
             return
         guard, s = _enter(stream, self.k, table, start, k_out, v_out)
@@ -188,7 +191,7 @@ class KvCache:
         if shape != [T, width] or width % self.head_dim:
             raise ValueError("q and out: [tokens, n_heads * head_dim]")
         B, n_heads = kv_len.numel(), width // self.head_dim
-        tp, ldt = _table(table, B)
+        tp, ldt = _table(table, B, max_kv, self.page_size)
         guard, s = _enter(stream, self.k, q, q_start, kv_len, table, out)
         if ws is None:
             n = self.attend_workspace_bytes(n_heads, T, B, max_q, max_kv)  # 0: the call below says what is wrong

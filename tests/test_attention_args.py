@@ -181,3 +181,20 @@ def test_binding_checks_tensors():
                  lambda: c.read(i(0)[None], i(0, 3), x, x[:, ::2], 3)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_narrow_slice_of_a_page_table_is_refused():
+    """The bound on the lengths reaches past the table's columns, into a wider table that it is a slice of."""
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    c = wal.KvCache(k, k)
+    i = lambda *v: torch.tensor(v, dtype=torch.int32)
+    wide = torch.zeros(2, 8, dtype=torch.int32)
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    for n in (1, 3, 7):
+        table = wide[:, 8 - n:]
+        with pytest.raises(ValueError, match="cover"):
+            c.attend(x, i(0, 1, 2), i(1, 1), table, x, max_q=1, max_kv=16 * n + 1)
+        with pytest.raises(ValueError, match="cover"):
+            c.read(table, i(0, 1, 2), x, x, max_len=16 * n + 1)
+        with pytest.raises(ValueError, match="device"):  # as far as the table goes: the next check
+            c.attend(x, i(0, 1, 2), i(1, 1), table, x, max_q=1, max_kv=16 * n)
