@@ -493,8 +493,8 @@ size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, in
  * with the maximum, the sum and the accumulators in fp32, and each softmax
  * weight rounded to bf16 (or fp16) for its product with V.  A row that sees no key gets
  * zeros.  Keys a row does not see never reach it, whatever they hold.
- * 1 <= B <= 65535; max_q >= 1 and max_kv >= 1 bound the lengths (they size the grid and
- * the workspace), ceil(max_kv / page_size) <= ld_table.  Rows of no sequence
+ * 1 <= B <= 65535; max_q >= 1 and 1 <= max_kv <= 2^30 bound the lengths (they size the
+ * grid and the workspace), ceil(max_kv / page_size) <= ld_table.  Rows of no sequence
  * (before q_start[0] or from q_start[B] on) are left as they are.
  * A sequence whose starts decrease or leave [0, T], with more than max_q new
  * tokens, or with kv_len outside [0, max_kv] is left out, its rows unwritten;
@@ -509,7 +509,8 @@ int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, in
 /* Causal attention over whole prompts, packed one after another: rows
  * start[b] .. start[b + 1] - 1 of Q, K, V and O (bf16) are sequence b, and its
  * token i sees its tokens 0 .. i.  Formula, types, bounds and reports as in
- * wal_attn_paged with max_len in the place of max_q.  head_dim 64 or 128.
+ * wal_attn_paged with max_len in the place of max_q; min(max_len, T) <= 2^30.
+ * head_dim 64 or 128.
  * ws: NULL, or at least 512 bytes.  Asynchronous. */
 int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
                     int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B, int max_len,

@@ -521,6 +521,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
   finish_row<D>(p, s, b, head, tok, acc, ll);
 }
 
+// Longest sequence: the kernels add a split or a step to a key's number in 32 bits.
+constexpr int kMaxKeys = 1 << 30;
+
 int check_attn(int n_heads, int n_kv_heads, int head_dim, int T, int B, int max_q, int max_kv, float scale) {
   if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads)
     return fail(WAL_ERR_SHAPE, "n_heads must be a positive multiple of the K/V heads");
@@ -530,6 +533,7 @@ int check_attn(int n_heads, int n_kv_heads, int head_dim, int T, int B, int max_
     return fail(WAL_ERR_SHAPE, "T >= 0, 1 <= B <= 65535 and the length bounds >= 1");
   if ((int64_t)max_q * (n_heads / n_kv_heads) > 0x7FFFFF00) return fail(WAL_ERR_UNSUPPORTED, "max_q * group must be below 2^31 - 256");
   if (((int64_t)T * n_heads / kTcAttnRows + (int64_t)B * n_kv_heads) > 0x7FFFFFFF / 128) return fail(WAL_ERR_UNSUPPORTED, "T * n_heads and B * n_kv_heads must stay below 2^32 and 2^24");
+  if (max_kv > kMaxKeys) return fail(WAL_ERR_UNSUPPORTED, "at most 2^30 tokens a sequence");
   if (!std::isfinite(scale)) return fail(WAL_ERR_ARG, "scale must be finite");
   return WAL_OK;
 }
@@ -714,7 +718,7 @@ extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint1
                                int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B,
                                int max_len, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
                                wal_stream_t stream) {
-  int st = check_attn(n_heads, n_kv_heads, head_dim, T, B, max_len, max_len, scale);
+  int st = check_attn(n_heads, n_kv_heads, head_dim, T, B, max_len, std::max(1, std::min(max_len, T)), scale);
   if (st) return st;
   const int64_t width = (int64_t)n_heads * head_dim, kv_width = (int64_t)n_kv_heads * head_dim;
   if ((st = check_bf16_rows(Q, ldq, width, T > 0, "Q")) || (st = check_bf16_rows(K, ldk, kv_width, T > 0, "K")) ||

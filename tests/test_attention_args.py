@@ -198,3 +198,18 @@ def test_a_narrow_slice_of_a_page_table_is_refused():
             c.read(table, i(0, 1, 2), x, x, max_len=16 * n + 1)
         with pytest.raises(ValueError, match="device"):  # as far as the table goes: the next check
             c.attend(x, i(0, 1, 2), i(1, 1), table, x, max_q=1, max_kv=16 * n)
+
+
+def test_lengths_past_32_bits_of_arithmetic_are_refused():
+    """The kernels add splits and steps to a key's number: a bound near 2^31 would wrap them."""
+    wide = dict(cache=cache(n_pages=2 ** 22, page_size=256, n_heads=1, type=wal.WAL_KV_BF16), n_heads=1, ldq=64, ldo=64,
+                ld_table=2 ** 23)
+    for n_kv in (2 ** 30 + 1, 2 ** 31 - 1):
+        for max_q in (1, 3):
+            refuses(wal.WAL_ERR_UNSUPPORTED, wal.wal_attn_paged, *args(PAGED, dict(wide, max_kv=n_kv, max_q=max_q)))
+            assert wal.wal_attn_paged_workspace_bytes(wide["cache"], 1, 6, 2, max_q, n_kv) == 0
+    assert wal.wal_attn_paged_workspace_bytes(wide["cache"], 1, 6, 2, 3, 2 ** 30) >= 512
+    refuses(wal.WAL_ERR_UNSUPPORTED, wal.wal_attn_prompt, *args(PROMPT, dict(n_heads=1, n_kv_heads=1, T=2 ** 30 + 1, max_len=2 ** 31 - 300)))
+    # a loose bound is no reason: no sequence has more tokens than the call
+    if not torch.cuda.is_available():
+        refuses(wal.WAL_ERR_CUDA, wal.wal_attn_prompt, *args(PROMPT, dict(n_heads=1, n_kv_heads=1, max_len=2 ** 31 - 300)))
