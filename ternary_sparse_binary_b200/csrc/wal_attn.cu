@@ -16,8 +16,8 @@ namespace {
 
 constexpr int kRowWarps = 4;
 
-// Divide, round and store a row held by a warp.  A row that does not see every
-// key and came out as NaN is done again from its own keys.
+// Divide, round and store a row held by a warp.  A row that came out as NaN
+// beside a non-finite V which it does not see is done again from its own keys.
 template <int D>
 __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s, int b, int head, int tok, const float* acc,
                                            float l) {
@@ -30,9 +30,12 @@ __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s
     y[i] = lim == 0 ? 0.f : acc[i] / l;
     nan |= y[i] != y[i];
   }
-  if (__any_sync(0xffffffffu, nan) && lim < s.len) {
-    attend_row<D>(p, s, b, head, tok);
-    return;
+  if (__any_sync(0xffffffffu, nan && l == l)) {
+    const int h = head / p.group, reach = attn_reach(p, s, tok * p.group + head - h * p.group);
+    if (lim < reach && attn_last_nonfinite<D>(p, s, b, h, lim, reach) >= 0) {
+      attend_row<D>(p, s, b, head, tok);
+      return;
+    }
   }
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + (s.q0 + tok) * p.ldo + head * D + lane * VPL);
 #pragma unroll

@@ -75,12 +75,59 @@ __device__ __forceinline__ int64_t attn_part_row(const AttnParams& p, const Attn
   return (int64_t)(s.q0 + tok) * p.n_heads + head;
 }
 
+// A key that a row does not see has the weight 0 there, but the row's piece
+// multiplies it with V all the same, and 0 * NaN or 0 * inf is NaN.  Such a row
+// is done again by attend_row; a row that is NaN by a key it sees, by its own Q
+// or by its sum of weights (hidden keys add exactly 0 to that) is right as it
+// is.  The keys in question are few: a piece's keys end at the limit of its last
+// row, and its rows are those of one multiple of kTcAttnRows (the decode
+// kernel's are fewer than that altogether).
+__device__ __forceinline__ int attn_reach(const AttnParams& p, const AttnSeq& s, int row) {
+  return attn_limit(s, min(row | (kTcAttnRows - 1), s.n_q * p.group - 1) / p.group);
+}
+// The last of the keys [from, to) whose V, or V scale, is not finite; -1 without
+// one.  By a warp, a key a lane.
+template <int D>
+__device__ __noinline__ int attn_last_nonfinite(const AttnParams& p, const AttnSeq& s, int b, int h, int from, int to) {
+  const bool codes = p.table && p.type != WAL_KV_BF16;
+  int last = -1;
+#pragma unroll 1
+  for (int j = from + (int)(threadIdx.x & 31); j < to; j += 32) {
+    const int64_t row = p.table ? attn_page_row(p, b, h, j) : 0;
+    const char* v = static_cast<const char*>(p.v);
+    if (!p.table)
+      v += ((s.q0 + j) * p.ldv + h * D) * 2;
+    else
+      v += row * (codes ? D : 2 * D);
+    // the largest magnitude of the row's halves or, in e4m3, bytes; int8 codes are all finite
+    uint32_t top = 0;
+    if (!codes || p.type == WAL_KV_E4M3) {
+      const uint32_t mask = codes ? 0x7F7F7F7Fu : 0x7FFF7FFFu;
+#pragma unroll 4
+      for (int i = 0; i < (codes ? D / 16 : D / 8); ++i) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(v) + i);
+        const uint32_t x = codes ? __vmaxu4(__vmaxu4(u.x & mask, u.y & mask), __vmaxu4(u.z & mask, u.w & mask))
+                                 : __vmaxu2(__vmaxu2(u.x & mask, u.y & mask), __vmaxu2(u.z & mask, u.w & mask));
+        top = codes ? __vmaxu4(top, x) : __vmaxu2(top, x);
+      }
+    }
+    bool bad;
+    if (codes)
+      bad = !(fabsf(p.vs[row]) < INFINITY) || __vcmpeq4(top, 0x7F7F7F7Fu) != 0;
+    else
+      bad = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
+    if (bad) last = j;
+  }
+  return __reduce_max_sync(0xffffffffu, last);
+}
+
 // One row by one warp, in fp32: lane i holds columns [i * VPL, (i + 1) * VPL).
-// Only visible keys are touched, and a non-finite one among them acts as in
-// the formula: a NaN score, a +inf score, scores that are all -inf, or a
-// non-finite value under any weight give NaN.  The kernels below come back to
-// it for a row that a key of its tile turned into NaN without being visible
-// (its weight is 0, but 0 * NaN is NaN).
+// Only visible keys are touched, and a non-finite one among them acts as in the
+// formula: a NaN or +inf score, or scores that are all -inf, give NaN; so does
+// a NaN in V, or an infinity there under the weight 0; under another weight the
+// infinity stays one.  Nothing can change a row of NaN, so it ends there.  Slow,
+// a key after the other (0.5 us each): a prompt of 8192, 32 q heads of 128 on 8, whose
+// last V is NaN takes 137 ms (0.44 without it), all for the rows of the last pieces.
 template <int D>
 __device__ __noinline__ void attend_row(const AttnParams& p, const AttnSeq& s, int b, int head, int tok) {
   constexpr int VPL = D / 32;
@@ -150,6 +197,12 @@ __device__ __noinline__ void attend_row(const AttnParams& p, const AttnSeq& s, i
     l = l * c + w;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] = acc[i] * c + w * v[i];
+    if ((j & 15) == 0) {
+      bool dead = true;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) dead &= acc[i] != acc[i];
+      if (__all_sync(0xffffffffu, dead || l != l)) break;
+    }
   }
   uint16_t* o = p.O + (s.q0 + tok) * p.ldo + head * D + lane * VPL;
 #pragma unroll

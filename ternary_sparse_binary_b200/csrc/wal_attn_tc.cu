@@ -40,7 +40,8 @@
 // Keys past a row's limit get the score -inf.  V rows past the last key of the
 // CTA are zeroed, since 0 * NaN would spread what lies there; a key that only
 // some rows see may still do that to the others, and such a row, NaN at the
-// end, is done again from its own keys (attend_row).
+// end though its sum of weights is not, is done again from its own keys if a V
+// behind its last key is to blame (attn_last_nonfinite, attend_row).
 //
 // All waits are bounded; one that gives up records WAL_ERR_TIMEOUT, and its
 // role stops, waits for its copies or MMAs in flight and leaves.
@@ -671,6 +672,46 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32
 }
 
 // ---------------------------------------------------------------------------
+// rows beside a non-finite value
+// ---------------------------------------------------------------------------
+// Rows of half t that a key which they do not see has made NaN.  This comes after
+// the CTA's last piece, when nobody waits for this warp; a call of its own, so
+// that its code and registers stay out of the loop of softmax_rows.
+template <int D, int TYPE>
+__device__ __noinline__ void redo_rows(const AttnParams& p, int most, int t) {
+  const int tid = threadIdx.x & 127;
+  Walk<TYPE> walk(p, most);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  while (walk.next(w, s)) {
+    const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
+    const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
+    const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
+    if (!__any_sync(0xffffffffu, live)) continue;
+    const int last = attn_last_nonfinite<D>(p, s, w.b, w.h, __shfl_sync(0xffffffffu, attn_limit(s, tok), 0), w.k1);
+    bool nan = false;
+    if (live && attn_limit(s, tok) <= last) {
+      const uint4* o = reinterpret_cast<const uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D);
+#pragma unroll 2
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 o8 = o[i];
+        const uint32_t u[4] = {o8.x, o8.y, o8.z, o8.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) nan |= (u[k] & 0x7FFFu) > 0x7F80u || ((u[k] >> 16) & 0x7FFFu) > 0x7F80u;
+      }
+    }
+    uint32_t again = __ballot_sync(0xffffffffu, nan);
+#pragma unroll 1
+    while (again) {
+      const int src = __ffs(again) - 1;
+      again &= again - 1;
+      attend_row<D>(p, s, w.b, __shfl_sync(0xffffffffu, head, src), __shfl_sync(0xffffffffu, tok, src));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // softmax and output (four warps for a half of the CTA, a row a thread)
 // ---------------------------------------------------------------------------
 // The loops over steps and pieces are kept rolled here and in the other roles:
@@ -885,31 +926,9 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       if (live) p.part_ml[pr] = make_float2(m, l);
       continue;
     }
-    redo |= __any_sync(0xffffffffu, live && nan && lim < w.k1);
+    redo |= __any_sync(0xffffffffu, live && nan && l == l && lim < w.k1);
   }
-  if (!redo) return;
-  // Rows that a key which they do not see may have made NaN.  This comes after
-  // the last piece, when nobody waits for this warp.
-  Walk<TYPE> once_more(p, most);
-#pragma unroll 1
-  while (once_more.next(w, s)) {
-    const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
-    const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
-    const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
-    bool nan = false;
-    if (live && attn_limit(s, tok) < w.k1) {
-      const uint16_t* o = p.O + (s.q0 + tok) * p.ldo + head * D;
-#pragma unroll 1
-      for (int i = 0; i < D; ++i) nan |= (o[i] & 0x7FFF) > 0x7F80;
-    }
-    uint32_t again = __ballot_sync(0xffffffffu, nan);
-#pragma unroll 1
-    while (again) {
-      const int src = __ffs(again) - 1;
-      again &= again - 1;
-      attend_row<D>(p, s, w.b, __shfl_sync(0xffffffffu, head, src), __shfl_sync(0xffffffffu, tok, src));
-    }
-  }
+  if (redo) redo_rows<D, TYPE>(p, most, t);
 }
 
 template <int D, int TYPE>
