@@ -392,7 +392,11 @@ int wal_int3_embed(const wal_int3_table* t, const int32_t* ids, int M, float* ou
  * causes an access outside the caller's buffers.  It records WAL_ERR_ARG in
  * the workspace status word (wal_device_status), as wal_int3_embed does, and
  * each entry point says what happens to the rows concerned.  A call that needs
- * no scratch takes NULL for ws: the same happens, and nothing is recorded. */
+ * no scratch takes NULL for ws: the same happens, and nothing is recorded.
+ *
+ * The device waits of the attention kernels are bounded, as everywhere.  One that
+ * gives up makes the rows that are left without a result NaN, with or without a
+ * workspace, and records WAL_ERR_TIMEOUT. */
 enum { WAL_F32 = 0, WAL_BF16 = 1 };                       /* element types of activations */
 enum { WAL_ROPE_HALF = 0, WAL_ROPE_INTERLEAVED = 1 };     /* which columns make a pair */
 enum { WAL_SCALING_NONE = 0, WAL_SCALING_LINEAR = 1, WAL_SCALING_PARTS = 2 };
@@ -505,6 +509,14 @@ int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, in
                    const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,
                    int max_q, int max_kv, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
                    wal_stream_t stream);
+
+/* For tests of such a wait: attention calls from now on poll that many times
+ * before a wait gives up (0: every wait does so at once), and the usual number
+ * with -1.  Such a call ends early and leaves the device usable: each role of a
+ * CTA stops at its first wait that gives up, waits for its own copies and MMAs in
+ * flight and leaves.  A captured call keeps the number it was captured with.
+ * Returns the previous setting. */
+int wal_debug_wait_polls(int polls);
 
 /* Causal attention over whole prompts, packed one after another: rows
  * start[b] .. start[b + 1] - 1 of Q, K, V and O (bf16) are sequence b, and its

@@ -22,7 +22,7 @@ from ._abi import (  # noqa: F401
     WAL_F32, WAL_BF16, WAL_ROPE_HALF, WAL_ROPE_INTERLEAVED, WAL_SCALING_NONE, WAL_SCALING_LINEAR, WAL_SCALING_PARTS,
     WAL_KV_BF16, WAL_KV_INT8, WAL_KV_E4M3, wal_rope_plan, wal_kv_cache,
     wal_rope_freqs, wal_rope, wal_kv_cache_sizes, wal_kv_append, wal_kv_read,
-    wal_attn_paged_workspace_bytes, wal_attn_paged, wal_attn_prompt,
+    wal_attn_paged_workspace_bytes, wal_attn_paged, wal_attn_prompt, wal_debug_wait_polls,
 )
 from .packed import PackedMatrix, Pq2Matrix, Rc1Matrix, pack_host, pack_pq2_host, to_device, BodyPass  # noqa: F401
 from . import attention  # noqa: F401

@@ -37,7 +37,7 @@ EXPORTED_SYMBOLS = [
     "wal_int4_sizes", "wal_int3_sizes", "wal_int4_pack", "wal_int3_pack", "wal_int4_workspace_bytes",
     "wal_int4_gemm", "wal_int3_embed",
     "wal_rope_freqs", "wal_rope", "wal_kv_cache_sizes", "wal_kv_append", "wal_kv_read",
-    "wal_attn_paged_workspace_bytes", "wal_attn_paged", "wal_attn_prompt",
+    "wal_attn_paged_workspace_bytes", "wal_attn_paged", "wal_attn_prompt", "wal_debug_wait_polls",
     "wal_status_string", "wal_last_error",
 ]
 
@@ -157,6 +157,7 @@ lib.wal_attn_paged_workspace_bytes.argtypes = [_CP, _i, _i, _i, _i, _i]
 lib.wal_attn_paged_workspace_bytes.restype = _sz
 lib.wal_attn_paged.argtypes = [_CP, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
 lib.wal_attn_prompt.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
+lib.wal_debug_wait_polls.argtypes = [_i]
 lib.wal_status_string.argtypes = [_i]
 lib.wal_status_string.restype = ctypes.c_char_p
 lib.wal_last_error.argtypes = []
@@ -405,3 +406,9 @@ def wal_attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, st
                     ws_bytes, stream):
     return _check(lib.wal_attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len,
                                       scale, O, ldo, ws, ws_bytes, stream), "wal_attn_prompt")
+
+
+def wal_debug_wait_polls(polls):
+    """For the timeout tests: polls of a device wait of later attention calls before it gives up, -1 for the
+    usual number.  Returns the previous setting."""
+    return int(lib.wal_debug_wait_polls(polls))

@@ -7,8 +7,10 @@ one of the tensors' device, and nothing here synchronises.  A call that needs
 scratch takes it from torch's allocator on its stream unless it is given `ws`
 (a contiguous uint8 tensor of the size that the matching *_workspace_bytes
 gives, 512 where there is none), which then also receives what `status()`
-reads: whether an index value was out of range.  Without `ws` such values are
-handled the same way, unrecorded.  One `ws` serves one call at a time.
+reads: whether an index value was out of range, or a device wait gave up.
+Without `ws` such values are handled the same way, unrecorded; the rows that a
+wait leaves without a result are NaN either way.  One `ws` serves one call at a
+time.
 """
 import contextlib
 import math

@@ -6,8 +6,10 @@
 // new token i.  One pass over the keys with the running maximum m and sum l:
 // when m grows to m', l and the accumulator are multiplied by 2^(m - m').
 #include "wal_attn.h"
+#include "wal_ptx.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 namespace wal {
@@ -647,7 +649,12 @@ void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int
   *n_split = (int)((max_kv + keys - 1) / keys);
 }
 
-int launch_attn(const AttnParams& p, cudaStream_t stream) {
+// Set by wal_debug_wait_polls: the limit of the device waits of later calls; below 0, the usual one.
+std::atomic<int> g_wait_polls{-1};
+
+int launch_attn(AttnParams& p, cudaStream_t stream) {
+  const int polls = g_wait_polls.load();
+  p.polls = polls < 0 ? (int)ptx::kSpinLimit : polls;
   if (!p.table || (int64_t)p.max_q * p.group > kDecMaxRows) {
     const int st = launch_attn_tc(p, stream);
     return st || p.n_split == 1 ? st : launch_combine(p, stream);
@@ -668,6 +675,8 @@ int launch_attn(const AttnParams& p, cudaStream_t stream) {
 }  // namespace wal
 
 using namespace wal;
+
+extern "C" int wal_debug_wait_polls(int polls) { return g_wait_polls.exchange(polls < 0 ? -1 : polls); }
 
 extern "C" size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q,
                                                  int max_kv) {

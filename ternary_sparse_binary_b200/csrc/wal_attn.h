@@ -23,6 +23,7 @@ struct AttnParams {
   int shift, n_pages;        // log2(page_size)
   int T, B, max_q, max_kv;
   float scale_log2;          // scale * log2(e)
+  int polls;                 // of a device wait before it gives up
   int32_t* status;           // NULL: nothing is recorded
   // A call that splits its keys clears the status word in its first kernel and
   // reports index values in its second, a prompt does both in its one kernel,

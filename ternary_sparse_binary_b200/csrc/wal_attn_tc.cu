@@ -44,7 +44,9 @@
 // behind its last key is to blame (attn_last_nonfinite, attend_row).
 //
 // All waits are bounded; one that gives up records WAL_ERR_TIMEOUT, and its
-// role stops, waits for its copies or MMAs in flight and leaves.
+// role stops, waits for its copies or MMAs in flight and leaves.  What the others
+// wait for then does not come, so that they give up too, the softmax warps last:
+// they make the rows that they have no result for NaN.
 #include "wal_attn.h"
 #include "wal_ptx.cuh"
 
@@ -143,11 +145,11 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 // mbar_wait with its loop rolled: the kernel has many waits, and its code must
 // stay small (see softmax_rows).
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const AttnParams& p) {
 #pragma unroll 1
-  for (uint32_t it = 0; it < kSpinLimit; ++it)
+  for (int it = 0; it < p.polls; ++it)
     if (mbar_try_wait(bar, parity)) return true;
-  if (status) atomicExch(status, (int32_t)WAL_ERR_TIMEOUT);
+  if (p.status) atomicExch(p.status, (int32_t)WAL_ERR_TIMEOUT);
   return false;
 }
 // 32 bytes to a 32-byte aligned address: a whole sector, where two 16-byte
@@ -373,7 +375,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int slot = item % kSlots;
-        if (item >= kSlots) ok = bar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p.status);
+        if (item >= kSlots) ok = bar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tail = !C::codes && kv == 1 && cnt < kTile;
@@ -394,7 +396,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
         }
         __syncwarp();
         if (tail) {  // the piece's last V tile: zero the rows that hold no key of it
-          ok = __all_sync(0xffffffffu, bar_wait(bar, tails & 1, p.status));
+          ok = __all_sync(0xffffffffu, bar_wait(bar, tails & 1, p));
           if (!ok) break;
           ++tails;
 #pragma unroll 1
@@ -435,9 +437,9 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uin
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int rs = item % C::raws, slot = item % C::slots;
-        bool ok = bar_wait(bars.raw_full(rs), (item / C::raws) & 1, p.status);
-        if (ok && kv == 0 && tiles >= kScaleRing) ok = bar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p.status);
-        if (ok && item >= C::slots) ok = bar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p.status);
+        bool ok = bar_wait(bars.raw_full(rs), (item / C::raws) & 1, p);
+        if (ok && kv == 0 && tiles >= kScaleRing) ok = bar_wait(bars.sc_empty(si), ((tiles / kScaleRing) & 1) ^ 1, p);
+        if (ok && item >= C::slots) ok = bar_wait(bars.empty(slot), ((item / C::slots) & 1) ^ 1, p);
         if (!__all_sync(0xffffffffu, ok)) return;
         const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
         // keys that are not there get codes and scales of zero
@@ -499,7 +501,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, int most, uint32_t b
     for (int t = 0; t < 2; ++t) {  // both tiles' copies, then what is left to do for each
       if (!w.has_q(t)) continue;
       uint32_t& uses = t ? uses1 : uses0;
-      if (!__all_sync(0xffffffffu, uses == 0 || bar_wait(bars.q_empty(t), (uses - 1) & 1, p.status))) {
+      if (!__all_sync(0xffffffffu, uses == 0 || bar_wait(bars.q_empty(t), (uses - 1) & 1, p))) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
       }
@@ -571,8 +573,8 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32
       next();
     }
   };
-  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.status); };
-  auto kv_wait = [&](const Pos& at) { return bar_wait(bars.full(at.slot), at.parity, p.status); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p); };
+  auto kv_wait = [&](const Pos& at) { return bar_wait(bars.full(at.slot), at.parity, p); };
   auto all = [&](bool ok) { return (bool)__all_sync(0xffffffffu, ok); };
   // the functions below run in the elected lane
   auto scores = [&](int t, int qt, uint32_t slot) {  // S_t = Q_qt K^T
@@ -672,7 +674,7 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32
 }
 
 // ---------------------------------------------------------------------------
-// rows beside a non-finite value
+// rows beside a non-finite value, and rows without a result
 // ---------------------------------------------------------------------------
 // Rows of half t that a key which they do not see has made NaN.  This comes after
 // the CTA's last piece, when nobody waits for this warp; a call of its own, so
@@ -711,6 +713,32 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, int most, int t) {
   }
 }
 
+// Rows of half t in the CTA's pieces after the first `done`, which a wait that gave
+// up has cut off: NaN, so that the loss shows whoever reads the status word.
+template <int D, int TYPE>
+__device__ __noinline__ void lose_rows(const AttnParams& p, int most, int t, uint32_t done) {
+  const int tid = threadIdx.x & 127;
+  Walk<TYPE> walk(p, most);
+  Work w;
+  AttnSeq s;
+#pragma unroll 1
+  for (uint32_t i = 0; walk.next(w, s); ++i) {
+    const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
+    if (i >= done && row < w.r0 + w.rows && !(w.dual && t == 1)) {
+      const int tok = row / p.group, head = w.h * p.group + row - tok * p.group;
+      const float nan = __int_as_float(0x7FC00000);
+      if (p.n_split > 1) {
+        p.part_ml[(int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head)] = make_float2(nan, nan);
+      } else {
+        uint4* o = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D);
+#pragma unroll 1
+        for (int k = 0; k < D / 8; ++k) o[k] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // ---------------------------------------------------------------------------
 // softmax and output (four warps for a half of the CTA, a row a thread)
 // ---------------------------------------------------------------------------
@@ -729,8 +757,9 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
   const float2 sl2 = make_float2(sl, sl);
   const bool sectors = (((uintptr_t)p.O | (uintptr_t)(p.ldo * 2)) & 31) == 0;  // every row of O starts on 32 bytes
   uint32_t steps = 0, pieces = 0, duals = 0, tiles = 0;
-  bool redo = false;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, bar_wait(bar, parity, p.status)); };
+  uint32_t begun = 0;
+  bool redo = false, lost = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, bar_wait(bar, parity, p)); };
   auto arrive = [&](uint32_t bar) {  // for the warp
     tc_fence_before();
     __syncwarp();
@@ -741,6 +770,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
   AttnSeq s;
 #pragma unroll 1
   while (walk.next(w, s)) {
+    ++begun;
     const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
     const int n = w.n_t(t);
     const int lim = row < w.r0 + w.rows ? min(w.k1, attn_limit(s, row / p.group)) : w.k1;
@@ -751,8 +781,8 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       const int kb = w.k0 + kTile * w.tile_of(t, k);
       const uint32_t ti = tiles + w.tile_of(t, k);
       const uint32_t sc = base + C::scale_off + (ti % kScaleRing) * (2 * kTile * 4);  // K's scales of the tile, then V's
-      if (!wait(bars.s_full(t), steps & 1)) return;
-      if (C::codes && !wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1)) return;
+      lost = !wait(bars.s_full(t), steps & 1) || (C::codes && !wait(bars.sc_full(ti % kScaleRing), (ti / kScaleRing) & 1));
+      if (lost) break;
       tc_fence_after();
       float x[kTile];
 #pragma unroll
@@ -849,6 +879,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
         if (w.dual || w.rows <= kTile) mbar_arrive(bars.sc_empty(ti % kScaleRing));
       }
     }
+    if (lost) break;
     tiles += w.n;
 
     // output: the row's sums over its keys, or its share of them.  A dual
@@ -856,7 +887,8 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
     const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
     float f = 1.f, f1 = 0.f;  // factors of this half's and the other half's sums
     if (n > 0) {
-      if (!wait(bars.o_done(t), pieces++ & 1)) return;
+      lost = !wait(bars.o_done(t), pieces++ & 1);
+      if (lost) break;
       tc_fence_after();
     }
     if (w.dual) {
@@ -864,10 +896,12 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       if (t == 1) {  // half 0 takes it from here
         sts64(ml, make_uint2(__float_as_uint(m), __float_as_uint(l)));
         arrive(bars.join());
-        if (!wait(bars.o1_free(), duals++ & 1)) return;
+        lost = !wait(bars.o1_free(), duals++ & 1);
+        if (lost) break;
         continue;
       }
-      if (!wait(bars.join(), duals++ & 1)) return;
+      lost = !wait(bars.join(), duals++ & 1);
+      if (lost) break;
       tc_fence_after();
       const uint2 u = lds64(ml);
       const float m1 = __uint_as_float(u.x), l1 = __uint_as_float(u.y), mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
@@ -929,6 +963,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
     redo |= __any_sync(0xffffffffu, live && nan && l == l && lim < w.k1);
   }
   if (redo) redo_rows<D, TYPE>(p, most, t);
+  if (lost) lose_rows<D, TYPE>(p, most, t, begun - 1);
 }
 
 template <int D, int TYPE>
