@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
   if (p.clear) {
     if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
   } else if (s.bad && h == 0 && threadIdx.x == 0 && p.status) {
-    atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+    attn_report(p.status);
   }
   if (s.bad) return;
   const int rows = s.n_q * p.group;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
     bool bad = s.bad;
     const int pages = (s.len + (1 << p.shift) - 1) >> p.shift;
     for (int i = threadIdx.x; i < pages; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + b * p.ld_table + i) >= (uint32_t)p.n_pages;
-    if (bad) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+    if (bad) attn_report(p.status);
   }
   const int row = blockIdx.x * (kRowWarps / PER) + warp / PER;  // (token, head)
   if (s.bad || row >= s.n_q * p.n_heads) return;                // PER > 1: the whole CTA

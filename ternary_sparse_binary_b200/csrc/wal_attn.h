@@ -39,6 +39,9 @@ struct AttnParams {
 constexpr int kTcAttnRows = 256;  // query rows of one CTA there
 int launch_attn_tc(const AttnParams& p, cudaStream_t stream);
 
+// An index value out of range: recorded, unless something is already (a wait that gave up).
+__device__ __forceinline__ void attn_report(int32_t* status) { atomicCAS(status, 0, (int32_t)WAL_ERR_ARG); }
+
 // Sequence b as its index arrays give it; n_q = 0 where they are out of range.
 struct AttnSeq {
   int q0, n_q, len;
@@ -63,7 +66,7 @@ __device__ __forceinline__ int attn_limit(const AttnSeq& s, int i) { return max(
 __device__ __forceinline__ int attn_page(const AttnParams& p, int b, int j) {
   const int page = __ldg(p.table + b * p.ld_table + (j >> p.shift));
   if ((uint32_t)page < (uint32_t)p.n_pages) return page;
-  if (!p.clear && p.status) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+  if (!p.clear && p.status) attn_report(p.status);
   return 0;
 }
 // Row of key j in the cache (in units of head_dim elements).

@@ -1032,7 +1032,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   const int most = shape[0];
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) {
     if (p.clear) *p.status = p.n_split == 1 && shape[1] ? (int32_t)WAL_ERR_ARG : 0;
-    else if (shape[1]) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
+    else if (shape[1]) attn_report(p.status);
   }
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 

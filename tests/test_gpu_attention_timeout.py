@@ -109,6 +109,24 @@ def test_chunk(n_q, lens, split, D, typ, polls):
     check(call, out, ws, D, polls)
 
 
+@pytest.mark.parametrize("lens", [[3000, 2500], [100, 90]])
+def test_a_timeout_outlives_a_bad_index(lens):
+    """Both happen: the lost rows are what the status word tells of."""
+    w = wal()
+    call, out, ws, n, table = paged("bf16", 64, [40, 9], lens)
+    assert (n > 1) == (max(lens) > 1000)
+    table[1, 1] = -5
+    call(ws)
+    assert recorded(ws) == w.WAL_ERR_ARG
+    w.wal_debug_wait_polls(0)
+    try:
+        call(ws)
+        torch.cuda.synchronize()
+    finally:
+        w.wal_debug_wait_polls(-1)
+    assert recorded(ws) == w.WAL_ERR_TIMEOUT
+
+
 def test_single_tokens_have_no_such_waits():
     call, out, ws, _, _ = paged("int8", 128, [1, 1], [3000, 70])
     check(call, out, ws, 128, 0, loses=False)
