@@ -399,6 +399,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
           ok = __all_sync(0xffffffffu, bar_wait(bar, tails & 1, p));
           if (!ok) break;
           ++tails;
+          tail = false;
 #pragma unroll 1
           for (int r8 = lane; r8 < (kTile - cnt) * (D / 8); r8 += 32) {
             const int r = cnt + r8 / (D / 8), ch = r8 % (D / 8);

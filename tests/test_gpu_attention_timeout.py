@@ -49,7 +49,7 @@ def check(call, out, ws, head_dim, polls, loses=True):
             took = time.perf_counter() - t0
         finally:
             w.wal_debug_wait_polls(before)
-        assert before == -1 and took < 10.0, f"the call took {took:.1f} s to give up"
+        assert before == -1 and took < 1.0, f"the call took {took:.1f} s to give up"
         got = rows()
         lost = torch.isnan(got).all(-1)
         assert torch.equal(got[~lost], clean[~lost]), "a row is neither right nor NaN"
