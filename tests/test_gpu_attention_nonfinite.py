@@ -3,9 +3,11 @@ import numpy as np
 import pytest
 import torch
 
-from attn_util import TYPES
+from oracle import attn_oracle as ao
+
+from attn_util import TYPES, assert_close, attention_tolerance, bf16, random_cache
 from gpu_util import needs_gpu, wal
-from test_gpu_attention import i32
+from test_gpu_attention import i32, run_paged
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
 
@@ -123,3 +125,74 @@ def test_seen_and_hidden_columns_are_told_apart(D):
     # a row may be done again another way: the weights' rounding to bf16 (2^-8 of at most max |v| < 6), two of the output
     r, o = ref.float(), out.float()
     assert torch.all((o - r)[~hit].abs() <= 2.0 ** -7 * r[~hit].abs() + 6 * 2.0 ** -8)
+
+
+# ---- keys split over CTAs --------------------------------------------------------
+
+BAD = [("bf16", "v", float("nan")), ("bf16", "v", float("inf")), ("bf16", "v", -float("inf")), ("bf16", "k", float("nan")),
+       ("bf16", "k", float("inf")), ("int8", "vs", float("nan")), ("int8", "ks", float("nan")), ("e4m3", "vs", float("nan")),
+       ("e4m3", "ks", float("nan")), ("e4m3", "code", None)]
+
+
+@pytest.mark.parametrize("typ,where,bad", BAD)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_q", [4, 40])
+def test_nonfinite_last_keys_where_keys_are_split(n_q, D, typ, where, bad):
+    """The last two tokens' K or V (or scales) are not finite.  The new tokens of each
+    sequence lie on both sides of a multiple of 128, one of which every border
+    between splits is, so that some rows see nothing of the last split.  Rows
+    before those two tokens are as if they were not there."""
+    w = wal()
+    rng = np.random.default_rng(n_q + D)
+    heads, kv_heads, page = 4, 1, 16
+    lens = [128 * m + n_q // 2 for m in range(4, 24)]
+    (k, v, ks, vs), table, kv, vv = random_cache(rng, lens, page, kv_heads, D, typ)
+    for b, n in enumerate(lens):
+        for j in (n - 2, n - 1):
+            at = (table[b, j // page], slice(None), j % page)
+            if where == "code":
+                v.view(torch.uint8)[at] = 0x7F if j % 2 else 0xFF
+            else:
+                dict(k=k, v=v, ks=ks, vs=vs)[where][at] = bad
+    cache = w.KvCache(*[None if t is None else t.cuda() for t in (k, v, ks, vs)])
+    T, max_kv = n_q * len(lens), max(lens)
+    q = bf16(rng.normal(size=(T, heads * D)))
+    Q = torch.from_numpy(q).bfloat16().cuda()
+    O = torch.full_like(Q, 77.0)
+    assert splits(cache, heads, T, len(lens), n_q, max_kv) > 1
+    cache.attend(Q, i32(range(0, T + 1, n_q)), i32(lens), torch.from_numpy(table).cuda(), O, max_q=n_q, max_kv=max_kv)
+    got = O.cpu().double().numpy().reshape(len(lens), n_q, heads, D)
+    for b, n in enumerate(lens):
+        qb = q[n_q * b:n_q * (b + 1)].reshape(n_q, heads, D)[:n_q - 2]
+        o, a = ao.attend(qb, kv[b][:n - 2], vv[b][:n - 2], D ** -0.5, heads)
+        assert_close(got[b, :n_q - 2], o, attention_tolerance(o, a, qb, kv[b][:n - 2], D ** -0.5), f"sequence {b}")
+        if where == "code":
+            continue  # what the NaN codes read as is not specified
+        if where == "v" and bad == bad:  # infinity, or NaN under a weight of zero
+            assert not np.isfinite(got[b, n_q - 2:]).any()
+        else:  # an infinite K meets q of both signs: inf - inf
+            assert np.isnan(got[b, n_q - 2:]).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_rows_that_see_an_infinite_key(bad, D):
+    """All columns of one K are infinite and q has both signs: the score is inf - inf."""
+    w = wal()
+    T, heads, kv, j = 300, 4, 2, 150
+    q, k, v = normal(T, heads * D), normal(T, kv * D), normal(T, kv * D)
+    ref, out, start = torch.empty_like(q), torch.empty_like(q), i32([0, T])
+    w.attn_prompt(q, k, v, start, ref, head_dim=D, max_len=T)
+    k[j, :D] = bad
+    w.attn_prompt(q, k, v, start, out, head_dim=D, max_len=T)
+    hit = torch.zeros(T, heads * D, dtype=torch.bool, device="cuda")
+    hit[j:, :2 * D] = True
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], ref[~hit])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+@pytest.mark.parametrize("typ", ["int8", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 4, 64])
+def test_zero_and_negative_scales_over_codes(n_q, typ, scale):
+    run_paged([90, 200], [n_q, n_q], 8, 2, 64, 32, typ, scale=scale, seed=n_q)
+    run_paged([1500, 2600], [n_q, n_q], 8, 2, 128, 32, typ, scale=scale, seed=n_q + 1)
