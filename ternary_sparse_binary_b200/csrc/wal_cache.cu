@@ -407,15 +407,18 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   const bool bad = (uint32_t)page >= (uint32_t)p.n_pages;
   if (bad && threadIdx.x == 0 && p.status) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   const int off = j0 & ((1 << p.shift) - 1);
-  const int items = p.head_dim / 16, per = p.n_heads * items, all = 2 * n * per;
+  // a NULL output's half of the cache is left alone
+  const int items = p.head_dim / 16, per = p.n_heads * items, all = (p.out[0] && p.out[1] ? 2 : 1) * n * per;
+  const int first = p.out[0] ? 0 : 1;
   const int64_t row0 = (((int64_t)(bad ? 0 : page) * p.n_heads) << p.shift) + off;  // head 0, token j0
   struct Place {
     int which, j, h, it;
   };
   auto place = [&](int q) {
     Place x;
-    x.which = q >= n * per;
-    const int r = q - x.which * n * per;
+    const int second = q >= n * per;
+    const int r = q - second * n * per;
+    x.which = first + second;
     x.j = r / per;
     const int e = r - x.j * per;
     x.h = e / items;
@@ -444,7 +447,6 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
       if (q0 + u * kThreads >= all) break;
       const Place x = place(q0 + u * kThreads);
       char* out = static_cast<char*>(x.which ? p.out[1] : p.out[0]);
-      if (!out) continue;
       const int64_t dst = (s0 + j0 + x.j) * (x.which ? p.ld[1] : p.ld[0]) + x.h * p.head_dim + 16 * x.it;
       float v[16];
       if (TYPE == WAL_KV_BF16) {

@@ -251,3 +251,45 @@ def test_other_device_values_and_streams():
     cache.read(i32([[0, 1]]), i32([0, 20]), k, v, max_len=20, stream=s)
     s.synchronize()
     assert torch.equal(k, x.bfloat16()) and torch.equal(v, x.bfloat16())
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+def test_reading_one_half_moves_one_half(typ):
+    """With a NULL K or V the other one is read as ever, in half the time."""
+    w = wal()
+    B, L, heads, D, page = 16, 4096, 8, 128, 64
+    cache = w.KvCache.empty(B * L // page, page, heads, D, dtype=TYPES[typ])
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).random_(0, 0x40)
+    for t in (cache.k_scale, cache.v_scale):
+        if t is not None:
+            t.uniform_(0.5, 1.5)
+    table = torch.randperm(B * L // page, device="cuda").int().view(B, -1)
+    start = i32([L * b for b in range(B + 1)])
+    K, V, out = (torch.full((B * L, heads * D), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    s = torch.cuda.current_stream().cuda_stream
+
+    def read(k, v):
+        ptr = lambda x: None if x is None else x.data_ptr()
+        w.wal_kv_read(cache.desc, table.data_ptr(), table.shape[1], start.data_ptr(), B, L, ptr(k), ptr(v), w.WAL_BF16, B * L,
+                      heads * D, heads * D, None, 0, s)
+
+    def us(*args):
+        times = []
+        for _ in range(9):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            read(*args)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return sorted(times)[4]
+
+    both = us(K, V)
+    # bytes in and out, of 8 (bf16) or 6 with both: 4 or 3 without the other half's, 6 or 4 with its reads
+    limit = 0.625 * both
+    for ref, args in ((K, (out, None)), (V, (None, out))):
+        out.fill_(3.0)
+        took = us(*args)
+        assert torch.equal(out, ref)
+        assert took <= limit, f"{took * 1e3:.0f} us against {both * 1e3:.0f} for both"
