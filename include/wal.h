@@ -522,6 +522,7 @@ int wal_debug_wait_polls(int polls);
  * start[b] .. start[b + 1] - 1 of Q, K, V and O (bf16) are sequence b, and its
  * token i sees its tokens 0 .. i.  Formula, types, bounds and reports as in
  * wal_attn_paged with max_len in the place of max_q; min(max_len, T) <= 2^30.
+ * O must not overlap Q, K or V.
  * head_dim 64 or 128.
  * ws: NULL, or at least 512 bytes.  Asynchronous. */
 int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,

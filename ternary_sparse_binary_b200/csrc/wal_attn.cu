@@ -708,6 +708,7 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   if ((st = current_device(&dev))) return st;
   p.clear = p.n_split > 1;
   p.status = status_word(ws);
+  if (T > 0 && O == Q) return fail(WAL_ERR_ARG, "O must not be Q: rows are read again after others are written");
   if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
   if (T == 0) return WAL_OK;
   p.Q = Q; p.O = O;
@@ -743,6 +744,7 @@ extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint1
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
   if (T == 0) return clear_status(ws, s, &p.status);
+  if (O == Q || O == K || O == V) return fail(WAL_ERR_ARG, "O must not be Q, K or V: their rows are read after others are written");
   p.clear = ws != nullptr;
   p.status = status_word(ws);
   p.Q = Q; p.O = O;

@@ -270,3 +270,21 @@ def test_calls_without_tokens():
         w.attn_prompt(x, kv, kv, i32([0, 0]), x, head_dim=64, max_len=100, ws=scratch)
     w.attention.status(ws)
     assert not cache.k.any() and not cache.k_scale.any()
+
+
+def test_outputs_that_are_inputs_are_refused():
+    """Rows are read after others are written, so nothing may be done in place."""
+    w = wal()
+    cache = w.KvCache.empty(4, 16, 2, 64)
+    q, k, v = (torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    start = i32([0, 3])
+
+    def refuses(call):
+        with pytest.raises(w.WalError) as e:
+            call()
+        assert e.value.status == w.WAL_ERR_ARG
+
+    for max_q in (3, 100):
+        refuses(lambda: cache.attend(q, start, i32([3]), i32([[0]]), q, max_q=max_q, max_kv=16))
+    for out in (q, k, v):
+        refuses(lambda: w.attn_prompt(q, k, v, start, out, head_dim=64, max_len=3))
