@@ -26,6 +26,14 @@ _KV_TYPES = {torch.bfloat16: _abi.WAL_KV_BF16, torch.int8: _abi.WAL_KV_INT8, tor
 _X_TYPES = {torch.float32: _abi.WAL_F32, torch.bfloat16: _abi.WAL_BF16}
 _BF16 = {torch.bfloat16: _abi.WAL_BF16}
 _HERE = contextlib.nullcontext()
+_INT = 2 ** 31 - 1
+
+
+def _fits(value, what):
+    """ctypes would pass the low 32 bits of a larger number on."""
+    if value > _INT:
+        raise ValueError(f"{what}: {value} does not fit (strides, sizes and bounds are below 2^31)")
+    return value
 
 
 def _rows(x, what, dtypes=_X_TYPES):
@@ -38,7 +46,7 @@ def _rows(x, what, dtypes=_X_TYPES):
     if one != 1 and cols > 1:
         raise ValueError(f"{what}: the last stride must be 1")
     # a one-row (or empty) tensor's row stride is arbitrary; its width serves
-    return kind, (ld if rows > 1 else cols), rows, cols
+    return kind, _fits(ld if rows > 1 else cols, what), rows, cols
 
 
 def _index(x, what, n=None):
@@ -53,7 +61,7 @@ def _table(x, B, most, page_size):
     # the library sees the row stride alone, which in a slice of a wider table says nothing of its columns
     if x.shape[1] * page_size < most:
         raise ValueError(f"table: {x.shape[1]} pages of {page_size} do not cover {most} tokens")
-    return x.data_ptr(), (x.stride(0) if B > 1 else x.shape[1])
+    return x.data_ptr(), _fits(x.stride(0) if B > 1 else x.shape[1], "table")
 
 
 def _enter(stream, *tensors):
@@ -180,6 +188,7 @@ class KvCache:
         shape = (n_heads, T, B, max_q, max_kv)
         n = self._scratch.get(shape)
         if n is None:
+            _fits(max(shape), "workspace size")
             if len(self._scratch) >= 256:
                 self._scratch.clear()
             n = self._scratch[shape] = _abi.wal_attn_paged_workspace_bytes(self.desc, n_heads, T, B, max_q, max_kv)
@@ -193,6 +202,7 @@ class KvCache:
         if shape != [T, width] or width % self.head_dim:
             raise ValueError("q and out: [tokens, n_heads * head_dim]")
         B, n_heads = kv_len.numel(), width // self.head_dim
+        _fits(max_q, "max_q")
         tp, ldt = _table(table, B, max_kv, self.page_size)
         guard, s = _enter(stream, self.k, q, q_start, kv_len, table, out)
         if ws is None:
@@ -216,6 +226,7 @@ def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, str
     _, ldo, *shape = _rows(out, "out", _BF16)
     if shape != [T, width] or k_shape != v_shape or k_shape[0] != T or width % head_dim or k_shape[1] % head_dim:
         raise ValueError("q and out: [tokens, n_heads * head_dim]; k and v: [tokens, n_kv_heads * head_dim]")
+    _fits(max_len, "max_len")
     guard, s = _enter(stream, q, k, v, start, out)
     wp, wn = _ws(ws, q)
     with guard:

@@ -213,3 +213,24 @@ def test_lengths_past_32_bits_of_arithmetic_are_refused():
     # a loose bound is no reason: no sequence has more tokens than the call
     if not torch.cuda.is_available():
         refuses(wal.WAL_ERR_CUDA, wal.wal_attn_prompt, *args(PROMPT, dict(n_heads=1, n_kv_heads=1, max_len=2 ** 31 - 300)))
+
+
+def test_numbers_past_32_bits_are_refused():
+    """Strides and bounds of which the library would see the low 32 bits only."""
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    c = wal.KvCache(k, k)
+    i = lambda *v: torch.tensor(v, dtype=torch.int32)
+    x = torch.zeros(3, 128, dtype=torch.bfloat16)
+    far = torch.empty(3, 2 ** 32 + 128, dtype=torch.bfloat16, device="meta")[:, :128]
+    table = i(0, 1)[None]
+    for call in (lambda: wal.Rope(64, device="cpu").apply(far, i(0, 1, 2), x), lambda: wal.Rope(64, device="cpu").apply(x, i(0, 1, 2), far),
+                 lambda: c.append(far, x, i(0, 1, 2)), lambda: c.append(x, far, i(0, 1, 2)),
+                 lambda: c.read(table, i(0, 3), far, x, 3), lambda: c.read(table, i(0, 3), x, far, 3),
+                 lambda: c.attend(far, i(0, 3), i(3), table, x, 3, 3), lambda: c.attend(x, i(0, 3), i(3), table, far, 3, 3),
+                 lambda: c.attend(x, i(0, 3), i(3), table, x, 2 ** 32 + 3, 3),
+                 lambda: c.attend(x, i(0, 1, 3), i(1, 2), torch.empty(2, 2 ** 32 + 2, dtype=torch.int32, device="meta")[:, :2], x, 3, 3),
+                 lambda: c.attend_workspace_bytes(2, 3, 1, 3, 2 ** 32 + 3), lambda: c.attend_workspace_bytes(2, 3, 1, 2 ** 32 + 3, 3),
+                 lambda: wal.attn_prompt(x, far, x, i(0, 3), x, 64, 3), lambda: wal.attn_prompt(x, x, far, i(0, 3), x, 64, 3),
+                 lambda: wal.attn_prompt(x, x, x, i(0, 3), x, 64, 2 ** 32 + 3)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
