@@ -486,7 +486,9 @@ int wal_kv_read(const wal_kv_cache* cache, const int32_t* table, int ld_table, c
 
 /* Scratch bytes of wal_attn_paged: the 256-byte header, and partial results
  * where the keys of a sequence are split over CTAs; 512 where they are not (ws
- * may then be NULL).  0 on a bad argument. */
+ * may then be NULL).  0 on a bad argument.  Keys are split to keep the SMs busy,
+ * so fewer tokens or sequences may need MORE bytes than many: a workspace for
+ * several shapes has the largest of their sizes, not that of the largest batch. */
 size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q, int max_kv);
 
 /* Attention of new tokens over the cache that holds them already.  Rows

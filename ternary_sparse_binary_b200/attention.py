@@ -185,6 +185,8 @@ class KvCache:
                              v_out.data_ptr(), kt, T, ldk, ldv, wp, wn, s)
 
     def attend_workspace_bytes(self, n_heads, T, B, max_q, max_kv):
+        """Bytes of a `ws` for attend.  Not monotone: a smaller batch may need more (its keys are split
+        further), so one `ws` for several shapes takes the largest of their sizes."""
         shape = (n_heads, T, B, max_q, max_kv)
         n = self._scratch.get(shape)
         if n is None:

@@ -234,3 +234,18 @@ def test_numbers_past_32_bits_are_refused():
                  lambda: wal.attn_prompt(x, x, x, i(0, 3), x, 64, 2 ** 32 + 3)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+@pytest.mark.parametrize("shapes", [[(n, n, 1, 32768) for n in range(1, 65)], [(T, 4, T, 16384) for T in (1, 16, 64, 256, 512, 1024, 4096)]])
+def test_a_workspace_serves_every_shape_whose_size_it_has(shapes):
+    """Sizes rise and fall with the batch; the largest of them serves all, and each is exact."""
+    c = cache(n_pages=1 << 16, page_size=64, n_heads=8, head_dim=128)
+    call = dict(cache=c, n_heads=32, ldq=4096, ldo=4096, ld_table=512)
+    need = [wal.wal_attn_paged_workspace_bytes(c, 32, *s) for s in shapes]
+    assert need != sorted(need)  # a smaller batch may need more
+    for (T, B, max_q, max_kv), n in zip(shapes, need):
+        kw = dict(call, T=T, B=B, max_q=max_q, max_kv=max_kv)
+        refuses(wal.WAL_ERR_WORKSPACE, wal.wal_attn_paged, *args(PAGED, dict(kw, ws_bytes=n - 1)))
+        if not torch.cuda.is_available():
+            for enough in (n, max(need)):
+                refuses(wal.WAL_ERR_CUDA, wal.wal_attn_paged, *args(PAGED, dict(kw, ws_bytes=enough)))
