@@ -442,10 +442,12 @@ int wal_rope(const wal_rope_plan* rope, const void* X, int x_type, int T, int n_
  *   k_scale, v_scale   fp32 [n_pages][n_heads][page_size], NULL for bf16.
  * A value is its code, times the scale of its (slot, head) row in the 8-bit
  * types: int8 codes in [-127, 127], or e4m3 codes (the two NaN codes are never
- * written; what they read as is not specified), and finite scales.  Buffers are 16-byte aligned.
+ * written; what they read as is not specified), and a scale that is finite, or
+ * NaN for a row that reads as NaN.  Buffers are 16-byte aligned.
  * head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; n_pages * page_size
- * below 2^31.  K and V are the caller's; slots nobody wrote may hold anything,
- * and no entry point reads past a sequence's length. */
+ * below 2^31.  K and V are the caller's.  Slots past a sequence's length may hold
+ * anything: no result depends on them, though the rest of its last page may be
+ * read.  Pages that are not in a sequence's table row up to its length are not. */
 typedef struct wal_kv_cache {
   int32_t n_pages, page_size, n_heads, head_dim, type;
   void* k;
@@ -476,7 +478,8 @@ int wal_kv_append(const wal_kv_cache* cache, const void* K, const void* V, int i
  * lies in page table[b * ld_table + j / page_size] at j % page_size and goes
  * to row start[b] + j of K and V (fp32 or bf16, out_type; one rounding to
  * bf16).  K or V may be NULL to skip it.  max_len bounds the lengths and
- * ceil(max_len / page_size) <= ld_table; T is the number of rows in K and V.
+ * ceil(max_len / page_size) <= ld_table; T is the number of rows in K and V.  With
+ * neither K nor V nothing is looked at.
  * A sequence whose start values do not increase, leave [0, T] or span more than
  * max_len tokens writes nothing, a page id outside [0, n_pages) gives zero
  * rows; both record WAL_ERR_ARG.  ws: NULL, or at least 512 bytes.  Asynchronous. */
@@ -501,7 +504,8 @@ size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, in
  * zeros.  Keys a row does not see never reach it, whatever they hold.
  * 1 <= B <= 65535; max_q >= 1 and 1 <= max_kv <= 2^30 bound the lengths (they size the
  * grid and the workspace), ceil(max_kv / page_size) <= ld_table.  Rows of no sequence
- * (before q_start[0] or from q_start[B] on) are left as they are.
+ * (before q_start[0] or from q_start[B] on) are left as they are.  With T = 0
+ * nothing is looked at.
  * A sequence whose starts decrease or leave [0, T], with more than max_q new
  * tokens, or with kv_len outside [0, max_kv] is left out, its rows unwritten;
  * a page id outside [0, n_pages) makes its sequence's rows unspecified; both
@@ -524,7 +528,8 @@ int wal_debug_wait_polls(int polls);
  * start[b] .. start[b + 1] - 1 of Q, K, V and O (bf16) are sequence b, and its
  * token i sees its tokens 0 .. i.  Formula, types, bounds and reports as in
  * wal_attn_paged with max_len in the place of max_q; min(max_len, T) <= 2^30.
- * O must not overlap Q, K or V.
+ * O must not overlap Q, K or V.  Up to 127 rows of K and V past a sequence's last
+ * may be read, of the T; no result depends on them.
  * head_dim 64 or 128.
  * ws: NULL, or at least 512 bytes.  Asynchronous. */
 int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
