@@ -749,7 +749,7 @@ __device__ __noinline__ void lose_rows(const AttnParams& p, int most, int t, uin
 // step, several times what the instructions do.
 template <int D, int TYPE>
 __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int t, float sl, uint32_t base,
-                                             const uint8_t* gbase, uint32_t tmem, const Bars& bars) {
+                                             uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   const int tid = threadIdx.x & 127;
   const bool lead = (tid & 31) == 0;
@@ -1039,7 +1039,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
-    softmax_rows<D, TYPE>(p, most, warp >> 2, sl, base, gbase, tmem, bars);
+    softmax_rows<D, TYPE>(p, most, warp >> 2, sl, base, tmem, bars);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
     if (warp == 8) {
