@@ -48,8 +48,9 @@ __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s
 // few query rows: keys split over CTAs, mma.sync
 // ---------------------------------------------------------------------------
 // Bound by bytes over bf16 (25 sequences of up to 16384 keys, 8 heads of 128: 133 us,
-// 0.93 of the copy rate) and by instructions over codes (up to 32768 int8 keys: 179
-// us, 0.71); one sequence of 2048 keys takes 8.7 us of a graph, both kernels.
+// 0.93 of the copy rate) and by latency over codes (up to 32768 int8 keys: 179 us,
+// 0.71; registers allow 8 warps an SM, which use 41 % of the issue slots); one
+// sequence of 2048 keys takes 8.9 us of a graph, both kernels.
 // A CTA takes one (sequence, K/V head, split of the keys) and its 8 * NT query
 // rows at most; its four warps take steps of 16 * MT keys in turn.  The keys
 // are the M side of both products, so the few query rows waste little:
@@ -614,7 +615,10 @@ constexpr int kPlanSms = 148;  // SMs the splits are planned for: a constant, so
 // more so as only bounds of the lengths are known here; a split writes and
 // reads fp32 partial results at about 5.7 TB/s, and adds a launch.  Measured,
 // without and with the split it takes: two sequences of up to 1024 tokens over
-// up to 16384 keys 223 and 128 us; 2 x 2048 over 4096 (none) 189, with three 333.
+// up to 16384 keys 223 and 125 us (109 with three instead of two); 2 x 2048 over
+// 4096 (none) 189, with three 333.  All of these are bf16 pages and heads of 128:
+// 8-bit pages, whose steps are longer, and heads of 64 are planned by the same
+// numbers.
 void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int max_kv, int* n_split, int* split_keys) {
   *n_split = 1;
   *split_keys = max_kv;

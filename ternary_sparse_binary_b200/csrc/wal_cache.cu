@@ -126,7 +126,7 @@ __device__ __forceinline__ void rotate16(float (&v)[16], const Rope& r, int it, 
 // ---------------------------------------------------------------------------
 // rotate
 // ---------------------------------------------------------------------------
-// Bound by bytes: 16384 tokens of 40 heads in 53 us, 0.98 of the copy rate; 25 tokens
+// Bound by bytes: 16384 tokens of 40 heads in 54 us, 0.97 of the copy rate; 25 tokens
 // take 2.7 us of a graph.  A CTA takes kTokens tokens (one where there are few:
 // latency).  A thread has
 // the same item of each of them, so that its place is worked out once, and loads
@@ -244,8 +244,8 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Bound by instructions in the 8-bit types (38 us for 16381 tokens of 8 heads, 0.41 of
-// the copy rate; 26 and 0.81 to a bf16 cache): the reduction, the conversions and the
+// Bound by instructions in the 8-bit types (39 us for 16381 tokens of 8 heads, 0.41 of
+// the copy rate, 2.7 of 4 issued a cycle; 25 and 0.82 to a bf16 cache): the reduction, the conversions and the
 // border test.  A CTA takes kTokens tokens; a head row (head_dim / 16 items of neighbouring
 // threads, 4 or 8) is reduced by shuffles.
 template <int XT, int TYPE, int kTokens>
@@ -389,7 +389,7 @@ struct ReadParams {
 };
 constexpr int kReadTokens = 16;  // tokens of one CTA: a divisor of every page size, so one page
 
-// Bound by bytes: 25 sequences of up to 8192 tokens from int8 to bf16 132 us, 0.95
+// Bound by bytes: 25 sequences of up to 8192 tokens from int8 to bf16 129 us, 0.97
 // of the copy rate.  Neighbouring threads take items of a row, then heads of a token (the output's
 // rows are contiguous over both), then tokens, then K and V; four items a thread
 // at a time, all loaded before the first is stored.
