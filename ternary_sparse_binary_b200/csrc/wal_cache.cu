@@ -385,11 +385,12 @@ struct ReadParams {
   const int32_t* start;
   int64_t ld_table;
   int n_heads, head_dim, shift, n_pages, max_len, T;
+  int halves;  // K and V, or the one that is wanted in the first place
   int32_t* status;
 };
 constexpr int kReadTokens = 16;  // tokens of one CTA: a divisor of every page size, so one page
 
-// Bound by bytes: 25 sequences of up to 8192 tokens from int8 to bf16 129 us, 0.97
+// Bound by bytes: 25 sequences of up to 8192 tokens from int8 to bf16 128 us, 0.98
 // of the copy rate.  Neighbouring threads take items of a row, then heads of a token (the output's
 // rows are contiguous over both), then tokens, then K and V; four items a thread
 // at a time, all loaded before the first is stored.
@@ -407,18 +408,15 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   const bool bad = (uint32_t)page >= (uint32_t)p.n_pages;
   if (bad && threadIdx.x == 0 && p.status) atomicExch(p.status, (int32_t)WAL_ERR_ARG);
   const int off = j0 & ((1 << p.shift) - 1);
-  // a NULL output's half of the cache is left alone
-  const int items = p.head_dim / 16, per = p.n_heads * items, all = (p.out[0] && p.out[1] ? 2 : 1) * n * per;
-  const int first = p.out[0] ? 0 : 1;
+  const int items = p.head_dim / 16, per = p.n_heads * items, all = p.halves * n * per;
   const int64_t row0 = (((int64_t)(bad ? 0 : page) * p.n_heads) << p.shift) + off;  // head 0, token j0
   struct Place {
     int which, j, h, it;
   };
   auto place = [&](int q) {
     Place x;
-    const int second = q >= n * per;
-    const int r = q - second * n * per;
-    x.which = first + second;
+    x.which = q >= n * per;
+    const int r = q - x.which * n * per;
     x.j = r / per;
     const int e = r - x.j * per;
     x.h = e / items;
@@ -625,6 +623,13 @@ extern "C" int wal_kv_read(const wal_kv_cache* cache, const int32_t* table, int 
   p.scale[0] = cache->k_scale; p.scale[1] = cache->v_scale;
   p.out[0] = K; p.out[1] = V;
   p.ld[0] = ldk; p.ld[1] = ldv;
+  p.halves = K && V ? 2 : 1;
+  if (!K) {
+    p.cache[0] = p.cache[1];
+    p.scale[0] = p.scale[1];
+    p.out[0] = p.out[1];
+    p.ld[0] = p.ld[1];
+  }
   p.table = table;
   p.start = start;
   p.ld_table = ld_table;

@@ -257,7 +257,7 @@ def test_other_device_values_and_streams():
 def test_reading_one_half_moves_one_half(typ):
     """With a NULL K or V the other one is read as ever, in half the time."""
     w = wal()
-    B, L, heads, D, page = 16, 4096, 8, 128, 64
+    B, L, heads, D, page = 96, 4096, 8, 128, 64
     cache = w.KvCache.empty(B * L // page, page, heads, D, dtype=TYPES[typ])
     for t in (cache.k, cache.v):
         t.view(torch.uint8).random_(0, 0x40)
