@@ -396,7 +396,7 @@ int wal_int3_embed(const wal_int3_table* t, const int32_t* ids, int M, float* ou
  *
  * The device waits of the attention kernels are bounded, as everywhere.  One that
  * gives up makes the rows that are left without a result NaN, with or without a
- * workspace, and records WAL_ERR_TIMEOUT, before which an index value gives way. */
+ * workspace, and records WAL_ERR_TIMEOUT, which an index value does not overwrite. */
 enum { WAL_F32 = 0, WAL_BF16 = 1 };                       /* element types of activations */
 enum { WAL_ROPE_HALF = 0, WAL_ROPE_INTERLEAVED = 1 };     /* which columns make a pair */
 enum { WAL_SCALING_NONE = 0, WAL_SCALING_LINEAR = 1, WAL_SCALING_PARTS = 2 };
