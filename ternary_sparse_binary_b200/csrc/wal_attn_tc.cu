@@ -715,7 +715,7 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, int most, int t) {
 }
 
 // Rows of half t in the CTA's pieces after the first `done`, which a wait that gave
-// up has cut off: NaN, so that the loss shows whoever reads the status word.
+// up has cut off: NaN, so that the loss shows even if nobody reads the status word.
 template <int D, int TYPE>
 __device__ __noinline__ void lose_rows(const AttnParams& p, int most, int t, uint32_t done) {
   const int tid = threadIdx.x & 127;
