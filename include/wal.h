@@ -536,6 +536,68 @@ int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int
                     int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B, int max_len,
                     float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes, wal_stream_t stream);
 
+/* ---- a serving step over long contexts ------------------------------------------
+ * Plans of pages and rows, and norms of q and k heads with the rotation and the cache
+ * in one launch.  Conventions as in the section before. */
+
+/* The plan of a step: B sequences, of which sequence b holds kv_len[b] tokens in the
+ * pages of its table row, get n_new[b] tokens more (n_new[b] < 0: their last -n_new[b]
+ * tokens are dropped, as rejected drafts are, or a finished request's: all of them).
+ * Everything is device memory that the device alone reads and writes, so a captured
+ * step replays with what the step before it left.
+ *   Pages: a dropped sequence gives the pages that hold no token of it any more back:
+ * they go on top of the list free_pages[0 .. n_free[0]) ([n_pages] entries of room), in
+ * the order of the sequences and of their tokens.  Then each growing sequence takes the
+ * pages it lacks from the top of the list, in the same order, into its table row.
+ *   Rows: q_start [B + 1] are the sums of the new tokens; row q_start[b] + i has the
+ * position kv_len[b] + i and the slot of its page and offset (as wal_kv_append wants
+ * them); rows from q_start[B] to T - 1 get position 0 and slot -1, which skips them.
+ *   Afterwards kv_len_out[b] = kv_len[b] + n_new[b] and n_free_out[0] is the length of
+ * the list; both may be written in place.  Other arrays must not overlap.
+ * A sequence with kv_len or kv_len + n_new outside [0, max_kv] is left out: it keeps its
+ * length and gets no rows.  If rows (T) or pages run short, so are the first growing
+ * sequence that finds too little and all growing ones after it; dropped tokens and their
+ * pages go through.  If n_free is outside [0, n_pages], or the list would become longer
+ * than that, all are left out.  A page id outside [0, n_pages) moves as it is, and the
+ * rows in that page get the slot -1.  All of these record WAL_ERR_ARG.  Pages that
+ * several sequences hold are given back once for each: whoever shares pages drops tokens
+ * down to the shared ones only.
+ * 1 <= B <= 65535, T < 2^31 - 1, 1 <= max_kv <= 2^30, ceil(max_kv / page_size) <=
+ * ld_table.  The cache's pages are not touched.  ws: NULL, or at least 512 bytes.
+ * Asynchronous. */
+int wal_kv_plan(const wal_kv_cache* cache, const int32_t* n_new, const int32_t* kv_len, int B, int32_t* table, int ld_table,
+                int max_kv, int32_t* free_pages, const int32_t* n_free, int T, int32_t* q_start, int32_t* positions,
+                int32_t* slots, int32_t* kv_len_out, int32_t* n_free_out, void* ws, size_t ws_bytes, wal_stream_t stream);
+
+/* Norms of q and k heads: y = x w / sqrt(mean(x^2) + eps) over the head_dim columns of
+ * each head, in fp32, with a weight for each column that all q (or k) heads share. */
+typedef struct wal_head_norm {
+  int32_t head_dim;
+  int32_t type;          /* of the weights: WAL_F32 or WAL_BF16 */
+  float eps;             /* > 0 */
+  const void* q_weight;  /* device [head_dim], 4-byte aligned */
+  const void* k_weight;
+} wal_head_norm;
+
+/* Yq[t][h] = rotate(norm(Q[t][h]), positions[t]), and Yk the same of K, in one launch:
+ * T >= 0 rows of n_heads and n_kv_heads heads (at most 65536 each), fp32 or bf16 (x_type)
+ * to bf16, rounded once.  norm NULL: the rotation alone.  Yq may be Q itself (and Yk K)
+ * when the type is bf16 and the row strides are equal; any other overlap is not allowed.
+ * Asynchronous. */
+int wal_qk_norm_rope(const wal_head_norm* norm, const wal_rope_plan* rope, const void* Q, const void* K, int x_type, int T,
+                     int n_heads, int n_kv_heads, int ldq, int ldk, const int32_t* positions, uint16_t* Yq, int ldyq,
+                     uint16_t* Yk, int ldyk, wal_stream_t stream);
+
+/* The same, with K's heads and V's stored in the cache as wal_kv_append stores them:
+ * K after its norm and rotation, V as it is; n_heads q heads go to Yq (bf16).  A row
+ * whose slot is -1 (or out of range) has its Yq written all the same.  norm or rope may
+ * be NULL to leave it out (positions are then not looked at without rope).
+ * ws: NULL, or at least 512 bytes.  Asynchronous. */
+int wal_qkv_append(const wal_kv_cache* cache, const wal_head_norm* norm, const wal_rope_plan* rope, const void* Q,
+                   const void* K, const void* V, int in_type, int T, int n_heads, int ldq, int ldk, int ldv,
+                   const int32_t* slots, const int32_t* positions, uint16_t* Yq, int ldy, void* ws, size_t ws_bytes,
+                   wal_stream_t stream);
+
 const char* wal_status_string(int status);
 const char* wal_last_error(void);
 

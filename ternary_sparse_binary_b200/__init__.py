@@ -23,7 +23,8 @@ from ._abi import (  # noqa: F401
     WAL_KV_BF16, WAL_KV_INT8, WAL_KV_E4M3, wal_rope_plan, wal_kv_cache,
     wal_rope_freqs, wal_rope, wal_kv_cache_sizes, wal_kv_append, wal_kv_read,
     wal_attn_paged_workspace_bytes, wal_attn_paged, wal_attn_prompt, wal_debug_wait_polls,
+    wal_head_norm, wal_kv_plan, wal_qk_norm_rope, wal_qkv_append,
 )
 from .packed import PackedMatrix, Pq2Matrix, Rc1Matrix, pack_host, pack_pq2_host, to_device, BodyPass  # noqa: F401
 from . import attention  # noqa: F401
-from .attention import Rope, KvCache, attn_prompt  # noqa: F401
+from .attention import Rope, HeadNorm, KvCache, attn_prompt  # noqa: F401

@@ -38,6 +38,7 @@ EXPORTED_SYMBOLS = [
     "wal_int4_gemm", "wal_int3_embed",
     "wal_rope_freqs", "wal_rope", "wal_kv_cache_sizes", "wal_kv_append", "wal_kv_read",
     "wal_attn_paged_workspace_bytes", "wal_attn_paged", "wal_attn_prompt", "wal_debug_wait_polls",
+    "wal_kv_plan", "wal_qk_norm_rope", "wal_qkv_append",
     "wal_status_string", "wal_last_error",
 ]
 
@@ -81,6 +82,11 @@ class wal_kv_cache(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class wal_head_norm(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
 
 
 def _load():
@@ -157,6 +163,10 @@ lib.wal_attn_paged_workspace_bytes.argtypes = [_CP, _i, _i, _i, _i, _i]
 lib.wal_attn_paged_workspace_bytes.restype = _sz
 lib.wal_attn_paged.argtypes = [_CP, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
 lib.wal_attn_prompt.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
+_NP = ctypes.POINTER(wal_head_norm)
+lib.wal_kv_plan.argtypes = [_CP, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.wal_qk_norm_rope.argtypes = [_NP, _OP, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _i, _vp]
+lib.wal_qkv_append.argtypes = [_CP, _NP, _OP, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _sz, _vp]
 lib.wal_debug_wait_polls.argtypes = [_i]
 lib.wal_status_string.argtypes = [_i]
 lib.wal_status_string.restype = ctypes.c_char_p
@@ -406,6 +416,29 @@ def wal_attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, st
                     ws_bytes, stream):
     return _check(lib.wal_attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len,
                                       scale, O, ldo, ws, ws_bytes, stream), "wal_attn_prompt")
+
+
+def _ref(desc):
+    return ctypes.byref(desc) if desc is not None else None
+
+
+def wal_kv_plan(cache, n_new, kv_len, B, table, ld_table, max_kv, free_pages, n_free, T, q_start, positions, slots,
+                kv_len_out, n_free_out, ws, ws_bytes, stream):
+    return _check(lib.wal_kv_plan(ctypes.byref(cache), n_new, kv_len, B, table, ld_table, max_kv, free_pages, n_free, T,
+                                  q_start, positions, slots, kv_len_out, n_free_out, ws, ws_bytes, stream), "wal_kv_plan")
+
+
+def wal_qk_norm_rope(norm, rope, Q, K, x_type, T, n_heads, n_kv_heads, ldq, ldk, positions, Yq, ldyq, Yk, ldyk, stream):
+    """norm: a wal_head_norm, or None for the rotation alone."""
+    return _check(lib.wal_qk_norm_rope(_ref(norm), ctypes.byref(rope), Q, K, x_type, T, n_heads, n_kv_heads, ldq, ldk,
+                                       positions, Yq, ldyq, Yk, ldyk, stream), "wal_qk_norm_rope")
+
+
+def wal_qkv_append(cache, norm, rope, Q, K, V, in_type, T, n_heads, ldq, ldk, ldv, slots, positions, Yq, ldy, ws,
+                   ws_bytes, stream):
+    """norm: a wal_head_norm or None; rope: a wal_rope_plan or None."""
+    return _check(lib.wal_qkv_append(ctypes.byref(cache), _ref(norm), _ref(rope), Q, K, V, in_type, T, n_heads, ldq, ldk,
+                                     ldv, slots, positions, Yq, ldy, ws, ws_bytes, stream), "wal_qkv_append")
 
 
 def wal_debug_wait_polls(polls):

@@ -18,7 +18,7 @@ import math
 import torch
 
 from . import _abi
-from ._abi import wal_kv_cache, wal_rope_plan
+from ._abi import wal_head_norm, wal_kv_cache, wal_rope_plan
 
 _LAYOUTS = {"half": _abi.WAL_ROPE_HALF, "interleaved": _abi.WAL_ROPE_INTERLEAVED}
 _SCALINGS = {"none": _abi.WAL_SCALING_NONE, "linear": _abi.WAL_SCALING_LINEAR, "parts": _abi.WAL_SCALING_PARTS}
@@ -115,6 +115,38 @@ class Rope:
                           _index(positions, "positions", T), out.data_ptr(), ldo, s)
 
 
+    def apply_qk(self, q, k, positions, q_out, k_out, norm=None, stream=None):
+        """q_out and k_out (bf16) = q and k (fp32 or bf16), each head normalised by `norm` (a HeadNorm) and
+        rotated, [tokens, heads * head_dim]; a bf16 input may be its own output."""
+        xt, ldq, T, wq = _rows(q, "q")
+        kt, ldk, Tk, wk = _rows(k, "k")
+        _, ldyq, *q_shape = _rows(q_out, "q_out", _BF16)
+        _, ldyk, *k_shape = _rows(k_out, "k_out", _BF16)
+        if kt != xt or Tk != T or q_shape != [T, wq] or k_shape != [T, wk] or wq % self.head_dim or wk % self.head_dim:
+            raise ValueError("q and k: [tokens, heads * head_dim] of one type, q_out and k_out of the same shapes")
+        guard, s = _enter(stream, q, k, positions, q_out, k_out, self.freq, *_norm(norm))
+        with guard:
+            _abi.wal_qk_norm_rope(None if norm is None else norm.desc, self.desc, q.data_ptr(), k.data_ptr(), xt, T,
+                                  wq // self.head_dim, wk // self.head_dim, ldq, ldk, _index(positions, "positions", T),
+                                  q_out.data_ptr(), ldyq, k_out.data_ptr(), ldyk, s)
+
+
+class HeadNorm:
+    """Weights of the q and k heads' norms, [head_dim] of float32 or bfloat16, plus their wal_head_norm descriptor."""
+
+    def __init__(self, q_weight, k_weight, eps=1e-6):
+        kind = _X_TYPES.get(q_weight.dtype)
+        for w in (q_weight, k_weight):
+            if kind is None or w.dtype != q_weight.dtype or w.dim() != 1 or w.shape != q_weight.shape or not w.is_contiguous():
+                raise ValueError("q_weight and k_weight: contiguous vectors [head_dim] of float32 or bfloat16")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        self.desc = wal_head_norm(q_weight.numel(), kind, eps, q_weight.data_ptr(), k_weight.data_ptr())
+
+
+def _norm(norm):
+    return () if norm is None else (norm.q_weight, norm.k_weight)
+
+
 class KvCache:
     """A paged KV cache: k and v [pages, heads, page_size, head_dim] (bf16,
     int8 or float8_e4m3fn) and, for the 8-bit types, fp32 scales [pages, heads,
@@ -167,6 +199,46 @@ class KvCache:
             _abi.wal_kv_append(self.desc, k.data_ptr(), v.data_ptr(), kt, T, ldk, ldv, _index(slots, "slots", T),
                                None if rope is None else _index(positions, "positions", T),
                                None if rope is None else rope.desc, wp, wn, s)
+
+    def append_qkv(self, q, k, v, slots, q_out, positions=None, rope=None, norm=None, ws=None, stream=None):
+        """append() of k and v with each head of k normalised by `norm` (a HeadNorm) before its rotation, and
+        q_out (bf16) = q [tokens, n_heads * head_dim] with the same done to it, in one launch."""
+        xt, ldq, T, wq = _rows(q, "q")
+        kt, ldk, *k_shape = _rows(k, "k")
+        vt, ldv, *v_shape = _rows(v, "v")
+        _, ldy, *q_shape = _rows(q_out, "q_out", _BF16)
+        if kt != xt or vt != xt or k_shape != [T, self.n_heads * self.head_dim] or v_shape != k_shape:
+            raise ValueError("q, k and v: [tokens, heads * head_dim] of one type")
+        if q_shape != [T, wq] or wq % self.head_dim:
+            raise ValueError("q and q_out: [tokens, n_heads * head_dim]")
+        if rope is not None and positions is None:
+            raise ValueError("positions are required with a rope")
+        turned = () if rope is None else (positions, rope.freq)
+        guard, s = _enter(stream, self.k, q, k, v, slots, q_out, *turned, *_norm(norm))
+        wp, wn = _ws(ws, q)
+        with guard:
+            _abi.wal_qkv_append(self.desc, None if norm is None else norm.desc, None if rope is None else rope.desc,
+                                q.data_ptr(), k.data_ptr(), v.data_ptr(), xt, T, wq // self.head_dim, ldq, ldk, ldv,
+                                _index(slots, "slots", T), None if rope is None else _index(positions, "positions", T),
+                                q_out.data_ptr(), ldy, wp, wn, s)
+
+    def plan(self, n_new, kv_len, table, free, n_free, q_start, positions, slots, kv_len_out=None, n_free_out=None,
+             max_kv=None, ws=None, stream=None):
+        """The plan of a step in which sequence b gets n_new[b] tokens more (or loses -n_new[b]): its pages go from
+        the list `free` [n_pages] of n_free[0] pages to its row of `table`, or back; q_start, and position and slot of
+        every row of the step, are written, and the new lengths (in place without kv_len_out and n_free_out)."""
+        B, T = n_new.numel(), slots.numel()
+        most = table.shape[-1] * self.page_size if max_kv is None else _fits(max_kv, "max_kv")
+        tp, ldt = _table(table, B, most, self.page_size)
+        kv_len_out = kv_len if kv_len_out is None else kv_len_out
+        n_free_out = n_free if n_free_out is None else n_free_out
+        guard, s = _enter(stream, self.k, n_new, kv_len, table, free, n_free, q_start, positions, slots, kv_len_out, n_free_out)
+        wp, wn = _ws(ws, slots)
+        with guard:
+            _abi.wal_kv_plan(self.desc, _index(n_new, "n_new"), _index(kv_len, "kv_len", B), B, tp, ldt, min(most, 2 ** 30),
+                             _index(free, "free", self.n_pages), _index(n_free, "n_free", 1), T,
+                             _index(q_start, "q_start", B + 1), _index(positions, "positions", T), _index(slots, "slots", T),
+                             _index(kv_len_out, "kv_len_out", B), _index(n_free_out, "n_free_out", 1), wp, wn, s)
 
     def read(self, table, start, k_out, v_out, max_len, ws=None, stream=None):
         """Rows start[b] .. start[b + 1] - 1 of k_out and v_out (fp32 or bf16) = the first tokens of sequence b."""
