@@ -537,8 +537,9 @@ int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int
                     float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes, wal_stream_t stream);
 
 /* ---- a serving step over long contexts ------------------------------------------
- * Plans of pages and rows, and norms of q and k heads with the rotation and the cache
- * in one launch.  Conventions as in the section before. */
+ * Plans of pages and rows, norms of q and k heads with the rotation and the cache in
+ * one launch, attention that sees a window, and attention of sequences that share
+ * their first tokens.  Conventions as in the section before. */
 
 /* The plan of a step: B sequences, of which sequence b holds kv_len[b] tokens in the
  * pages of its table row, get n_new[b] tokens more (n_new[b] < 0: their last -n_new[b]
@@ -597,6 +598,44 @@ int wal_qkv_append(const wal_kv_cache* cache, const wal_head_norm* norm, const w
                    const void* K, const void* V, int in_type, int T, int n_heads, int ldq, int ldk, int ldv,
                    const int32_t* slots, const int32_t* positions, uint16_t* Yq, int ldy, void* ws, size_t ws_bytes,
                    wal_stream_t stream);
+
+/* wal_attn_paged and wal_attn_prompt where a token sees the last `window` keys up to its
+ * own and the first `sinks` of its sequence: of the keys j < u that it would see without a
+ * window, those with j >= u - window or j < sinks.  window >= 1, sinks >= 0.  All else as
+ * there; table entries of pages that no new token of the call sees are not looked at, so
+ * such pages may be gone. */
+size_t wal_attn_paged_window_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q, int max_kv,
+                                             int window, int sinks);
+int wal_attn_paged_window(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
+                          const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,
+                          int max_q, int max_kv, int window, int sinks, float scale, uint16_t* O, int ldo, void* ws,
+                          size_t ws_bytes, wal_stream_t stream);
+int wal_attn_prompt_window(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
+                           int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B, int max_len,
+                           int window, int sinks, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
+                           wal_stream_t stream);
+
+/* wal_attn_paged for sequences that share their first tokens (a system prompt, samples of
+ * one request): group g is the sequences group_start[g] .. group_start[g + 1] - 1 (int32
+ * [G + 1], not falling), whose first prefix_len[g] tokens are the same.  Their keys and
+ * values are read once for the whole group, from the table row of its first sequence; of
+ * the other rows only the pages from the prefix's end on are looked at (a prefix need not
+ * end with a page).  kv_len counts the shared tokens too.  Sequences of no group, before
+ * group_start[0] or from group_start[G] on, share nothing.
+ * Bounds: max_kv of kv_len, max_prefix >= 0 of prefix_len, max_own >= 1 of the tokens
+ * behind the prefix; ceil(max_kv / page_size) <= ld_table; 1 <= G <= 65535.
+ * A sequence whose new tokens are not all behind its group's prefix, that breaks a bound,
+ * or whose rows do not lie within its group's, is left out like one of wal_attn_paged;
+ * so are all of a group whose start values fall or leave [0, B] or whose prefix_len is
+ * outside [0, max_prefix].  Rows of a group's sequences follow one another in Q.  The
+ * workspace is required when T > 0. */
+size_t wal_attn_paged_shared_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int G, int max_q,
+                                             int max_prefix, int max_own);
+int wal_attn_paged_shared(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
+                          const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,
+                          const int32_t* group_start, const int32_t* prefix_len, int G, int max_q, int max_kv,
+                          int max_prefix, int max_own, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
+                          wal_stream_t stream);
 
 const char* wal_status_string(int status);
 const char* wal_last_error(void);

@@ -56,3 +56,24 @@ def head_norm(x, w, eps):
     """x [.., D] over its root mean square, times w [D]."""
     x = np.asarray(x, np.float64)
     return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(w, np.float64)
+
+
+def window_sees(n, L, window, sinks):
+    """[n, L]: which of L keys each of the last n tokens sees, with a window and first keys that stay visible."""
+    up = (L - n + 1 + np.arange(n))[:, None]
+    j = np.arange(L)
+    return (j < up) & ((j >= up - window) | (j < sinks))
+
+
+def attend(q, k, v, scale, group, sees):
+    """q [n, heads, D] over k and v [L, kv_heads, D], row i over the keys sees[i].  Returns (o, a) as attn_oracle.attend."""
+    n, heads, D = q.shape
+    o, a = np.zeros((n, heads, D)), np.zeros((n, heads, D))
+    some = sees.any(1) if len(k) else np.zeros(n, bool)
+    for h in range(heads):
+        s = np.where(sees, q[:, h] @ k[:, h // group].T * scale, -np.inf)[some]
+        w = np.exp(s - s.max(1, keepdims=True, initial=-np.inf))
+        w /= w.sum(1, keepdims=True)
+        o[some, h] = w @ v[:, h // group]
+        a[some, h] = w @ np.abs(v[:, h // group])
+    return o, a

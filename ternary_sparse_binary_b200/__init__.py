@@ -24,6 +24,8 @@ from ._abi import (  # noqa: F401
     wal_rope_freqs, wal_rope, wal_kv_cache_sizes, wal_kv_append, wal_kv_read,
     wal_attn_paged_workspace_bytes, wal_attn_paged, wal_attn_prompt, wal_debug_wait_polls,
     wal_head_norm, wal_kv_plan, wal_qk_norm_rope, wal_qkv_append,
+    wal_attn_paged_window_workspace_bytes, wal_attn_paged_window, wal_attn_prompt_window,
+    wal_attn_paged_shared_workspace_bytes, wal_attn_paged_shared,
 )
 from .packed import PackedMatrix, Pq2Matrix, Rc1Matrix, pack_host, pack_pq2_host, to_device, BodyPass  # noqa: F401
 from . import attention  # noqa: F401

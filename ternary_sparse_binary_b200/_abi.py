@@ -39,6 +39,8 @@ EXPORTED_SYMBOLS = [
     "wal_rope_freqs", "wal_rope", "wal_kv_cache_sizes", "wal_kv_append", "wal_kv_read",
     "wal_attn_paged_workspace_bytes", "wal_attn_paged", "wal_attn_prompt", "wal_debug_wait_polls",
     "wal_kv_plan", "wal_qk_norm_rope", "wal_qkv_append",
+    "wal_attn_paged_window_workspace_bytes", "wal_attn_paged_window", "wal_attn_prompt_window",
+    "wal_attn_paged_shared_workspace_bytes", "wal_attn_paged_shared",
     "wal_status_string", "wal_last_error",
 ]
 
@@ -167,6 +169,13 @@ _NP = ctypes.POINTER(wal_head_norm)
 lib.wal_kv_plan.argtypes = [_CP, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 lib.wal_qk_norm_rope.argtypes = [_NP, _OP, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _i, _vp]
 lib.wal_qkv_append.argtypes = [_CP, _NP, _OP, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _sz, _vp]
+lib.wal_attn_paged_window_workspace_bytes.argtypes = [_CP] + [_i] * 7
+lib.wal_attn_paged_window_workspace_bytes.restype = _sz
+lib.wal_attn_paged_window.argtypes = [_CP, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
+lib.wal_attn_prompt_window.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
+lib.wal_attn_paged_shared_workspace_bytes.argtypes = [_CP] + [_i] * 7
+lib.wal_attn_paged_shared_workspace_bytes.restype = _sz
+lib.wal_attn_paged_shared.argtypes = [_CP, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _sz, _vp]
 lib.wal_debug_wait_polls.argtypes = [_i]
 lib.wal_status_string.argtypes = [_i]
 lib.wal_status_string.restype = ctypes.c_char_p
@@ -439,6 +448,36 @@ def wal_qkv_append(cache, norm, rope, Q, K, V, in_type, T, n_heads, ldq, ldk, ld
     """norm: a wal_head_norm or None; rope: a wal_rope_plan or None."""
     return _check(lib.wal_qkv_append(ctypes.byref(cache), _ref(norm), _ref(rope), Q, K, V, in_type, T, n_heads, ldq, ldk,
                                      ldv, slots, positions, Yq, ldy, ws, ws_bytes, stream), "wal_qkv_append")
+
+
+def wal_attn_paged_window_workspace_bytes(cache, n_heads, T, B, max_q, max_kv, window, sinks):
+    return int(lib.wal_attn_paged_window_workspace_bytes(ctypes.byref(cache), n_heads, T, B, max_q, max_kv, window, sinks))
+
+
+def wal_attn_paged_window(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, window, sinks,
+                          scale, O, ldo, ws, ws_bytes, stream):
+    return _check(lib.wal_attn_paged_window(ctypes.byref(cache), Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B,
+                                            max_q, max_kv, window, sinks, scale, O, ldo, ws, ws_bytes, stream),
+                  "wal_attn_paged_window")
+
+
+def wal_attn_prompt_window(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len, window, sinks,
+                           scale, O, ldo, ws, ws_bytes, stream):
+    return _check(lib.wal_attn_prompt_window(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len,
+                                             window, sinks, scale, O, ldo, ws, ws_bytes, stream),
+                  "wal_attn_prompt_window")
+
+
+def wal_attn_paged_shared_workspace_bytes(cache, n_heads, T, B, G, max_q, max_prefix, max_own):
+    return int(lib.wal_attn_paged_shared_workspace_bytes(ctypes.byref(cache), n_heads, T, B, G, max_q, max_prefix,
+                                                         max_own))
+
+
+def wal_attn_paged_shared(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, group_start, prefix_len, G,
+                          max_q, max_kv, max_prefix, max_own, scale, O, ldo, ws, ws_bytes, stream):
+    return _check(lib.wal_attn_paged_shared(ctypes.byref(cache), Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B,
+                                            group_start, prefix_len, G, max_q, max_kv, max_prefix, max_own, scale, O, ldo,
+                                            ws, ws_bytes, stream), "wal_attn_paged_shared")
 
 
 def wal_debug_wait_polls(polls):

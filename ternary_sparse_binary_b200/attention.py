@@ -82,6 +82,17 @@ def _ws(ws, like):
     return ws.data_ptr(), ws.numel()
 
 
+def _scratch(n, like, stream):
+    with _HERE if stream is None else torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=like.device)
+
+
+def _window(window, sinks):
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    return min(window, _INT), min(sinks, _INT)  # beyond any sequence either way
+
+
 def status(ws, stream=None):
     """Raise WalError if the last call that was given this workspace recorded one (synchronises the stream)."""
     if _ws(ws, ws)[1] < 512:
@@ -256,44 +267,79 @@ class KvCache:
             _abi.wal_kv_read(self.desc, tp, ldt, _index(start, "start"), B, max_len, k_out.data_ptr(),
                              v_out.data_ptr(), kt, T, ldk, ldv, wp, wn, s)
 
-    def attend_workspace_bytes(self, n_heads, T, B, max_q, max_kv):
-        """Bytes of a `ws` for attend.  Not monotone: a smaller batch may need more (its keys are split
-        further), so one `ws` for several shapes takes the largest of their sizes."""
-        shape = (n_heads, T, B, max_q, max_kv)
-        n = self._scratch.get(shape)
+    def _bytes(self, fn, *shape):
+        """Workspace size of a recent shape."""
+        n = self._scratch.get((fn, *shape))
         if n is None:
             _fits(max(shape), "workspace size")
             if len(self._scratch) >= 256:
                 self._scratch.clear()
-            n = self._scratch[shape] = _abi.wal_attn_paged_workspace_bytes(self.desc, n_heads, T, B, max_q, max_kv)
+            n = self._scratch[(fn, *shape)] = fn(self.desc, *shape)
         return n
 
-    def attend(self, q, q_start, kv_len, table, out, max_q, max_kv, scale=None, ws=None, stream=None):
+    def attend_workspace_bytes(self, n_heads, T, B, max_q, max_kv, window=None, sinks=0):
+        """Bytes of a `ws` for attend.  Not monotone: a smaller batch may need more (its keys are split
+        further), so one `ws` for several shapes takes the largest of their sizes."""
+        if window is None:
+            return self._bytes(_abi.wal_attn_paged_workspace_bytes, n_heads, T, B, max_q, max_kv)
+        return self._bytes(_abi.wal_attn_paged_window_workspace_bytes, n_heads, T, B, max_q, max_kv, *_window(window, sinks))
+
+    def attend(self, q, q_start, kv_len, table, out, max_q, max_kv, scale=None, ws=None, stream=None, window=None, sinks=0):
         """out (bf16) = attention of the new tokens' q (bf16) [tokens, n_heads * head_dim] over the cache;
-        rows q_start[b] .. q_start[b + 1] - 1 are the last tokens of sequence b's kv_len[b]."""
+        rows q_start[b] .. q_start[b + 1] - 1 are the last tokens of sequence b's kv_len[b].  With a
+        `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence."""
+        ldq, ldo, T, n_heads = self._tokens(q, out)
+        B = kv_len.numel()
+        _fits(max_q, "max_q")
+        seen = () if window is None else _window(window, sinks)
+        tp, ldt = _table(table, B, max_kv, self.page_size)
+        guard, s = _enter(stream, self.k, q, q_start, kv_len, table, out)
+        if ws is None:
+            n = self.attend_workspace_bytes(n_heads, T, B, max_q, max_kv, window, sinks)  # 0: the call below says what is wrong
+            ws = _scratch(n, q, stream) if n > 512 else None
+        wp, wn = _ws(ws, q)
+        call = _abi.wal_attn_paged if window is None else _abi.wal_attn_paged_window
+        with guard:
+            call(self.desc, q.data_ptr(), n_heads, T, ldq, _index(q_start, "q_start", B + 1), _index(kv_len, "kv_len"), tp, ldt,
+                 B, max_q, max_kv, *seen, self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo, wp, wn, s)
+
+    def attend_shared_workspace_bytes(self, n_heads, T, B, G, max_q, max_prefix, max_own):
+        """Bytes of a `ws` for attend_shared; not monotone, as attend's."""
+        return self._bytes(_abi.wal_attn_paged_shared_workspace_bytes, n_heads, T, B, G, max_q, max_prefix, max_own)
+
+    def attend_shared(self, q, q_start, kv_len, table, group_start, prefix_len, out, max_q, max_kv, max_prefix, max_own,
+                      scale=None, ws=None, stream=None):
+        """attend() of sequences that share their first tokens: group g is the sequences group_start[g] ..
+        group_start[g + 1] - 1, whose first prefix_len[g] tokens (at most max_prefix) are read once, from the
+        pages of the first of them; max_own bounds the tokens behind."""
+        ldq, ldo, T, n_heads = self._tokens(q, out)
+        B, G = kv_len.numel(), prefix_len.numel()
+        _fits(max(max_q, max_prefix, max_own), "bounds")
+        tp, ldt = _table(table, B, max_kv, self.page_size)
+        guard, s = _enter(stream, self.k, q, q_start, kv_len, table, group_start, prefix_len, out)
+        if ws is None:
+            n = self.attend_shared_workspace_bytes(n_heads, T, B, G, max_q, max_prefix, max_own)
+            ws = _scratch(n, q, stream) if n > 512 else None
+        wp, wn = _ws(ws, q)
+        with guard:
+            _abi.wal_attn_paged_shared(self.desc, q.data_ptr(), n_heads, T, ldq, _index(q_start, "q_start", B + 1),
+                                       _index(kv_len, "kv_len"), tp, ldt, B, _index(group_start, "group_start", G + 1),
+                                       _index(prefix_len, "prefix_len"), G, max_q, max_kv, max_prefix, max_own,
+                                       self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo, wp, wn, s)
+
+    def _tokens(self, q, out):
+        """(row strides of q and out, tokens, q heads)"""
         _, ldq, T, width = _rows(q, "q", _BF16)
         _, ldo, *shape = _rows(out, "out", _BF16)
         if shape != [T, width] or width % self.head_dim:
             raise ValueError("q and out: [tokens, n_heads * head_dim]")
-        B, n_heads = kv_len.numel(), width // self.head_dim
-        _fits(max_q, "max_q")
-        tp, ldt = _table(table, B, max_kv, self.page_size)
-        guard, s = _enter(stream, self.k, q, q_start, kv_len, table, out)
-        if ws is None:
-            n = self.attend_workspace_bytes(n_heads, T, B, max_q, max_kv)  # 0: the call below says what is wrong
-            if n > 512:
-                with _HERE if stream is None else torch.cuda.stream(stream):
-                    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-        wp, wn = _ws(ws, q)
-        with guard:
-            _abi.wal_attn_paged(self.desc, q.data_ptr(), n_heads, T, ldq, _index(q_start, "q_start", B + 1),
-                                _index(kv_len, "kv_len"), tp, ldt, B, max_q, max_kv,
-                                self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo, wp, wn, s)
+        return ldq, ldo, T, width // self.head_dim
 
 
-def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, stream=None):
+def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, stream=None, window=None, sinks=0):
     """out (bf16) = causal attention over packed prompts; q and out [tokens, n_heads * head_dim],
-    k and v [tokens, n_kv_heads * head_dim], sequence b in rows start[b] .. start[b + 1] - 1."""
+    k and v [tokens, n_kv_heads * head_dim], sequence b in rows start[b] .. start[b + 1] - 1.  With a
+    `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence."""
     _, ldq, T, width = _rows(q, "q", _BF16)
     _, ldk, *k_shape = _rows(k, "k", _BF16)
     _, ldv, *v_shape = _rows(v, "v", _BF16)
@@ -301,9 +347,11 @@ def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, str
     if shape != [T, width] or k_shape != v_shape or k_shape[0] != T or width % head_dim or k_shape[1] % head_dim:
         raise ValueError("q and out: [tokens, n_heads * head_dim]; k and v: [tokens, n_kv_heads * head_dim]")
     _fits(max_len, "max_len")
+    seen = () if window is None else _window(window, sinks)
     guard, s = _enter(stream, q, k, v, start, out)
     wp, wn = _ws(ws, q)
+    call = _abi.wal_attn_prompt if window is None else _abi.wal_attn_prompt_window
     with guard:
-        _abi.wal_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), width // head_dim, k_shape[1] // head_dim,
-                             head_dim, T, ldq, ldk, ldv, _index(start, "start"), start.numel() - 1, max_len,
-                             1.0 / math.sqrt(head_dim) if scale is None else scale, out.data_ptr(), ldo, wp, wn, s)
+        call(q.data_ptr(), k.data_ptr(), v.data_ptr(), width // head_dim, k_shape[1] // head_dim, head_dim, T, ldq, ldk, ldv,
+             _index(start, "start"), start.numel() - 1, max_len, *seen, 1.0 / math.sqrt(head_dim) if scale is None else scale,
+             out.data_ptr(), ldo, wp, wn, s)

@@ -20,7 +20,7 @@ constexpr int kRowWarps = 4;
 
 // Divide, round and store a row held by a warp.  A row that came out as NaN
 // beside a non-finite V which it does not see is done again from its own keys.
-template <int D>
+template <int D, bool GEN>
 __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s, int b, int head, int tok, const float* acc,
                                            float l) {
   constexpr int VPL = D / 32;
@@ -33,10 +33,17 @@ __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s
     nan |= y[i] != y[i];
   }
   if (__any_sync(0xffffffffu, nan && l == l)) {
-    const int h = head / p.group, reach = attn_reach(p, s, tok * p.group + head - h * p.group);
+    const int h = head / p.group, row = tok * p.group + head - h * p.group, reach = attn_reach(p, s, row);
     if (lim < reach && attn_last_nonfinite<D>(p, s, b, h, lim, reach) >= 0) {
-      attend_row<D>(p, s, b, head, tok);
+      attend_row<D, GEN>(p, s, b, head, tok);
       return;
+    }
+    if (GEN) {
+      const int from = attn_from(p, s, row), low = attn_low(p, s, lim);
+      if (from < low && attn_last_nonfinite<D>(p, s, b, h, from, low) >= 0) {
+        attend_row<D, GEN>(p, s, b, head, tok);
+        return;
+      }
     }
   }
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + (s.q0 + tok) * p.ldo + head * D + lane * VPL);
@@ -110,8 +117,8 @@ __device__ __forceinline__ float lg2(float x) {
 }
 constexpr float kDecLazy = 4.f;
 
-template <int D, int TYPE, int NT, int MT>
-__global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1 ? 3 : 2) attn_decode_kernel(const __grid_constant__ AttnParams p) {
+template <int D, int TYPE, int NT, int MT, bool GEN>
+__device__ __forceinline__ void attn_decode(const AttnParams& p) {
   constexpr bool CODES = TYPE != WAL_KV_BF16;
   constexpr int KB = CODES ? 1 : 2;      // bytes of a code
   constexpr int W = D * KB / 16;         // 32-bit words of K per lane and key (of 4 lanes)
@@ -123,16 +130,23 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const AttnSeq s = attn_seq(p, b);
+  const AttnSeq s = attn_seq<GEN>(p, b);
   if (p.clear) {
-    if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
+    if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0 && !(GEN && p.part_first)) *p.status = 0;
   } else if (s.bad && h == 0 && threadIdx.x == 0 && p.status) {
     attn_report(p.status);
   }
   if (s.bad) return;
   const int rows = s.n_q * p.group;
-  const int k0 = split * p.split_keys, k1 = min(s.len, k0 + p.split_keys);
+  const int tab = GEN ? s.tab : b;
+  AttnSpan span = {};
+  if (GEN && rows) span = attn_span(p, s, attn_limit<GEN>(p, s, 0), attn_limit<GEN>(p, s, s.n_q - 1));
+  const int sinks16 = GEN ? attn_sinks16(p) : 0;
+  const int k0 = split * p.split_keys, k1 = min(GEN ? span.n : s.len, k0 + p.split_keys);
   if (rows == 0 || (k0 >= k1 && split > 0)) return;  // split 0 also answers for a sequence without keys
+  // key of place v (the same without GEN), and whether some row sees it
+  auto key = [&](int v) { return GEN ? attn_key(v, sinks16, span.delta) : v; };
+  auto seen = [&](int v, int j) { return v < k1 && (!GEN || j >= span.low || j < p.sinks); };
 
   // K and V of a step, and where they lie: a tile of 16 keys is in one page
   uint32_t kw[MT][2][W], vw[MT][4][NW];
@@ -140,7 +154,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
   int64_t row[MT];
   auto find = [&](int j0) {
 #pragma unroll
-    for (int u = 0; u < MT; ++u) row[u] = j0 + 16 * u < k1 ? attn_page_row(p, b, h, j0 + 16 * u) : 0;
+    for (int u = 0; u < MT; ++u) row[u] = j0 + 16 * u < k1 ? attn_page_row(p, tab, h, key(j0 + 16 * u)) : 0;
   };
   auto load_k = [&](int j0) {
     const uint8_t* base = static_cast<const uint8_t*>(p.k);
@@ -149,7 +163,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = g + 8 * e;
-        const bool live = j0 + 16 * u + j < k1;
+        const bool live = seen(j0 + 16 * u + j, key(j0 + 16 * u) + j);
         const uint8_t* src = base + (row[u] + j) * (D * KB) + 16 * c;
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = 2 * c + (e & 1) + 8 * (e >> 1);
-        const bool live = j0 + 16 * u + j < k1;
+        const bool live = seen(j0 + 16 * u + j, key(j0 + 16 * u) + j);
         const uint8_t* src = base + (row[u] + j) * (D * KB);
         if (NW >= 4) {
 #pragma unroll
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
       }
       if (CODES)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) vs[u][e] = j0 + 16 * u + g + 8 * e < k1 ? __ldg(p.vs + row[u] + g + 8 * e) : 0.f;
+        for (int e = 0; e < 2; ++e) vs[u][e] = seen(j0 + 16 * u + g + 8 * e, key(j0 + 16 * u) + g + 8 * e) ? __ldg(p.vs + row[u] + g + 8 * e) : 0.f;
     }
   };
   int j0 = k0 + warp * STEP;
@@ -237,11 +251,13 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * t + 2 * c + e;
-      lim[t][e] = r < rows ? attn_limit(s, r / p.group) : s.len;
+      lim[t][e] = r < rows ? attn_limit<GEN>(p, s, r / p.group) : s.len;
       m[t][e] = m2[t][e] = -INFINITY;
       l[t][e] = 0.f;
     }
-  const int lim_min = min(k1, attn_limit(s, 0));
+  // places that every row sees end at lim_min and, but for the first keys, begin at low_max
+  const int lim_min = min(k1, attn_limit<GEN>(p, s, 0) - span.delta);
+  const int low_max = GEN ? attn_low(p, s, attn_limit<GEN>(p, s, s.n_q - 1)) - span.delta : 0;
   float o[DT][NT][4];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -289,15 +305,20 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
             if (CODES) x *= ks[u][r];
           }
       }
-    if (j0 + STEP > lim_min) {  // keys a row does not see get -inf
+    if (j0 + STEP > lim_min || (GEN && j0 < low_max)) {  // keys a row does not see get -inf
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int j = j0 + 16 * u + g + 8 * (e >> 1);
-            if (j >= min(k1, lim[t][e & 1])) sc[u][t][e] = -INFINITY;
+            const int v = j0 + 16 * u + g + 8 * (e >> 1);
+            if (GEN) {
+              const int j = key(j0 + 16 * u) + g + 8 * (e >> 1), up = lim[t][e & 1];
+              if (v >= k1 || j >= up || (j < attn_low(p, s, up) && j >= p.sinks)) sc[u][t][e] = -INFINITY;
+            } else if (v >= min(k1, lim[t][e & 1])) {
+              sc[u][t][e] = -INFINITY;
+            }
           }
     }
     // the next step's K, in the registers of this one's
@@ -450,8 +471,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
       for (int i = 0; i < VPL; ++i) acc[i] += f * s_o[w][r][lane * VPL + i];
     }
     const int tok = r / p.group, head = h * p.group + r % p.group;
-    if (p.n_split > 1) {
-      const int64_t pr = (int64_t)split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
+    if (p.n_split > 1 || (GEN && p.phase)) {
+      const int64_t pr = (int64_t)((GEN ? p.part_first : 0) + split) * p.T * p.n_heads + attn_part_row(p, s, tok, head);
       float* dst = p.part_o + pr * D + lane * VPL;
       if (VPL == 4)
         *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[VPL - 2], acc[VPL - 1]);
@@ -459,36 +480,62 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
         *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
       if (lane == 0) p.part_ml[pr] = make_float2(mm, ll);
     } else {
-      finish_row<D>(p, s, b, head, tok, acc, ll);
+      finish_row<D, GEN>(p, s, tab, head, tok, acc, ll);
     }
   }
+}
+// The second launch of a shared call starts beside the first.  Its first CTA waits for
+// that, so that what comes after the second comes after both.
+__device__ __forceinline__ void after_prefix(const AttnParams& p) {
+  if (p.part_first && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <int D, int TYPE, int NT, int MT, bool GEN>
+__global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1 ? 3 : 2) attn_decode_kernel(const __grid_constant__ AttnParams p) {
+  attn_decode<D, TYPE, NT, MT, GEN>(p);
+  if (GEN) after_prefix(p);
 }
 
 // Add the splits of a row, and report index values out of range.  PER warps of
 // the CTA share a row, each its splits in order, joined in order: one where
 // there are few splits, four where a warp alone would wait for one load after
 // the other.
-template <int D, int PER>
+template <int D, int PER, bool GEN>
 __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __grid_constant__ AttnParams p) {
   constexpr int VPL = D / 32;
   __shared__ float s_o[PER > 1 ? kRowWarps : 1][D];
   __shared__ float s_l[PER > 1 ? kRowWarps : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const AttnSeq s = attn_seq(p, b);
+  const AttnSeq s = attn_seq<GEN>(p, b);
   if (blockIdx.x == 0) {  // the first kernel cleared the status word; what it skipped is reported here
     bool bad = s.bad;
     const int pages = (s.len + (1 << p.shift) - 1) >> p.shift;
-    for (int i = threadIdx.x; i < pages; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + b * p.ld_table + i) >= (uint32_t)p.n_pages;
+    auto look = [&](int row, int from, int to) {
+      for (int i = from + threadIdx.x; i < to; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + row * p.ld_table + i) >= (uint32_t)p.n_pages;
+    };
+    if (!GEN) {
+      look(b, 0, pages);
+    } else if (s.n_q > 0) {  // the pages of keys that some row sees
+      const int low = attn_low(p, s, attn_limit(s, 0)), first = p.phase == kOwn ? s.lo : min(p.sinks, s.len);
+      look(s.head, 0, (first + (1 << p.shift) - 1) >> p.shift);
+      look(b, low >> p.shift, pages);
+    }
     if (bad) attn_report(p.status);
   }
   const int row = blockIdx.x * (kRowWarps / PER) + warp / PER;  // (token, head)
   if (s.bad || row >= s.n_q * p.n_heads) return;                // PER > 1: the whole CTA
   const int tok = row / p.n_heads, head = row - tok * p.n_heads;
-  const int n = max(1, (s.len + p.split_keys - 1) / p.split_keys);
+  int n = max(1, (s.len + p.split_keys - 1) / p.split_keys);
+  int prefix = 0, gap = 0;  // splits of the prefix, and those it might have had before the others
+  if (GEN) {
+    prefix = p.phase == kOwn ? (s.lo + p.prefix_keys - 1) / p.prefix_keys : 0;
+    gap = p.part_first - prefix;
+    n = prefix + attn_splits(p, s);
+  }
   const int64_t pr = attn_part_row(p, s, tok, head), stride = (int64_t)p.T * p.n_heads;
+  auto part = [&](int i) { return pr + (GEN && i >= prefix ? i + gap : i) * stride; };
   float mm = -INFINITY;
-  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[pr + i * stride].x);
+  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[part(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
   const float ref = mm == -INFINITY ? 0.f : mm;
@@ -497,8 +544,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
 #pragma unroll 4
   for (int i = warp % PER; i < n; i += PER) {
-    const float2 ml = p.part_ml[pr + i * stride];
-    const float* src = p.part_o + (pr + i * stride) * D + lane * VPL;
+    const float2 ml = p.part_ml[part(i)];
+    const float* src = p.part_o + part(i) * D + lane * VPL;
     float v[VPL];
 #pragma unroll
     for (int k = 0; k < VPL; ++k) v[k] = src[k];
@@ -524,7 +571,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
       for (int k = 0; k < VPL; ++k) acc[k] += s_o[i][lane * VPL + k];
     }
   }
-  finish_row<D>(p, s, b, head, tok, acc, ll);
+  finish_row<D, GEN>(p, s, b, head, tok, acc, ll);
 }
 
 // Longest sequence: the kernels add a split or a step to a key's number in 32 bits.
@@ -566,18 +613,37 @@ int launched(cudaError_t e, const char* what) {
 // fits three CTAs on an SM (25 sequences, 16384 keys: 133 us against 136 with two
 // tiles and two CTAs); codes take two and fit two CTAs (int8, 32768 keys: 181 us,
 // 189 squeezed into three, 203 with one tile).
-template <int D, int TYPE>
-void launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
+template <int D, int TYPE, bool GEN>
+cudaError_t launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
   constexpr int MT = TYPE == WAL_KV_BF16 ? 1 : 2;
-  if (p.max_q * p.group <= 8)
-    attn_decode_kernel<D, TYPE, 1, MT><<<grid, 32 * kDecWarps, 0, s>>>(p);
-  else
-    attn_decode_kernel<D, TYPE, 2, MT><<<grid, 32 * kDecWarps, 0, s>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kDecWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (GEN && p.part_first) {  // beside the prefix's launch
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  if (p.max_q * p.group <= 8) return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, TYPE, 1, MT, GEN>, p);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, TYPE, 2, MT, GEN>, p);
+}
+template <bool GEN>
+cudaError_t launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
+  const bool wide = p.head_dim == 128;
+  switch (p.type) {
+    case WAL_KV_BF16: return wide ? launch_decode<128, WAL_KV_BF16, GEN>(p, grid, s) : launch_decode<64, WAL_KV_BF16, GEN>(p, grid, s);
+    case WAL_KV_INT8: return wide ? launch_decode<128, WAL_KV_INT8, GEN>(p, grid, s) : launch_decode<64, WAL_KV_INT8, GEN>(p, grid, s);
+    default: return wide ? launch_decode<128, WAL_KV_E4M3, GEN>(p, grid, s) : launch_decode<64, WAL_KV_E4M3, GEN>(p, grid, s);
+  }
 }
 
+template <bool GEN>
 int launch_combine(const AttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const bool shared = p.n_split > 6;
+  const bool shared = p.n_split + p.part_first > 6;
   const int rows = shared ? 1 : kRowWarps;  // of a CTA
   cfg.gridDim = dim3((unsigned)(((int64_t)p.max_q * p.n_heads + rows - 1) / rows), 1, (unsigned)p.B);
   cfg.blockDim = dim3(32 * kRowWarps);
@@ -589,9 +655,9 @@ int launch_combine(const AttnParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   cudaError_t e;
   if (p.head_dim == 64)
-    e = shared ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4>, p) : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 1>, p);
+    e = shared ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 4, GEN>, p) : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 1, GEN>, p);
   else
-    e = shared ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4>, p) : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 1>, p);
+    e = shared ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 4, GEN>, p) : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 1, GEN>, p);
   return launched(e, "attn_combine_kernel");
 }
 
@@ -656,65 +722,52 @@ void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int
 // Set by wal_debug_wait_polls: the limit of the device waits of later calls; below 0, the usual one.
 std::atomic<int> g_wait_polls{-1};
 
-int launch_attn(AttnParams& p, cudaStream_t stream) {
+// The attention itself, and the sum over splits.
+int launch_pieces(AttnParams& p, cudaStream_t stream) {
   const int polls = g_wait_polls.load();
   p.polls = polls < 0 ? (int)ptx::kSpinLimit : polls;
-  if (!p.table || (int64_t)p.max_q * p.group > kDecMaxRows) {
-    const int st = launch_attn_tc(p, stream);
-    return st || p.n_split == 1 ? st : launch_combine(p, stream);
-  }
+  p.tc = !p.table || (int64_t)p.max_q * p.group > kDecMaxRows;
+  if (p.tc) return launch_attn_tc(p, stream);
   const dim3 grid((unsigned)p.n_split, (unsigned)p.n_kv_heads, (unsigned)p.B);
-  const bool wide = p.head_dim == 128;
-  switch (p.type) {
-    case WAL_KV_BF16: wide ? launch_decode<128, WAL_KV_BF16>(p, grid, stream) : launch_decode<64, WAL_KV_BF16>(p, grid, stream); break;
-    case WAL_KV_INT8: wide ? launch_decode<128, WAL_KV_INT8>(p, grid, stream) : launch_decode<64, WAL_KV_INT8>(p, grid, stream); break;
-    default: wide ? launch_decode<128, WAL_KV_E4M3>(p, grid, stream) : launch_decode<64, WAL_KV_E4M3>(p, grid, stream); break;
-  }
-  const int st = launched(cudaGetLastError(), "attn_decode_kernel");
-  return st || p.n_split == 1 ? st : launch_combine(p, stream);
+  return launched(p.gen ? launch_decode<true>(p, grid, stream) : launch_decode<false>(p, grid, stream), "attn_decode_kernel");
+}
+int launch_attn(AttnParams& p, cudaStream_t stream) {
+  const int st = launch_pieces(p, stream);
+  if (st || (p.n_split == 1 && !p.phase)) return st;
+  return p.gen ? launch_combine<true>(p, stream) : launch_combine<false>(p, stream);
 }
 
-}  // namespace
-
-}  // namespace wal
-
-using namespace wal;
-
-extern "C" int wal_debug_wait_polls(int polls) { return g_wait_polls.exchange(polls < 0 ? -1 : polls); }
-
-extern "C" size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q,
-                                                 int max_kv) {
-  if (check_cache(cache) != WAL_OK) return 0;
-  if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, 1.f) != WAL_OK) return 0;
-  int n_split, split_keys;
-  plan_split(*cache, n_heads, T, B, max_q, max_kv, &n_split, &split_keys);
-  return attn_ws_bytes(n_split, T, n_heads, cache->head_dim);
+// Window of a call, as its kernels take it: the general ones only where it hides something.
+struct Window {
+  bool gen;
+  int window, sinks;
+};
+int check_window(int window, int sinks) {
+  if (window < 1 || sinks < 0) return fail(WAL_ERR_SHAPE, "window must be >= 1 and sinks >= 0");
+  return WAL_OK;
+}
+Window window_of(int window, int sinks, int max_kv) {
+  if (window >= max_kv || sinks >= max_kv) return {false, kNoWindow, 0};
+  return {true, window, sinks};
+}
+// Keys in one run of a page (of a prompt's rows): 16 where the first keys come before the window's in a tile.
+int gran_of(int page_size, int sinks) { return sinks ? 16 : page_size ? std::min(page_size, 128) : 1; }
+int piece_toks(int group) { return (kTcAttnRows - 1) / group + 2; }
+// Most places of a piece's keys.
+int most_keys(const Window& w, int gran, int group, int max_q, int max_kv) {
+  if (!w.gen) return max_kv;
+  return (int)std::min<int64_t>(max_kv, (int64_t)w.window + std::min(max_q, piece_toks(group)) + (int64_t)align_up((size_t)w.sinks, 16) + gran);
+}
+void set_window(AttnParams& p, const Window& w, int gran) {
+  p.gen = w.gen;
+  p.window = w.window; p.sinks = w.sinks;
+  p.gran = gran;
+  p.piece_toks = std::min(p.max_q, piece_toks(p.group));
 }
 
-extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
-                              const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table,
-                              int B, int max_q, int max_kv, float scale, uint16_t* O, int ldo, void* ws,
-                              size_t ws_bytes, wal_stream_t stream) {
-  int st = check_cache(cache);
-  if (st) return st;
-  if ((st = check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, scale))) return st;
-  const int64_t width = (int64_t)n_heads * cache->head_dim;
-  if ((st = check_bf16_rows(Q, ldq, width, T > 0, "Q")) || (st = check_bf16_rows(O, ldo, width, T > 0, "O"))) return st;
-  if (!q_start || !kv_len || !table || misaligned(q_start, 4) || misaligned(kv_len, 4) || misaligned(table, 4))
-    return fail(WAL_ERR_ARG, "q_start, kv_len and table are required, 4-byte aligned");
-  if ((int64_t)ld_table * cache->page_size < max_kv) return fail(WAL_ERR_ARG, "ld_table pages must cover max_kv tokens");
-  int dev = 0;
-  AttnParams p = {};
-  cudaStream_t s = (cudaStream_t)stream;
-  plan_split(*cache, n_heads, T, B, max_q, max_kv, &p.n_split, &p.split_keys);
-  if ((ws || p.n_split > 1) && (!ws || ws_bytes < attn_ws_bytes(p.n_split, T, n_heads, cache->head_dim)))
-    return fail(WAL_ERR_WORKSPACE, "workspace too small");
-  if ((st = current_device(&dev))) return st;
-  p.clear = p.n_split > 1;
-  p.status = status_word(ws);
-  if (T > 0 && O == Q) return fail(WAL_ERR_ARG, "O must not be Q: rows are read again after others are written");
-  if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
-  if (T == 0) return WAL_OK;
+// The cache and the new tokens of a call.
+void set_paged(AttnParams& p, const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq, const int32_t* q_start,
+               const int32_t* kv_len, const int32_t* table, int ld_table, int B, int max_q, int max_kv, float scale, uint16_t* O, int ldo) {
   p.Q = Q; p.O = O;
   p.k = cache->k; p.v = cache->v;
   p.ks = cache->k_scale; p.vs = cache->v_scale;
@@ -725,16 +778,52 @@ extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int 
   p.shift = log2_of(cache->page_size); p.n_pages = cache->n_pages;
   p.T = T; p.B = B; p.max_q = max_q < T ? max_q : T; p.max_kv = max_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
+}
+void set_parts(AttnParams& p, int n_split) {
   char* part = reinterpret_cast<char*>(p.status) + 256;
   p.part_ml = reinterpret_cast<float2*>(part);
-  p.part_o = reinterpret_cast<float*>(part + align_up((size_t)p.n_split * T * n_heads * 8, 256));
+  p.part_o = reinterpret_cast<float*>(part + align_up((size_t)n_split * p.T * p.n_heads * 8, 256));
+}
+int check_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq, const int32_t* q_start, const int32_t* kv_len,
+                const int32_t* table, int ld_table, int B, int max_q, int max_kv, float scale, const uint16_t* O, int ldo) {
+  int st = check_cache(cache);
+  if (st) return st;
+  if ((st = check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, scale))) return st;
+  const int64_t width = (int64_t)n_heads * cache->head_dim;
+  if ((st = check_bf16_rows(Q, ldq, width, T > 0, "Q")) || (st = check_bf16_rows(O, ldo, width, T > 0, "O"))) return st;
+  if (!q_start || !kv_len || !table || misaligned(q_start, 4) || misaligned(kv_len, 4) || misaligned(table, 4))
+    return fail(WAL_ERR_ARG, "q_start, kv_len and table are required, 4-byte aligned");
+  if ((int64_t)ld_table * cache->page_size < max_kv) return fail(WAL_ERR_ARG, "ld_table pages must cover max_kv tokens");
+  return WAL_OK;
+}
+
+int attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq, const int32_t* q_start, const int32_t* kv_len,
+               const int32_t* table, int ld_table, int B, int max_q, int max_kv, const Window& w, float scale, uint16_t* O, int ldo,
+               void* ws, size_t ws_bytes, wal_stream_t stream) {
+  int st = check_paged(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo);
+  if (st) return st;
+  int dev = 0;
+  AttnParams p = {};
+  cudaStream_t s = (cudaStream_t)stream;
+  const int gran = gran_of(cache->page_size, w.sinks);
+  plan_split(*cache, n_heads, T, B, max_q, most_keys(w, gran, n_heads / cache->n_heads, max_q, max_kv), &p.n_split, &p.split_keys);
+  if ((ws || p.n_split > 1) && (!ws || ws_bytes < attn_ws_bytes(p.n_split, T, n_heads, cache->head_dim)))
+    return fail(WAL_ERR_WORKSPACE, "workspace too small");
+  if ((st = current_device(&dev))) return st;
+  p.clear = p.n_split > 1;
+  p.status = status_word(ws);
+  if (T > 0 && O == Q) return fail(WAL_ERR_ARG, "O must not be Q: rows are read again after others are written");
+  if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
+  if (T == 0) return WAL_OK;
+  set_paged(p, cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo);
+  set_window(p, w, gran);
+  set_parts(p, p.n_split);
   return launch_attn(p, s);
 }
 
-extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
-                               int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B,
-                               int max_len, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
-                               wal_stream_t stream) {
+int attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads, int head_dim, int T, int ldq,
+                int ldk, int ldv, const int32_t* start, int B, int max_len, const Window& w, float scale, uint16_t* O, int ldo, void* ws,
+                size_t ws_bytes, wal_stream_t stream) {
   int st = check_attn(n_heads, n_kv_heads, head_dim, T, B, max_len, std::max(1, std::min(max_len, T)), scale);
   if (st) return st;
   const int64_t width = (int64_t)n_heads * head_dim, kv_width = (int64_t)n_kv_heads * head_dim;
@@ -760,5 +849,138 @@ extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint1
   p.T = T; p.B = B; p.max_q = p.max_kv = max_len < T ? max_len : T;
   p.n_split = 1; p.split_keys = p.max_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
+  set_window(p, w, gran_of(0, w.sinks));
+  return launch_attn(p, s);
+}
+
+// Splits of a shared call's two launches.  The prefix's rows are the groups' tokens, of which only T is known.
+struct SharedPlan {
+  int prefix, prefix_keys, own, own_keys;
+};
+SharedPlan plan_shared(const wal_kv_cache& c, int n_heads, int T, int B, int G, int max_q, int max_prefix, int max_own) {
+  SharedPlan r = {};
+  if (max_prefix) plan_split(c, n_heads, T, G, std::max(1, T), max_prefix, &r.prefix, &r.prefix_keys);
+  const int most = std::min(max_own + gran_of(c.page_size, 0) - 1, kMaxKeys);  // whole runs from where the prefix ends
+  plan_split(c, n_heads, T, B, max_q, most, &r.own, &r.own_keys);
+  return r;
+}
+size_t shared_ws_bytes(const SharedPlan& r, int T, int n_heads, int head_dim) {
+  return T ? attn_ws_bytes(std::max(2, r.prefix + r.own), T, n_heads, head_dim) : kStatusWs;
+}
+int check_shared(int G, int max_prefix, int max_own) {
+  if (G < 1 || G > 65535 || max_prefix < 0 || max_own < 1) return fail(WAL_ERR_SHAPE, "1 <= G <= 65535, max_prefix >= 0 and max_own >= 1");
+  if (max_prefix > kMaxKeys || max_own > kMaxKeys) return fail(WAL_ERR_UNSUPPORTED, "at most 2^30 tokens a sequence");
+  return WAL_OK;
+}
+
+}  // namespace
+}  // namespace wal
+
+using namespace wal;
+
+extern "C" int wal_debug_wait_polls(int polls) { return g_wait_polls.exchange(polls < 0 ? -1 : polls); }
+
+extern "C" size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q,
+                                                 int max_kv) {
+  if (check_cache(cache) != WAL_OK) return 0;
+  if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, 1.f) != WAL_OK) return 0;
+  int n_split, split_keys;
+  plan_split(*cache, n_heads, T, B, max_q, max_kv, &n_split, &split_keys);
+  return attn_ws_bytes(n_split, T, n_heads, cache->head_dim);
+}
+
+extern "C" int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
+                              const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table,
+                              int B, int max_q, int max_kv, float scale, uint16_t* O, int ldo, void* ws,
+                              size_t ws_bytes, wal_stream_t stream) {
+  return attn_paged(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, {false, kNoWindow, 0}, scale, O, ldo,
+                    ws, ws_bytes, stream);
+}
+
+extern "C" int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
+                               int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B,
+                               int max_len, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
+                               wal_stream_t stream) {
+  return attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len, {false, kNoWindow, 0}, scale, O, ldo, ws,
+                     ws_bytes, stream);
+}
+
+extern "C" size_t wal_attn_paged_window_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int max_q, int max_kv,
+                                                        int window, int sinks) {
+  if (check_cache(cache) != WAL_OK || check_window(window, sinks) != WAL_OK) return 0;
+  if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, 1.f) != WAL_OK) return 0;
+  const Window w = window_of(window, sinks, max_kv);
+  int n_split, split_keys;
+  plan_split(*cache, n_heads, T, B, max_q, most_keys(w, gran_of(cache->page_size, w.sinks), n_heads / cache->n_heads, max_q, max_kv),
+             &n_split, &split_keys);
+  return attn_ws_bytes(n_split, T, n_heads, cache->head_dim);
+}
+
+extern "C" int wal_attn_paged_window(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
+                                     const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,
+                                     int max_q, int max_kv, int window, int sinks, float scale, uint16_t* O, int ldo, void* ws,
+                                     size_t ws_bytes, wal_stream_t stream) {
+  const int st = check_window(window, sinks);
+  if (st) return st;
+  return attn_paged(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, window_of(window, sinks, max_kv), scale,
+                    O, ldo, ws, ws_bytes, stream);
+}
+
+extern "C" int wal_attn_prompt_window(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_heads, int n_kv_heads,
+                                      int head_dim, int T, int ldq, int ldk, int ldv, const int32_t* start, int B, int max_len,
+                                      int window, int sinks, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
+                                      wal_stream_t stream) {
+  const int st = check_window(window, sinks);
+  if (st) return st;
+  return attn_prompt(Q, K, V, n_heads, n_kv_heads, head_dim, T, ldq, ldk, ldv, start, B, max_len,
+                     window_of(window, sinks, std::min(max_len, std::max(T, 1))), scale, O, ldo, ws, ws_bytes, stream);
+}
+
+extern "C" size_t wal_attn_paged_shared_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int G, int max_q,
+                                                        int max_prefix, int max_own) {
+  if (check_cache(cache) != WAL_OK || check_shared(G, max_prefix, max_own) != WAL_OK) return 0;
+  if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, std::max(max_own, max_prefix), 1.f) != WAL_OK) return 0;
+  if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, G, std::max(T, 1), std::max(max_own, max_prefix), 1.f) != WAL_OK) return 0;
+  return shared_ws_bytes(plan_shared(*cache, n_heads, T, B, G, max_q, max_prefix, max_own), T, n_heads, cache->head_dim);
+}
+
+extern "C" int wal_attn_paged_shared(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
+                                     const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,
+                                     const int32_t* group_start, const int32_t* prefix_len, int G, int max_q, int max_kv,
+                                     int max_prefix, int max_own, float scale, uint16_t* O, int ldo, void* ws, size_t ws_bytes,
+                                     wal_stream_t stream) {
+  int st = check_paged(cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo);
+  if (st || (st = check_shared(G, max_prefix, max_own))) return st;
+  if ((st = check_attn(n_heads, cache->n_heads, cache->head_dim, T, G, std::max(T, 1), max_kv, scale))) return st;
+  if (max_prefix > max_kv) return fail(WAL_ERR_SHAPE, "max_prefix is at most max_kv");
+  if (!group_start || !prefix_len || misaligned(group_start, 4) || misaligned(prefix_len, 4))
+    return fail(WAL_ERR_ARG, "group_start and prefix_len are required, 4-byte aligned");
+  const SharedPlan r = plan_shared(*cache, n_heads, T, B, G, max_q, max_prefix, max_own);
+  if ((ws || T > 0) && (!ws || ws_bytes < shared_ws_bytes(r, T, n_heads, cache->head_dim))) return fail(WAL_ERR_WORKSPACE, "workspace too small");
+  int dev = 0;
+  if ((st = current_device(&dev))) return st;
+  AttnParams p = {};
+  cudaStream_t s = (cudaStream_t)stream;
+  if (T == 0) return clear_status(ws, s, &p.status);
+  if (O == Q) return fail(WAL_ERR_ARG, "O must not be Q: rows are read again after others are written");
+  p.status = status_word(ws);
+  p.clear = true;
+  set_paged(p, cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo);
+  set_window(p, {true, kNoWindow, 0}, gran_of(cache->page_size, 0));
+  set_parts(p, r.prefix + r.own);
+  p.group_start = group_start; p.prefix_len = prefix_len;
+  p.n_groups = G; p.n_seqs = B;
+  p.max_prefix = max_prefix; p.max_own = max_own;
+  if (r.prefix) {
+    AttnParams first = p;
+    first.phase = kPrefix;
+    first.B = G;
+    first.max_q = T;
+    first.n_split = r.prefix; first.split_keys = r.prefix_keys;
+    if ((st = launch_pieces(first, s))) return st;
+  }
+  p.phase = kOwn;
+  p.n_split = r.own; p.split_keys = r.own_keys;
+  p.part_first = r.prefix; p.prefix_keys = std::max(1, r.prefix_keys);
   return launch_attn(p, s);
 }

@@ -33,7 +33,21 @@ struct AttnParams {
   int n_split, split_keys;
   float* part_o;             // n_split > 1: [n_split][T * n_heads][head_dim], sums of w v
   float2* part_ml;           // [n_split][T * n_heads]: {m, l}, m in units of log2
+  // The general kernels (GEN): a window, or a shared prefix, whose keys one launch
+  // takes (kPrefix, its "sequences" being the groups) and what is behind it another
+  // (kOwn), each leaving partial results, the second from split part_first on.
+  bool gen, tc;              // tc: the tensor-core kernel
+  int window, sinks;         // a row sees its last `window` keys and the first `sinks`
+  int gran;                  // keys of a piece are looked up in runs of this many, aligned where there are pages
+  int piece_toks;            // new tokens of a piece of the tensor-core kernel at most
+  int phase;
+  int part_first, prefix_keys;  // kOwn: the prefix has part_first splits at most, of prefix_keys keys
+  const int32_t* group_start;
+  const int32_t* prefix_len;
+  int n_groups, n_seqs, max_prefix, max_own;
 };
+enum { kAll = 0, kPrefix = 1, kOwn = 2 };  // phase
+constexpr int kNoWindow = 1 << 30;
 
 // The tensor-core kernel (wal_attn_tc.cu).
 constexpr int kTcAttnRows = 256;  // query rows of one CTA there
@@ -46,13 +60,65 @@ __device__ __forceinline__ void attn_report(int32_t* status) { atomicCAS(status,
 struct AttnSeq {
   int q0, n_q, len;
   bool bad;
+  int tab;       // GEN: its row of the page table,
+  int lo, head;  // how many keys it shares (kOwn takes those from there on), and the table row of these
 };
+// Group g of a shared call: its sequences [first, last), their rows [q0, q1), the keys they share; false if out of range.
+struct AttnGroup {
+  int first, last, q0, q1, keys;
+};
+__device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup& r) {
+  r.first = p.group_start[g];
+  r.last = p.group_start[g + 1];
+  r.keys = p.prefix_len[g];
+  if (r.first < 0 || r.last < r.first || r.last > p.n_seqs || r.keys < 0 || r.keys > p.max_prefix) return false;
+  r.q0 = p.q_start[r.first];
+  r.q1 = p.q_start[r.last];
+  return r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.T;
+}
+template <bool GEN = false>
 __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
-  const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
   AttnSeq s = {0, 0, 0, true};
+  if (GEN) {
+    s.tab = s.head = b;
+    s.lo = 0;
+    if (p.phase == kPrefix) {
+      AttnGroup g;
+      if (!attn_group(p, b, g)) return s;
+      s.tab = g.first;
+      s.q0 = g.q0;
+      s.n_q = g.keys ? g.q1 - g.q0 : 0;
+      s.len = g.keys;
+      s.bad = false;
+      return s;
+    }
+  }
+  const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
   if (q0 < 0 || q1 < q0 || q1 > p.T || q1 - q0 > p.max_q) return s;
   const int len = p.kv_len ? p.kv_len[b] : q1 - q0;
   if (len < 0 || len > p.max_kv) return s;
+  if (GEN && p.phase == kOwn) {
+    int g = 0, end = p.n_groups;  // the last group that starts at b or before
+    while (end - g > 1) {
+      const int mid = (g + end) >> 1;
+      if (p.group_start[mid] <= b) g = mid; else end = mid;
+    }
+    AttnGroup r;
+    if (p.group_start[g] <= b) {
+      if (!attn_group(p, g, r)) return s;
+      if (b < r.last) {
+        if (q0 < r.q0 || q1 > r.q1) return s;
+        s.lo = r.keys;
+        s.head = r.first;
+      } else if (g != p.n_groups - 1) {
+        return s;
+      }
+    }
+    if (len - (q1 - q0) < s.lo || len - s.lo > p.max_own) {
+      s.lo = 0;
+      return s;
+    }
+  }
   s.q0 = q0;
   s.n_q = q1 - q0;
   s.len = len;
@@ -61,6 +127,44 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
 }
 // Keys that new token i sees: the first attn_limit(s, i) of the sequence.
 __device__ __forceinline__ int attn_limit(const AttnSeq& s, int i) { return max(0, s.len - s.n_q + i + 1); }
+// GEN: it sees keys j below that with j >= attn_low or j < sinks (and, in a shared call, the shared ones).
+template <bool GEN>
+__device__ __forceinline__ int attn_limit(const AttnParams& p, const AttnSeq& s, int i) {
+  return GEN && p.phase == kPrefix ? s.len : attn_limit(s, i);
+}
+__device__ __forceinline__ int attn_low(const AttnParams& p, const AttnSeq& s, int limit) { return max(s.lo, limit - p.window); }
+
+// The keys of a piece whose rows have limits from `first` to `last`, counted
+// without the gap between the first keys and the window: place v is key v below
+// sinks16 and key v + delta from there on.  Keys [low, ..) and [0, sinks) count, the
+// other places up to n are there for the alignment.  With a gap (delta > 0), every row
+// of the piece sees all of the first keys.
+struct AttnSpan {
+  int low, delta, n;
+};
+__device__ __forceinline__ int attn_sinks16(const AttnParams& p) { return (p.sinks + 15) & ~15; }
+__device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, const AttnSeq& s, int first, int last) {
+  AttnSpan a;
+  a.low = attn_low(p, s, first);
+  const int before = a.low - attn_sinks16(p);
+  a.delta = before > 0 ? before & -p.gran : 0;
+  a.n = max(0, last - a.delta);
+  return a;
+}
+__device__ __forceinline__ int attn_key(int v, int sinks16, int delta) { return v < sinks16 ? v : v + delta; }
+// Splits that the keys of a sequence have in this launch (of one that has rows).  Of the
+// tensor-core kernel's pieces this is a bound: those beyond a piece's keys are empty.
+__device__ __forceinline__ int attn_splits(const AttnParams& p, const AttnSeq& s) {
+  if (p.n_split == 1) return 1;
+  int n;
+  if (p.tc) {
+    const int64_t most = (int64_t)p.window + p.piece_toks + attn_sinks16(p) + p.gran;
+    n = (int)min((int64_t)(s.len - (s.lo & -p.gran)), most);
+  } else {
+    n = attn_span(p, s, attn_limit<true>(p, s, 0), attn_limit<true>(p, s, s.n_q - 1)).n;
+  }
+  return max(1, (n + p.split_keys - 1) / p.split_keys);
+}
 
 // Page of key j; an id out of range is recorded and page 0 read in its place.
 __device__ __forceinline__ int attn_page(const AttnParams& p, int b, int j) {
@@ -88,6 +192,10 @@ __device__ __forceinline__ int64_t attn_part_row(const AttnParams& p, const Attn
 // kernel's are fewer than that altogether).
 __device__ __forceinline__ int attn_reach(const AttnParams& p, const AttnSeq& s, int row) {
   return attn_limit(s, min(row | (kTcAttnRows - 1), s.n_q * p.group - 1) / p.group);
+}
+// With a window, the keys below the row's own that other rows of its piece see hide there too: from here on.
+__device__ __forceinline__ int attn_from(const AttnParams& p, const AttnSeq& s, int row) {
+  return attn_low(p, s, attn_limit(s, (row & ~(kTcAttnRows - 1)) / p.group));
 }
 // The last of the keys [from, to) whose V, or V scale, is not finite; -1 without
 // one.  By a warp, a key a lane.
@@ -132,11 +240,12 @@ __device__ __noinline__ int attn_last_nonfinite(const AttnParams& p, const AttnS
 // infinity stays one.  Nothing can change a row of NaN, so it ends there.  Slow,
 // a key after the other (0.5 us each): a prompt of 8192, 32 q heads of 128 on 8, whose
 // last V is NaN takes 137 ms (0.44 without it), all for the rows of the last pieces.
-template <int D>
+template <int D, bool GEN = false>
 __device__ __noinline__ void attend_row(const AttnParams& p, const AttnSeq& s, int b, int head, int tok) {
   constexpr int VPL = D / 32;
   const int lane = threadIdx.x & 31, h = head / p.group;
-  const int lim = attn_limit(s, tok);
+  const int lim = attn_limit(s, tok), low = GEN ? lim - p.window : 0;
+  const int own = b;
   float q[VPL], acc[VPL];
   const uint16_t* qr = p.Q + (s.q0 + tok) * p.ldq + head * D + lane * VPL;
 #pragma unroll
@@ -147,6 +256,8 @@ __device__ __noinline__ void attend_row(const AttnParams& p, const AttnSeq& s, i
   float m = -INFINITY, l = 0.f;
 #pragma unroll 1
   for (int j = 0; j < lim; ++j) {
+    if (GEN && j >= p.sinks && j < low) j = low;
+    if (GEN) b = j < s.lo ? s.head : own;
     float k[VPL], v[VPL];
     if (p.table && p.type != WAL_KV_BF16) {
       const int64_t row = attn_page_row(p, b, h, j);

@@ -199,6 +199,7 @@ struct Work {
   int k0, k1, n;     // keys [k0, k1), n tiles
   int n0, n1;        // key tiles of half 0 and 1
   bool dual;
+  int delta, low;    // GEN: keys are counted without the gap behind the first ones (AttnSpan)
   __device__ int n_t(int t) const { return t ? n1 : n0; }
   __device__ bool has_q(int t) const { return t ? n1 > 0 && !dual : n0 > 0; }
   __device__ int tile_of(int t, int k) const { return dual ? 2 * k + t : k; }
@@ -210,7 +211,7 @@ struct Work {
 // on, so that they get about the same.  Each role walks its CTA's pieces by
 // itself, whole warps at a time: a lane looks at a sequence, and the search for
 // a piece goes on where the last one ended.
-template <int TYPE>
+template <int TYPE, bool GEN>
 struct Walk {
   const AttnParams& p;
   int tile, at;            // tile pair, and the next piece's place among those from there on
@@ -230,9 +231,9 @@ struct Walk {
     tiles = 0;
     splits = 1;
     if (b >= p.B) return;
-    mine = attn_seq(p, b);
+    mine = attn_seq<GEN>(p, b);
     tiles = (mine.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows;
-    if (p.n_split > 1) splits = max(1, (mine.len + p.split_keys - 1) / p.split_keys);
+    if (p.n_split > 1) splits = GEN ? attn_splits(p, mine) : max(1, (mine.len + p.split_keys - 1) / p.split_keys);
   }
   // The next piece.
   __device__ __forceinline__ bool next(Work& w, AttnSeq& s) {
@@ -281,6 +282,10 @@ struct Walk {
           s.n_q = __shfl_sync(0xffffffffu, mine.n_q, src);
           s.len = __shfl_sync(0xffffffffu, mine.len, src);
           s.bad = false;
+          if (GEN) {
+            s.tab = __shfl_sync(0xffffffffu, mine.tab, src);
+            s.lo = __shfl_sync(0xffffffffu, mine.lo, src);
+          }
           break;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
@@ -293,7 +298,14 @@ struct Walk {
       back = other;
       w.rows = min(kTcAttnRows, s.n_q * p.group - w.r0);
       w.k0 = w.split * p.split_keys;
-      w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
+      if (GEN) {
+        const AttnSpan a = attn_span(p, s, attn_limit<GEN>(p, s, w.r0 / p.group), attn_limit<GEN>(p, s, (w.r0 + w.rows - 1) / p.group));
+        w.delta = a.delta;
+        w.low = a.low;
+        w.k1 = min(a.n, w.k0 + p.split_keys);
+      } else {
+        w.k1 = min(min(s.len, attn_limit(s, (w.r0 + w.rows - 1) / p.group)), w.k0 + p.split_keys);
+      }
       w.n = w.k1 > w.k0 ? (w.k1 - w.k0 + kTile - 1) / kTile : 0;
       w.dual = w.rows <= kTile && w.n > 1;
       if (w.dual) {
@@ -303,7 +315,7 @@ struct Walk {
         w.n0 = w.n;
         w.n1 = w.rows > kTile ? w.n : 0;
         if (TYPE == WAL_KV_BF16 && w.rows > kTile) {  // the first tile's rows may see fewer keys
-          const int end = min(w.k1, attn_limit(s, (w.r0 + kTile - 1) / p.group));
+          const int end = min(w.k1, attn_limit<GEN>(p, s, (w.r0 + kTile - 1) / p.group) - (GEN ? w.delta : 0));
           w.n0 = end > w.k0 ? (end - w.k0 + kTile - 1) / kTile : 0;
         }
       }
@@ -313,11 +325,16 @@ struct Walk {
   }
 };
 
+// Whether a key lies at place v of a piece that one of its rows sees.
+__device__ __forceinline__ bool place_counts(const AttnParams& p, const Work& w, int v) {
+  return v < w.k1 && (v >= w.low - w.delta || v < p.sinks);
+}
+
 // ---------------------------------------------------------------------------
 // K/V tiles by TMA (one warp): bf16 tiles as the MMAs want them, or codes and
 // scales for the converters
 // ---------------------------------------------------------------------------
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const CUtensorMap* km, const CUtensorMap* vm,
                                            uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
@@ -329,7 +346,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
   auto empty = [&](int s) { return C::codes ? bars.raw_empty(s) : bars.empty(s); };
   uint32_t item = 0, tails = 0;
   bool ok = true, tail = false;
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -342,17 +359,26 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
       if (p.table) {
         box_rows = min(kTile, 1 << p.shift);
         boxes = (cnt + box_rows - 1) / box_rows;
-        if (lane < boxes) page = attn_page(p, w.b, kb + lane * box_rows);
+        if (!GEN && lane < boxes) page = attn_page(p, w.b, kb + lane * box_rows);
       }
       const int x0 = p.table ? 0 : w.h * D, z0 = p.table ? w.h : 0;
-      const int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
+      int y0 = p.table ? kb & ((1 << p.shift) - 1) : s.q0 + kb;
+      bool hidden = cnt < kTile;  // some of the tile's places hold no key that counts
+      if (GEN) {  // boxes of p.gran places (a whole tile of a prompt without first keys), each a run of keys in one page
+        box_rows = p.table || p.sinks ? p.gran : kTile;
+        boxes = (cnt + box_rows - 1) / box_rows;
+        const int j0 = attn_key(kb + lane * box_rows, attn_sinks16(p), w.delta);
+        if (p.table && lane < boxes) page = attn_page(p, s.tab, j0);
+        y0 = p.table ? j0 & ((1 << p.shift) - 1) : s.q0 + j0;
+        hidden |= w.low - w.delta > p.sinks && kb < w.low - w.delta && kb + kTile > p.sinks;
+      }
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
         const int slot = item % kSlots;
         if (item >= kSlots) ok = bar_wait(empty(slot), ((item / kSlots) & 1) ^ 1, p);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tail = !C::codes && kv == 1 && cnt < kTile;
+        tail = !C::codes && kv == 1 && hidden;
         const uint32_t dst = ring + (uint32_t)slot * kBytes, bar = tail ? bars.v_tail() : full(slot);
         const uint32_t row_bytes = C::codes ? D + 4 : D * 2;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows) * row_bytes);
@@ -375,8 +401,9 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
           ++tails;
           tail = false;
 #pragma unroll 1
-          for (int r8 = lane; r8 < (kTile - cnt) * (D / 8); r8 += 32) {
-            const int r = cnt + r8 / (D / 8), ch = r8 % (D / 8);
+          for (int r8 = lane; r8 < (GEN ? kTile : kTile - cnt) * (D / 8); r8 += 32) {
+            const int r = (GEN ? 0 : cnt) + r8 / (D / 8), ch = r8 % (D / 8);
+            if (GEN && place_counts(p, w, kb + r)) continue;
             sts128(dst + (ch >> 3) * 16384u + sw128(r, ch & 7), make_uint4(0, 0, 0, 0));
           }
           fence_proxy_async_smem();
@@ -395,12 +422,12 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
 // ---------------------------------------------------------------------------
 // codes to bf16 tiles (four warps)
 // ---------------------------------------------------------------------------
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   const int tid = threadIdx.x & 127;
   uint32_t item = 0, tiles = 0;
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -408,6 +435,7 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uin
 #pragma unroll 1
     for (int j = 0; j < w.n; ++j, ++tiles) {
       const int cnt = min(kTile, w.k1 - w.k0 - kTile * j);
+      auto counts = [&](int r) { return GEN ? place_counts(p, w, w.k0 + kTile * j + r) : r < cnt; };
       const int si = tiles % kScaleRing;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++item) {
@@ -419,7 +447,7 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uin
         const uint32_t src = base + C::raw_off + (uint32_t)rs * C::raw, dst = base + C::ring_off + (uint32_t)slot * C::tile;
         // keys that are not there get codes and scales of zero
         sts32(base + C::scale_off + (uint32_t)(si * 2 + kv) * (kTile * 4) + 4u * tid,
-              tid < cnt ? lds32(src + kTile * D + 4u * tid) : 0u);
+              counts(tid) ? lds32(src + kTile * D + 4u * tid) : 0u);
 #pragma unroll 4
         for (int q = 0; q < D / 16; ++q) {
           // 16 codes: piece `part` (of 64 columns' four) of `atom` in `row`.  Eight
@@ -434,7 +462,7 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uin
             atom = 0;
           }
           uint4 v = lds128(src + (uint32_t)row * D + atom * 64u + part * 16u);
-          if (row >= cnt) v = make_uint4(0, 0, 0, 0);
+          if (!counts(row)) v = make_uint4(0, 0, 0, 0);
           uint4 x, y;
           dev::codes4_to_bf16<TYPE>(v.x, x.x, x.y);
           dev::codes4_to_bf16<TYPE>(v.y, x.z, x.w);
@@ -458,7 +486,7 @@ __device__ __forceinline__ void convert_tiles(const AttnParams& p, int most, uin
 // ---------------------------------------------------------------------------
 // 16-byte asynchronous copies, all of a tile in flight at once: a row may be any
 // (token, head), so no box fits every group.
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __forceinline__ void load_q(const AttnParams& p, int most, uint32_t base, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr int kChunks = D / 8, kStep = kQThreads / kChunks;  // 16-byte chunks of a row, rows between a thread's copies
@@ -466,7 +494,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, int most, uint32_t b
   const int ch = tid % kChunks, r_first = tid / kChunks;
   const int step_tok = kStep / p.group, step_head = kStep % p.group;
   uint32_t uses0 = 0, uses1 = 0;
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -529,7 +557,7 @@ __device__ __forceinline__ void load_q(const AttnParams& p, int most, uint32_t b
 // The whole warp walks the loop: with one lane alone in it the operands are not
 // known to be uniform, and an MMA took about 200 cycles to issue instead of the
 // 64 that it runs.
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32_t base, uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
   constexpr uint32_t id_s = idesc_bf16(128, 128, false), id_o = idesc_bf16(128, D, true);
@@ -569,7 +597,7 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32
   Pos pos = {0, 0};                                  // the piece's next K tile
   uint32_t quse0 = 0, quse1 = 0, ph0 = 0, ph1 = 0;  // parities: of the Q tiles' uses, of the halves' weights
   bool ok = true;
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -654,10 +682,10 @@ __device__ __forceinline__ void issue_mmas(const AttnParams& p, int most, uint32
 // Rows of half t that a key which they do not see has made NaN.  This comes after
 // the CTA's last piece, when nobody waits for this warp; a call of its own, so
 // that its code and registers stay out of the loop of softmax_rows.
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __noinline__ void redo_rows(const AttnParams& p, int most, int t) {
   const int tid = threadIdx.x & 127;
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -666,9 +694,17 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, int most, int t) {
     const bool live = row < w.r0 + w.rows && !(w.dual && t == 1);
     const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
     if (!__any_sync(0xffffffffu, live)) continue;
-    const int last = attn_last_nonfinite<D>(p, s, w.b, w.h, __shfl_sync(0xffffffffu, attn_limit(s, tok), 0), w.k1);
+    bool maybe;  // a key that the row does not see may be to blame
+    if (GEN) {
+      const int lim = attn_limit(s, tok), top = __reduce_max_sync(0xffffffffu, live ? attn_low(p, s, lim) : 0);
+      maybe = attn_last_nonfinite<D>(p, s, s.tab, w.h, __shfl_sync(0xffffffffu, lim, 0), w.k1 + w.delta) >= 0 ||
+              attn_last_nonfinite<D>(p, s, s.tab, w.h, w.low, top) >= 0;
+    } else {
+      const int last = attn_last_nonfinite<D>(p, s, w.b, w.h, __shfl_sync(0xffffffffu, attn_limit(s, tok), 0), w.k1);
+      maybe = attn_limit(s, tok) <= last;
+    }
     bool nan = false;
-    if (live && attn_limit(s, tok) <= last) {
+    if (live && maybe) {
       const uint4* o = reinterpret_cast<const uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D);
 #pragma unroll 2
       for (int i = 0; i < D / 8; ++i) {
@@ -683,17 +719,17 @@ __device__ __noinline__ void redo_rows(const AttnParams& p, int most, int t) {
     while (again) {
       const int src = __ffs(again) - 1;
       again &= again - 1;
-      attend_row<D>(p, s, w.b, __shfl_sync(0xffffffffu, head, src), __shfl_sync(0xffffffffu, tok, src));
+      attend_row<D, GEN>(p, s, GEN ? s.tab : w.b, __shfl_sync(0xffffffffu, head, src), __shfl_sync(0xffffffffu, tok, src));
     }
   }
 }
 
 // Rows of half t in the CTA's pieces after the first `done`, which a wait that gave
 // up has cut off: NaN, so that the loss shows even if nobody reads the status word.
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __noinline__ void lose_rows(const AttnParams& p, int most, int t, uint32_t done) {
   const int tid = threadIdx.x & 127;
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -702,8 +738,8 @@ __device__ __noinline__ void lose_rows(const AttnParams& p, int most, int t, uin
     if (i >= done && row < w.r0 + w.rows && !(w.dual && t == 1)) {
       const int tok = row / p.group, head = w.h * p.group + row - tok * p.group;
       const float nan = __int_as_float(0x7FC00000);
-      if (p.n_split > 1) {
-        p.part_ml[(int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head)] = make_float2(nan, nan);
+      if (p.n_split > 1 || (GEN && p.phase)) {
+        p.part_ml[(int64_t)((GEN ? p.part_first : 0) + w.split) * p.T * p.n_heads + attn_part_row(p, s, tok, head)] = make_float2(nan, nan);
       } else {
         uint4* o = reinterpret_cast<uint4*>(p.O + (s.q0 + tok) * p.ldo + head * D);
 #pragma unroll 1
@@ -721,7 +757,7 @@ __device__ __noinline__ void lose_rows(const AttnParams& p, int most, int t, uin
 // the schedulers' instruction caches are small, and code that is fetched anew
 // in every step costs the MMA warp, which runs each of its instructions once a
 // step, several times what the instructions do.
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int t, float sl, uint32_t base,
                                              uint32_t tmem, const Bars& bars) {
   using C = Cfg<D, TYPE>;
@@ -740,7 +776,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
     __syncwarp();
     if (lead) mbar_arrive(bar);
   };
-  Walk<TYPE> walk(p, most);
+  Walk<TYPE, GEN> walk(p, most);
   Work w;
   AttnSeq s;
 #pragma unroll 1
@@ -748,8 +784,13 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
     ++begun;
     const int row = w.r0 + (w.dual ? 0 : kTile * t) + tid;
     const int n = w.n_t(t);
-    const int lim = row < w.r0 + w.rows ? min(w.k1, attn_limit(s, row / p.group)) : w.k1;
+    const int lim = row < w.r0 + w.rows ? min(w.k1, attn_limit<GEN>(p, s, row / p.group) - (GEN ? w.delta : 0)) : w.k1;
     const int lim0 = __shfl_sync(0xffffffffu, lim, 0);  // the warp's smallest: limits grow with the row
+    int low = 0, low_max = 0;  // GEN: the place from which the row sees keys, and the warp's largest
+    if (GEN) {
+      low = (row < w.r0 + w.rows ? attn_low(p, s, attn_limit<GEN>(p, s, row / p.group)) : w.low) - w.delta;
+      low_max = __reduce_max_sync(0xffffffffu, low);
+    }
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
     for (int k = 0; k < n; ++k, ++steps) {
@@ -764,7 +805,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32u * q, x + 32 * q);
       tmem_ld_wait();
       const int seen = lim - kb;  // this row's keys in the tile
-      const bool masked = kb + kTile > lim0;
+      const bool masked = kb + kTile > lim0, masked_low = GEN && kb < low_max && kb + kTile > p.sinks;
       // scores of n keys from the q-th on: the keys' K scales, and -inf for keys
       // that the row does not see
       auto prepare = [&](float* v, int q, int n) {
@@ -781,6 +822,11 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
         if (masked) {
 #pragma unroll
           for (int e = 0; e < n; ++e) v[e] = q + e < seen ? v[e] : -INFINITY;
+        }
+        if (GEN && masked_low) {
+          const int first = p.sinks - kb, from = low - kb;
+#pragma unroll
+          for (int e = 0; e < n; ++e) v[e] = q + e < first || q + e >= from ? v[e] : -INFINITY;
         }
       };
       prepare(x, 0, kTile);
@@ -886,10 +932,10 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       l = l * f + l1 * f1;
     }
     const int tok = live ? row / p.group : 0, head = w.h * p.group + (live ? row - tok * p.group : 0);
-    const bool partial = p.n_split > 1;
+    const bool partial = p.n_split > 1 || (GEN && p.phase);
     const float inv = lim == 0 ? 0.f : 1.f / l;
     bool nan = false;
-    const int64_t pr = (int64_t)w.split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
+    const int64_t pr = (int64_t)((GEN ? p.part_first : 0) + w.split) * p.T * p.n_heads + attn_part_row(p, s, tok, head);
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       float o[32];
@@ -935,13 +981,13 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, int most, int 
       if (live) p.part_ml[pr] = make_float2(m, l);
       continue;
     }
-    redo |= __any_sync(0xffffffffu, live && nan && l == l && lim < w.k1);
+    redo |= __any_sync(0xffffffffu, live && nan && l == l && (GEN || lim < w.k1));
   }
-  if (redo) redo_rows<D, TYPE>(p, most, t);
-  if (lost) lose_rows<D, TYPE>(p, most, t, begun - 1);
+  if (redo) redo_rows<D, TYPE, GEN>(p, most, t);
+  if (lost) lose_rows<D, TYPE, GEN>(p, most, t, begun - 1);
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 __global__ void __launch_bounds__(Cfg<D, TYPE>::threads, 1)
 attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
   using C = Cfg<D, TYPE>;
@@ -996,7 +1042,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     int tiles = 0, bad = 0;
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += C::threads) {
-      const AttnSeq s = attn_seq(p, b);
+      const AttnSeq s = attn_seq<GEN>(p, b);
       bad |= s.bad;
       tiles = max(tiles, (s.n_q * p.group + kTcAttnRows - 1) / kTcAttnRows);
     }
@@ -1006,30 +1052,33 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   __syncthreads();
   const int most = shape[0];
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) {
-    if (p.clear) *p.status = p.n_split == 1 && shape[1] ? (int32_t)WAL_ERR_ARG : 0;
+    if (GEN && p.part_first) {}  // the launch before this one cleared it, the one after reports
+    else if (p.clear) *p.status = p.n_split == 1 && !(GEN && p.phase) && shape[1] ? (int32_t)WAL_ERR_ARG : 0;
     else if (shape[1]) attn_report(p.status);
   }
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
-    softmax_rows<D, TYPE>(p, most, warp >> 2, sl, base, tmem, bars);
+    softmax_rows<D, TYPE, GEN>(p, most, warp >> 2, sl, base, tmem, bars);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
     if (warp == 8) {
-      issue_mmas<D, TYPE>(p, most, base, tmem, bars);
+      issue_mmas<D, TYPE, GEN>(p, most, base, tmem, bars);
     } else if (warp == 9) {
-      load_tiles<D, TYPE>(p, most, &km, &vm, base, bars);
+      load_tiles<D, TYPE, GEN>(p, most, &km, &vm, base, bars);
     } else if (warp < 12) {
-      load_q<D, TYPE>(p, most, base, bars);
+      load_q<D, TYPE, GEN>(p, most, base, bars);
     } else {
-      convert_tiles<D, TYPE>(p, most, base, bars);
+      convert_tiles<D, TYPE, GEN>(p, most, base, bars);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
+  // The second launch of a shared call starts beside the first; what comes after it must come after both.
+  if (GEN && p.part_first && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -1073,6 +1122,7 @@ int make_map(CUtensorMap* map, const AttnParams& p, const void* base, int64_t ld
     strides[2] = H * page * D * size;
     if (page < kTile) box[1] = (cuuint32_t)page;
   }
+  if (p.gen && (p.table || p.sinks)) box[1] = (cuuint32_t)p.gran;
   const CUresult r = enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                          strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1080,21 +1130,36 @@ int make_map(CUtensorMap* map, const AttnParams& p, const void* base, int64_t ld
   return WAL_OK;
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool GEN>
 int launch_one(const AttnParams& p, cudaStream_t stream) {
   CUtensorMap km = {}, vm = {};
   int st = make_map(&km, p, p.k, p.ldk);
   if (st || (st = make_map(&vm, p, p.v, p.ldv))) return st;
   // the attribute is per device; setting it again is cheap and needs no state
-  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, TYPE>::smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, TYPE, GEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, TYPE>::smem);
   if (e == cudaSuccess) {
     const int64_t tiles = ((int64_t)p.max_q * p.group + kTcAttnRows - 1) / kTcAttnRows;
     const int64_t pieces = tiles * p.n_split * p.n_kv_heads * p.B;
-    attn_tc_kernel<D, TYPE><<<(unsigned)(pieces < kGrid ? pieces : kGrid), Cfg<D, TYPE>::threads, Cfg<D, TYPE>::smem, stream>>>(p, km, vm);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pieces < kGrid ? pieces : kGrid));
+    cfg.blockDim = dim3(Cfg<D, TYPE>::threads);
+    cfg.dynamicSmemBytes = Cfg<D, TYPE>::smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (GEN && p.part_first) {  // beside the prefix's launch
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+    }
+    e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, TYPE, GEN>, p, km, vm);
   }
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string("attn_tc_kernel launch: ") + cudaGetErrorString(e));
   return WAL_OK;
+}
+template <int D, int TYPE>
+int launch_one(const AttnParams& p, cudaStream_t stream) {
+  return p.gen ? launch_one<D, TYPE, true>(p, stream) : launch_one<D, TYPE, false>(p, stream);
 }
 
 }  // namespace

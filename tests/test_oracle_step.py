@@ -43,3 +43,22 @@ def test_head_norm_by_hand():
     y = so.head_norm([[3.0, 4.0, 0.0, 0.0]], [1.0, 2.0, 1.0, 1.0], 0.0)
     assert np.allclose(y, [[3 / 2.5, 8 / 2.5, 0, 0]], rtol=1e-15)
     assert np.allclose(so.head_norm([[0.0, 0.0]], [1, 1], 1e-6), 0) and np.allclose(so.head_norm([[1e-3] * 2], [1, 1], 1e-6), 2 ** -0.5)
+
+
+def test_window_by_hand():
+    s = so.window_sees(3, 8, 2, 1).astype(int).tolist()
+    assert s == [[1, 0, 0, 0, 1, 1, 0, 0], [1, 0, 0, 0, 0, 1, 1, 0], [1, 0, 0, 0, 0, 0, 1, 1]]
+    assert so.window_sees(4, 2, 1, 0).astype(int).tolist() == [[0, 0], [0, 0], [1, 0], [0, 1]]
+
+
+def test_attention_of_what_a_row_sees():
+    rng = np.random.default_rng(4)
+    q, k, v = rng.normal(size=(4, 2, 8)), rng.normal(size=(9, 1, 8)), rng.normal(size=(9, 1, 8))
+    from oracle import attn_oracle as ao
+    for o, r in zip(so.attend(q, k, v, 0.3, 2, so.window_sees(4, 9, 9, 0)), ao.attend(q, k, v, 0.3, 2)):
+        assert np.allclose(o, r, atol=1e-14)
+    one = so.attend(q, k, v, 0.3, 2, so.window_sees(4, 9, 1, 0))[0]
+    assert np.allclose(one, np.repeat(v[5:, :1], 2, 1))
+    keep = [0, 1, 6, 7, 8]
+    last = so.attend(q, k, v, 0.3, 2, so.window_sees(4, 9, 3, 2))[0][3]
+    assert np.allclose(last, so.attend(q[3:], k[keep], v[keep], 0.3, 2, np.ones((1, 5), bool))[0][0])

@@ -64,6 +64,68 @@ def test_qkv_append_refuses(kw, status):
     refuses(status, wal.wal_qkv_append, *args(APPEND, kw))
 
 
+PAGED = dict(cache=cache(), Q=P, n_heads=4, T=3, ldq=256, q_start=P, kv_len=P, table=P, ld_table=4, B=2, max_q=2, max_kv=64, window=10,
+             sinks=2, scale=0.1, O=P + 4096, ldo=256, ws=P, ws_bytes=1 << 30, stream=None)
+BAD_ATTN = [(dict(n_heads=5), SHAPE), (dict(T=-1), SHAPE), (dict(B=0), SHAPE), (dict(B=65536), SHAPE), (dict(max_q=0), SHAPE), (dict(max_kv=0), SHAPE),
+            (dict(max_kv=65), ARG), (dict(max_kv=2 ** 30 + 1), UNSUPPORTED), (dict(scale=float("nan")), ARG), (dict(Q=None), ARG), (dict(Q=P + 8), ARG),
+            (dict(O=None), ARG), (dict(O=P), ARG), (dict(ldq=255), ARG), (dict(ldo=248), ARG), (dict(q_start=None), ARG), (dict(kv_len=P + 2), ARG),
+            (dict(table=None), ARG)]
+
+
+@pytest.mark.parametrize("kw,status", [(dict(cache=cache(**c)), s) for c, s in BAD_CACHE] + BAD_ATTN + [
+    (dict(window=0), SHAPE), (dict(window=-5), SHAPE), (dict(sinks=-1), SHAPE), (dict(ws_bytes=511), WORKSPACE)])
+def test_paged_window_refuses(kw, status):
+    if kw == dict(O=P):
+        status = ARG if torch.cuda.is_available() else wal.WAL_ERR_CUDA
+    refuses(status, wal.wal_attn_paged_window, *args(PAGED, kw))
+
+
+PROMPT = dict(Q=P, K=P, V=P, n_heads=4, n_kv_heads=2, head_dim=64, T=3, ldq=256, ldk=128, ldv=128, start=P, B=2, max_len=64, window=10, sinks=2,
+              scale=0.1, O=P + 4096, ldo=256, ws=P, ws_bytes=512, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(window=0), SHAPE), (dict(sinks=-1), SHAPE), (dict(n_heads=5), SHAPE), (dict(head_dim=96), UNSUPPORTED), (dict(T=-1), SHAPE), (dict(B=0), SHAPE),
+    (dict(max_len=0), SHAPE), (dict(scale=float("inf")), ARG), (dict(Q=None), ARG), (dict(K=P + 8), ARG), (dict(V=None), ARG), (dict(ldk=120), ARG),
+    (dict(start=None), ARG), (dict(ws_bytes=511), WORKSPACE)])
+def test_prompt_window_refuses(kw, status):
+    refuses(status, wal.wal_attn_prompt_window, *args(PROMPT, kw))
+
+
+SHARED = dict(cache=cache(), Q=P, n_heads=4, T=3, ldq=256, q_start=P, kv_len=P, table=P, ld_table=4, B=2, group_start=P, prefix_len=P, G=1, max_q=2,
+              max_kv=64, max_prefix=32, max_own=32, scale=0.1, O=P + 4096, ldo=256, ws=P, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [(dict(cache=cache(**c)), s) for c, s in BAD_CACHE] + [x for x in BAD_ATTN if x[0] != dict(O=P)] + [
+    (dict(G=0), SHAPE), (dict(G=65536), SHAPE), (dict(max_prefix=-1), SHAPE), (dict(max_prefix=65), SHAPE), (dict(max_own=0), SHAPE),
+    (dict(max_own=2 ** 30 + 1), UNSUPPORTED), (dict(group_start=None), ARG), (dict(prefix_len=P + 2), ARG), (dict(ws=None), WORKSPACE),
+    (dict(ws_bytes=600), WORKSPACE)])
+def test_shared_refuses(kw, status):
+    refuses(status, wal.wal_attn_paged_shared, *args(SHARED, kw))
+
+
+def test_workspace_sizes_are_those_that_the_calls_want():
+    c = cache(n_pages=1 << 16, type=wal.WAL_KV_BF16, k_scale=None, v_scale=None)
+    for T, B, max_q, max_kv in ((1, 1, 1, 64), (3, 3, 1, 30000), (90, 2, 50, 30000), (4000, 2, 2000, 4000)):
+        for window, sinks in ((1, 0), (900, 4), (2000, 300), (40000, 0)):
+            n = wal.wal_attn_paged_window_workspace_bytes(c, 4, T, B, max_q, max_kv, window, sinks)
+            assert n >= 512
+            kw = dict(cache=c, T=T, B=B, max_q=max_q, max_kv=max_kv, ld_table=2000, window=window, sinks=sinks, ws_bytes=n - 1)
+            refuses(WORKSPACE, wal.wal_attn_paged_window, *args(PAGED, kw))
+            if window >= max_kv:
+                assert n == wal.wal_attn_paged_workspace_bytes(c, 4, T, B, max_q, max_kv)
+        for G, pre, own in ((1, 0, 64), (2, 8000, 100), (3, 64, max_kv)):
+            n = wal.wal_attn_paged_shared_workspace_bytes(c, 4, T, B, G, max_q, pre, own)
+            kw = dict(cache=c, T=T, B=B, G=G, max_q=max_q, max_kv=30000, ld_table=2000, max_prefix=pre, max_own=own, ws_bytes=n - 1)
+            refuses(WORKSPACE, wal.wal_attn_paged_shared, *args(SHARED, kw))
+    for bad in (dict(window=0), dict(sinks=-1), dict(n_heads=3), dict(max_kv=0)):
+        kw = dict(n_heads=4, T=3, B=2, max_q=2, max_kv=64, window=9, sinks=0)
+        assert wal.wal_attn_paged_window_workspace_bytes(c, *{**kw, **bad}.values()) == 0
+    for bad in (dict(G=0), dict(max_prefix=-1), dict(max_own=0), dict(n_heads=3)):
+        kw = dict(n_heads=4, T=3, B=2, G=1, max_q=2, max_prefix=64, max_own=9)
+        assert wal.wal_attn_paged_shared_workspace_bytes(c, *{**kw, **bad}.values()) == 0
+
+
 def test_bindings_refuse():
     """What the library cannot see; every call stops before the device."""
     f = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype)
@@ -87,3 +149,15 @@ def test_bindings_refuse():
     for kw in (dict(table=i(3, 4)), dict(table=i(2, 8)[:, ::2]), dict(max_kv=65), dict(max_kv=2 ** 31), {}):
         with pytest.raises(ValueError):
             c.plan(**{**plan, **kw})
+    att = dict(q=f(3, 256), q_start=i(3), kv_len=i(2), table=i(2, 4), out=f(3, 256), max_q=2, max_kv=64)
+    for kw in (dict(window=0), dict(window=4, sinks=-1), dict(window=4, max_kv=65), dict(window=4, q=f(3, 250)), dict(window=4)):
+        with pytest.raises(ValueError):
+            c.attend(**{**att, **kw})
+    share = dict(att, group_start=i(2), prefix_len=i(1), max_prefix=16, max_own=48)
+    for kw in (dict(max_kv=65), dict(out=f(3, 128)), dict(max_own=2 ** 31), dict(max_prefix=2 ** 31), {}):
+        with pytest.raises(ValueError):
+            c.attend_shared(**{**share, **kw})
+    prompt = dict(q=f(3, 256), k=f(3, 128), v=f(3, 128), start=i(2), out=f(3, 256), head_dim=64, max_len=3)
+    for kw in (dict(window=0), dict(window=4, sinks=-1), dict(window=4)):
+        with pytest.raises(ValueError):
+            wal.attn_prompt(**{**prompt, **kw})
