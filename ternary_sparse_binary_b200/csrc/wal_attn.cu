@@ -5,7 +5,7 @@
 // over the keys a token sees: the first len - n_q + i + 1 of its sequence for
 // new token i.  One pass over the keys with the running maximum m and sum l:
 // when m grows to m', l and the accumulator are multiplied by 2^(m - m').
-#include "wal_attn.h"
+#include "wal_attn_dec.cuh"
 #include "wal_ptx.cuh"
 
 #include <algorithm>
@@ -17,39 +17,6 @@ namespace wal {
 namespace {
 
 constexpr int kRowWarps = 4;
-
-// Divide, round and store a row held by a warp.  A row that came out as NaN
-// beside a non-finite V which it does not see is done again from its own keys.
-template <int D, bool GEN>
-__device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s, int b, int head, int tok, const float* acc,
-                                           float l) {
-  constexpr int VPL = D / 32;
-  const int lane = threadIdx.x & 31, lim = attn_limit(s, tok);
-  float y[VPL];
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    y[i] = lim == 0 ? 0.f : acc[i] / l;
-    nan |= y[i] != y[i];
-  }
-  if (__any_sync(0xffffffffu, nan && l == l)) {
-    const int h = head / p.group, row = tok * p.group + head - h * p.group, reach = attn_reach(p, s, row);
-    if (lim < reach && attn_last_nonfinite<D>(p, s, b, h, lim, reach) >= 0) {
-      attend_row<D, GEN>(p, s, b, head, tok);
-      return;
-    }
-    if (GEN) {
-      const int from = attn_from(p, s, row), low = attn_low(p, s, lim);
-      if (from < low && attn_last_nonfinite<D>(p, s, b, h, from, low) >= 0) {
-        attend_row<D, GEN>(p, s, b, head, tok);
-        return;
-      }
-    }
-  }
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + (s.q0 + tok) * p.ldo + head * D + lane * VPL);
-#pragma unroll
-  for (int i = 0; i < VPL / 2; ++i) dst[i] = dev::float2_to_bf16x2(y[2 * i], y[2 * i + 1]);
-}
 
 // ---------------------------------------------------------------------------
 // few query rows: keys split over CTAs, mma.sync
@@ -81,44 +48,8 @@ __device__ __forceinline__ void finish_row(const AttnParams& p, const AttnSeq& s
 // keys); references, l, scores and O are fp32.
 // References are lazy: they follow the maximum when it has grown by more than
 // 2^4, which a vote finds; most steps have no reduction and leave O alone.
-constexpr int kDecWarps = 4;
-constexpr int kDecMaxRows = 16;
-
-template <bool HALF>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  if (HALF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kDecLazy = 4.f;
-
-template <int D, int TYPE, int NT, int MT, bool GEN>
-__device__ __forceinline__ void attn_decode(const AttnParams& p) {
+template <int D, int TYPE, int NT, int MT>
+__global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1 ? 3 : 2) attn_decode_kernel(const __grid_constant__ AttnParams p) {
   constexpr bool CODES = TYPE != WAL_KV_BF16;
   constexpr int KB = CODES ? 1 : 2;      // bytes of a code
   constexpr int W = D * KB / 16;         // 32-bit words of K per lane and key (of 4 lanes)
@@ -130,23 +61,16 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const AttnSeq s = attn_seq<GEN>(p, b);
+  const AttnSeq s = attn_seq(p, b);
   if (p.clear) {
-    if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0 && !(GEN && p.part_first)) *p.status = 0;
+    if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0) *p.status = 0;
   } else if (s.bad && h == 0 && threadIdx.x == 0 && p.status) {
     attn_report(p.status);
   }
   if (s.bad) return;
   const int rows = s.n_q * p.group;
-  const int tab = GEN ? s.tab : b;
-  AttnSpan span = {};
-  if (GEN && rows) span = attn_span(p, s, attn_limit<GEN>(p, s, 0), attn_limit<GEN>(p, s, s.n_q - 1));
-  const int sinks16 = GEN ? attn_sinks16(p) : 0;
-  const int k0 = split * p.split_keys, k1 = min(GEN ? span.n : s.len, k0 + p.split_keys);
+  const int k0 = split * p.split_keys, k1 = min(s.len, k0 + p.split_keys);
   if (rows == 0 || (k0 >= k1 && split > 0)) return;  // split 0 also answers for a sequence without keys
-  // key of place v (the same without GEN), and whether some row sees it
-  auto key = [&](int v) { return GEN ? attn_key(v, sinks16, span.delta) : v; };
-  auto seen = [&](int v, int j) { return v < k1 && (!GEN || j >= span.low || j < p.sinks); };
 
   // K and V of a step, and where they lie: a tile of 16 keys is in one page
   uint32_t kw[MT][2][W], vw[MT][4][NW];
@@ -154,7 +78,7 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
   int64_t row[MT];
   auto find = [&](int j0) {
 #pragma unroll
-    for (int u = 0; u < MT; ++u) row[u] = j0 + 16 * u < k1 ? attn_page_row(p, tab, h, key(j0 + 16 * u)) : 0;
+    for (int u = 0; u < MT; ++u) row[u] = j0 + 16 * u < k1 ? attn_page_row(p, b, h, j0 + 16 * u) : 0;
   };
   auto load_k = [&](int j0) {
     const uint8_t* base = static_cast<const uint8_t*>(p.k);
@@ -163,7 +87,7 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = g + 8 * e;
-        const bool live = seen(j0 + 16 * u + j, key(j0 + 16 * u) + j);
+        const bool live = j0 + 16 * u + j < k1;
         const uint8_t* src = base + (row[u] + j) * (D * KB) + 16 * c;
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
@@ -181,7 +105,7 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = 2 * c + (e & 1) + 8 * (e >> 1);
-        const bool live = seen(j0 + 16 * u + j, key(j0 + 16 * u) + j);
+        const bool live = j0 + 16 * u + j < k1;
         const uint8_t* src = base + (row[u] + j) * (D * KB);
         if (NW >= 4) {
 #pragma unroll
@@ -198,7 +122,7 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
       }
       if (CODES)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) vs[u][e] = seen(j0 + 16 * u + g + 8 * e, key(j0 + 16 * u) + g + 8 * e) ? __ldg(p.vs + row[u] + g + 8 * e) : 0.f;
+        for (int e = 0; e < 2; ++e) vs[u][e] = j0 + 16 * u + g + 8 * e < k1 ? __ldg(p.vs + row[u] + g + 8 * e) : 0.f;
     }
   };
   int j0 = k0 + warp * STEP;
@@ -251,13 +175,11 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * t + 2 * c + e;
-      lim[t][e] = r < rows ? attn_limit<GEN>(p, s, r / p.group) : s.len;
+      lim[t][e] = r < rows ? attn_limit(s, r / p.group) : s.len;
       m[t][e] = m2[t][e] = -INFINITY;
       l[t][e] = 0.f;
     }
-  // places that every row sees end at lim_min and, but for the first keys, begin at low_max
-  const int lim_min = min(k1, attn_limit<GEN>(p, s, 0) - span.delta);
-  const int low_max = GEN ? attn_low(p, s, attn_limit<GEN>(p, s, s.n_q - 1)) - span.delta : 0;
+  const int lim_min = min(k1, attn_limit(s, 0));
   float o[DT][NT][4];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -305,20 +227,15 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
             if (CODES) x *= ks[u][r];
           }
       }
-    if (j0 + STEP > lim_min || (GEN && j0 < low_max)) {  // keys a row does not see get -inf
+    if (j0 + STEP > lim_min) {  // keys a row does not see get -inf
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int v = j0 + 16 * u + g + 8 * (e >> 1);
-            if (GEN) {
-              const int j = key(j0 + 16 * u) + g + 8 * (e >> 1), up = lim[t][e & 1];
-              if (v >= k1 || j >= up || (j < attn_low(p, s, up) && j >= p.sinks)) sc[u][t][e] = -INFINITY;
-            } else if (v >= min(k1, lim[t][e & 1])) {
-              sc[u][t][e] = -INFINITY;
-            }
+            const int j = j0 + 16 * u + g + 8 * (e >> 1);
+            if (j >= min(k1, lim[t][e & 1])) sc[u][t][e] = -INFINITY;
           }
     }
     // the next step's K, in the registers of this one's
@@ -471,8 +388,8 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
       for (int i = 0; i < VPL; ++i) acc[i] += f * s_o[w][r][lane * VPL + i];
     }
     const int tok = r / p.group, head = h * p.group + r % p.group;
-    if (p.n_split > 1 || (GEN && p.phase)) {
-      const int64_t pr = (int64_t)((GEN ? p.part_first : 0) + split) * p.T * p.n_heads + attn_part_row(p, s, tok, head);
+    if (p.n_split > 1) {
+      const int64_t pr = (int64_t)split * p.T * p.n_heads + attn_part_row(p, s, tok, head);
       float* dst = p.part_o + pr * D + lane * VPL;
       if (VPL == 4)
         *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[VPL - 2], acc[VPL - 1]);
@@ -480,19 +397,9 @@ __device__ __forceinline__ void attn_decode(const AttnParams& p) {
         *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
       if (lane == 0) p.part_ml[pr] = make_float2(mm, ll);
     } else {
-      finish_row<D, GEN>(p, s, tab, head, tok, acc, ll);
+      finish_row<D, false>(p, s, b, head, tok, acc, ll);
     }
   }
-}
-// The second launch of a shared call starts beside the first.  Its first CTA waits for
-// that, so that what comes after the second comes after both.
-__device__ __forceinline__ void after_prefix(const AttnParams& p) {
-  if (p.part_first && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-template <int D, int TYPE, int NT, int MT, bool GEN>
-__global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1 ? 3 : 2) attn_decode_kernel(const __grid_constant__ AttnParams p) {
-  attn_decode<D, TYPE, NT, MT, GEN>(p);
-  if (GEN) after_prefix(p);
 }
 
 // Add the splits of a row, and report index values out of range.  PER warps of
@@ -613,31 +520,13 @@ int launched(cudaError_t e, const char* what) {
 // fits three CTAs on an SM (25 sequences, 16384 keys: 133 us against 136 with two
 // tiles and two CTAs); codes take two and fit two CTAs (int8, 32768 keys: 181 us,
 // 189 squeezed into three, 203 with one tile).
-template <int D, int TYPE, bool GEN>
-cudaError_t launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
+template <int D, int TYPE>
+void launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
   constexpr int MT = TYPE == WAL_KV_BF16 ? 1 : 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32 * kDecWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  if (GEN && p.part_first) {  // beside the prefix's launch
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  if (p.max_q * p.group <= 8) return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, TYPE, 1, MT, GEN>, p);
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, TYPE, 2, MT, GEN>, p);
-}
-template <bool GEN>
-cudaError_t launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
-  const bool wide = p.head_dim == 128;
-  switch (p.type) {
-    case WAL_KV_BF16: return wide ? launch_decode<128, WAL_KV_BF16, GEN>(p, grid, s) : launch_decode<64, WAL_KV_BF16, GEN>(p, grid, s);
-    case WAL_KV_INT8: return wide ? launch_decode<128, WAL_KV_INT8, GEN>(p, grid, s) : launch_decode<64, WAL_KV_INT8, GEN>(p, grid, s);
-    default: return wide ? launch_decode<128, WAL_KV_E4M3, GEN>(p, grid, s) : launch_decode<64, WAL_KV_E4M3, GEN>(p, grid, s);
-  }
+  if (p.max_q * p.group <= 8)
+    attn_decode_kernel<D, TYPE, 1, MT><<<grid, 32 * kDecWarps, 0, s>>>(p);
+  else
+    attn_decode_kernel<D, TYPE, 2, MT><<<grid, 32 * kDecWarps, 0, s>>>(p);
 }
 
 template <bool GEN>
@@ -728,8 +617,15 @@ int launch_pieces(AttnParams& p, cudaStream_t stream) {
   p.polls = polls < 0 ? (int)ptx::kSpinLimit : polls;
   p.tc = !p.table || (int64_t)p.max_q * p.group > kDecMaxRows;
   if (p.tc) return launch_attn_tc(p, stream);
+  if (p.gen) return launch_attn_ring(p, stream);
   const dim3 grid((unsigned)p.n_split, (unsigned)p.n_kv_heads, (unsigned)p.B);
-  return launched(p.gen ? launch_decode<true>(p, grid, stream) : launch_decode<false>(p, grid, stream), "attn_decode_kernel");
+  const bool wide = p.head_dim == 128;
+  switch (p.type) {
+    case WAL_KV_BF16: wide ? launch_decode<128, WAL_KV_BF16>(p, grid, stream) : launch_decode<64, WAL_KV_BF16>(p, grid, stream); break;
+    case WAL_KV_INT8: wide ? launch_decode<128, WAL_KV_INT8>(p, grid, stream) : launch_decode<64, WAL_KV_INT8>(p, grid, stream); break;
+    default: wide ? launch_decode<128, WAL_KV_E4M3>(p, grid, stream) : launch_decode<64, WAL_KV_E4M3>(p, grid, stream); break;
+  }
+  return launched(cudaGetLastError(), "attn_decode_kernel");
 }
 int launch_attn(AttnParams& p, cudaStream_t stream) {
   const int st = launch_pieces(p, stream);

@@ -52,6 +52,8 @@ constexpr int kNoWindow = 1 << 30;
 // The tensor-core kernel (wal_attn_tc.cu).
 constexpr int kTcAttnRows = 256;  // query rows of one CTA there
 int launch_attn_tc(const AttnParams& p, cudaStream_t stream);
+// The general kernel of few query rows (wal_attn_ring.cu).
+int launch_attn_ring(const AttnParams& p, cudaStream_t stream);
 
 // An index value out of range: recorded, unless something is already (a wait that gave up).
 __device__ __forceinline__ void attn_report(int32_t* status) { atomicCAS(status, 0, (int32_t)WAL_ERR_ARG); }
