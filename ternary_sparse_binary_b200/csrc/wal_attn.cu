@@ -608,6 +608,52 @@ void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int
   *n_split = (int)((max_kv + keys - 1) / keys);
 }
 
+// The same for the general kernels.
+// Ring kernel.  Its CTAs run ring_ctas at a time on an SM.  Where the sequences are about
+// as long as their bound (a window much shorter than the cache, a prefix), the split with
+// the least estimate: the keys' bytes at 6 TB/s, or rounds of CTAs of 4 us and a time a
+// key, whichever is longer, and 7 us for the second kernel.  25 slots, int8 pages, 32 q
+// heads of 128 on 8, in one, two, three and four splits: window of 4096 (it takes two)
+// 52.6, 46.5, 53.3 and 50.1 us; window of 1024 (one) 17.6, 19.1, 21.1, 21.0; bf16 pages
+// and 4096 (one) 58.3, 63.5, 67.7, 63.6; heads of 64 (two) 39.5, 31.9, 30.7, 36.7.
+// Where they are ragged, so many that twice the CTAs at a time have keys: the same slots
+// with a window beyond their up to 32768 tokens take 248 us in two splits, 172, 154, 145
+// and 150 in three, four, eight (it takes seven) and sixteen.
+struct Split {
+  int n, keys;
+};
+int ring_ctas(int head_dim, int64_t rows) { return rows > 8 ? 2 : head_dim == 64 ? 4 : 3; }
+Split plan_general(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int max_kv, bool even) {
+  Split r = {1, max_kv};
+  const int64_t rows = (int64_t)std::max(1, std::min(max_q, T)) * (n_heads / c.n_heads);
+  if (T == 0 || rows > kDecMaxRows) {
+    plan_split(c, n_heads, T, B, max_q, max_kv, &r.n, &r.keys);
+    return r;
+  }
+  const int64_t pieces = (int64_t)B * c.n_heads, tiles = ((int64_t)max_kv + 127) / 128, slots = kPlanSms * ring_ctas(c.head_dim, rows);
+  int64_t n = std::min(tiles, std::max<int64_t>(1, slots * 7 / (2 * pieces)));
+  if (even) {
+    const bool codes = c.type != WAL_KV_BF16;
+    const double bytes = (double)pieces * max_kv * (2 * c.head_dim * (codes ? 1 : 2) + (codes ? 8 : 0)) / 6e6;
+    const double tile = 128 * (codes ? 0.012 : 0.009) * (c.head_dim == 64 ? 0.75 : 1) * (rows > 8 ? 1.2 : 1);
+    double best = 0;
+    n = 1;
+    for (int64_t s = 1; s <= tiles && s <= 1024; ++s) {
+      const double rounds = (double)((pieces * s + slots - 1) / slots);
+      const double cost = std::max(bytes, rounds * (4 + (double)((tiles + s - 1) / s) * tile)) +
+                          (s > 1 ? 7 + (double)pieces * rows * s * c.head_dim * 4 * 2 / 5.7e6 : 0);
+      if (s == 1 || cost < best) {
+        n = s;
+        best = cost;
+      }
+    }
+  }
+  const int64_t keys = (tiles + n - 1) / n * 128;
+  r.keys = (int)std::min<int64_t>(keys, 0x7FFFFF80);
+  r.n = (int)((max_kv + keys - 1) / keys);
+  return r;
+}
+
 // Set by wal_debug_wait_polls: the limit of the device waits of later calls; below 0, the usual one.
 std::atomic<int> g_wait_polls{-1};
 
@@ -646,18 +692,31 @@ Window window_of(int window, int sinks, int max_kv) {
   if (window >= max_kv || sinks >= max_kv) return {false, kNoWindow, 0};
   return {true, window, sinks};
 }
-// Keys in one run of a page (of a prompt's rows): 16 where the first keys come before the window's in a tile.
-int gran_of(int page_size, int sinks) { return sinks ? 16 : page_size ? std::min(page_size, 128) : 1; }
+// Keys in one run of a page (of a prompt's rows): short ones where the first keys come before the window's in a tile.
+int gran_of(int page_size, int sinks) {
+  if (sinks) return page_size ? std::min(page_size, 32) : 32;
+  return page_size ? std::min(page_size, 128) : 1;
+}
 int piece_toks(int group) { return (kTcAttnRows - 1) / group + 2; }
 // Most places of a piece's keys.
 int most_keys(const Window& w, int gran, int group, int max_q, int max_kv) {
   if (!w.gen) return max_kv;
-  return (int)std::min<int64_t>(max_kv, (int64_t)w.window + std::min(max_q, piece_toks(group)) + (int64_t)align_up((size_t)w.sinks, 16) + gran);
+  return (int)std::min<int64_t>(max_kv, (int64_t)w.window + std::min(max_q, piece_toks(group)) + (int64_t)align_up((size_t)w.sinks, gran) + gran);
+}
+Split plan_paged(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int max_kv, const Window& w) {
+  if (w.gen) {
+    const int most = most_keys(w, gran_of(c.page_size, w.sinks), n_heads / c.n_heads, max_q, max_kv);
+    return plan_general(c, n_heads, T, B, max_q, most, most <= max_kv / 2);
+  }
+  Split r = {};
+  plan_split(c, n_heads, T, B, max_q, max_kv, &r.n, &r.keys);
+  return r;
 }
 void set_window(AttnParams& p, const Window& w, int gran) {
   p.gen = w.gen;
   p.window = w.window; p.sinks = w.sinks;
   p.gran = gran;
+  p.sinks_pad = (int)align_up((size_t)w.sinks, gran);
   p.piece_toks = std::min(p.max_q, piece_toks(p.group));
 }
 
@@ -701,8 +760,9 @@ int attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T,
   int dev = 0;
   AttnParams p = {};
   cudaStream_t s = (cudaStream_t)stream;
-  const int gran = gran_of(cache->page_size, w.sinks);
-  plan_split(*cache, n_heads, T, B, max_q, most_keys(w, gran, n_heads / cache->n_heads, max_q, max_kv), &p.n_split, &p.split_keys);
+  const Split sp = plan_paged(*cache, n_heads, T, B, max_q, max_kv, w);
+  p.n_split = sp.n;
+  p.split_keys = sp.keys;
   if ((ws || p.n_split > 1) && (!ws || ws_bytes < attn_ws_bytes(p.n_split, T, n_heads, cache->head_dim)))
     return fail(WAL_ERR_WORKSPACE, "workspace too small");
   if ((st = current_device(&dev))) return st;
@@ -712,7 +772,7 @@ int attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T,
   if (!p.clear && (st = clear_status(ws, s, &p.status))) return st;
   if (T == 0) return WAL_OK;
   set_paged(p, cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo);
-  set_window(p, w, gran);
+  set_window(p, w, gran_of(cache->page_size, w.sinks));
   set_parts(p, p.n_split);
   return launch_attn(p, s);
 }
@@ -749,19 +809,52 @@ int attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_h
   return launch_attn(p, s);
 }
 
-// Splits of a shared call's two launches.  The prefix's rows are the groups' tokens, of which only T is known.
+// Splits of a shared call's two launches.  The prefix's rows are the groups' tokens, of
+// which only T is known.
+// The tensor-core kernel's CTAs take an SM each, and the other launch has what is left,
+// so a prefix is not spread over all of them: the split is the one with which the longer
+// of both is shortest, the prefix's own pieces (2.7 us a step of 128 8-bit keys, 1.9 of
+// bf16, three steps more a piece) and the sum of all work over the SMs, the other launch's
+// at 6 TB/s of half its bounds.  More CTAs than half of the SMs, where two of them share
+// a pair of SMs, count a fifth more beside other work.  64 slots with up to 2048 tokens of
+// their own, 32 q heads of 128 on 8, behind 16384 shared int8 keys: in six, eight, nine
+// (which it takes), ten and sixteen splits 89, 74, 76, 85 and 87 us; over bf16 pages in
+// six, eight (nine), ten and twelve 81, 78, 80 and 83.
 struct SharedPlan {
-  int prefix, prefix_keys, own, own_keys;
+  Split prefix, own;  // prefix.n is 0 where there is none
 };
 SharedPlan plan_shared(const wal_kv_cache& c, int n_heads, int T, int B, int G, int max_q, int max_prefix, int max_own) {
   SharedPlan r = {};
-  if (max_prefix) plan_split(c, n_heads, T, G, std::max(1, T), max_prefix, &r.prefix, &r.prefix_keys);
   const int most = std::min(max_own + gran_of(c.page_size, 0) - 1, kMaxKeys);  // whole runs from where the prefix ends
-  plan_split(c, n_heads, T, B, max_q, most, &r.own, &r.own_keys);
+  r.own = plan_general(c, n_heads, T, B, max_q, most, false);
+  if (!max_prefix) return r;
+  r.prefix = plan_general(c, n_heads, T, G, std::max(1, T), max_prefix, true);
+  const int group = n_heads / c.n_heads;
+  if ((int64_t)T * group > kDecMaxRows) {
+    const bool codes = c.type != WAL_KV_BF16;
+    const int64_t tiles = ((int64_t)max_prefix + 127) / 128;
+    const int64_t pieces = c.n_heads * std::min<int64_t>(G * (((int64_t)T * group + kTcAttnRows - 1) / kTcAttnRows), (int64_t)T * group / kTcAttnRows + G);
+    const double step = codes ? 2.7 : 1.9, key = 2 * c.head_dim * (codes ? 1 : 2) + (codes ? 8 : 0);
+    const double own = 0.5 * B * c.n_heads * (double)max_own * key / 6e6 * kPlanSms;  // SM us
+    int64_t n = 1;
+    double best = 0;
+    for (int64_t s = 1; s <= tiles && s <= 128; ++s) {
+      const double rounds = (double)((pieces * s + kPlanSms - 1) / kPlanSms), each = ((double)((tiles + s - 1) / s) + 3) * step;
+      double cost = std::max(rounds * each, (pieces * s * each + own) / kPlanSms) + (double)T * n_heads * c.head_dim * 4 * s * 2 / 5.7e6;
+      if (pieces * s > kPlanSms / 2 && own > 0.3 * cost * kPlanSms) cost *= 1.2;
+      if (s == 1 || cost < best) {
+        n = s;
+        best = cost;
+      }
+    }
+    const int64_t keys = (tiles + n - 1) / n * 128;
+    r.prefix.keys = (int)std::min<int64_t>(keys, 0x7FFFFF80);
+    r.prefix.n = (int)((max_prefix + keys - 1) / keys);
+  }
   return r;
 }
 size_t shared_ws_bytes(const SharedPlan& r, int T, int n_heads, int head_dim) {
-  return T ? attn_ws_bytes(std::max(2, r.prefix + r.own), T, n_heads, head_dim) : kStatusWs;
+  return T ? attn_ws_bytes(std::max(2, r.prefix.n + r.own.n), T, n_heads, head_dim) : kStatusWs;
 }
 int check_shared(int G, int max_prefix, int max_own) {
   if (G < 1 || G > 65535 || max_prefix < 0 || max_own < 1) return fail(WAL_ERR_SHAPE, "1 <= G <= 65535, max_prefix >= 0 and max_own >= 1");
@@ -806,10 +899,7 @@ extern "C" size_t wal_attn_paged_window_workspace_bytes(const wal_kv_cache* cach
   if (check_cache(cache) != WAL_OK || check_window(window, sinks) != WAL_OK) return 0;
   if (check_attn(n_heads, cache->n_heads, cache->head_dim, T, B, max_q, max_kv, 1.f) != WAL_OK) return 0;
   const Window w = window_of(window, sinks, max_kv);
-  int n_split, split_keys;
-  plan_split(*cache, n_heads, T, B, max_q, most_keys(w, gran_of(cache->page_size, w.sinks), n_heads / cache->n_heads, max_q, max_kv),
-             &n_split, &split_keys);
-  return attn_ws_bytes(n_split, T, n_heads, cache->head_dim);
+  return attn_ws_bytes(plan_paged(*cache, n_heads, T, B, max_q, max_kv, w).n, T, n_heads, cache->head_dim);
 }
 
 extern "C" int wal_attn_paged_window(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
@@ -863,20 +953,20 @@ extern "C" int wal_attn_paged_shared(const wal_kv_cache* cache, const uint16_t* 
   p.clear = true;
   set_paged(p, cache, Q, n_heads, T, ldq, q_start, kv_len, table, ld_table, B, max_q, max_kv, scale, O, ldo);
   set_window(p, {true, kNoWindow, 0}, gran_of(cache->page_size, 0));
-  set_parts(p, r.prefix + r.own);
+  set_parts(p, r.prefix.n + r.own.n);
   p.group_start = group_start; p.prefix_len = prefix_len;
   p.n_groups = G; p.n_seqs = B;
   p.max_prefix = max_prefix; p.max_own = max_own;
-  if (r.prefix) {
+  if (r.prefix.n) {
     AttnParams first = p;
     first.phase = kPrefix;
     first.B = G;
     first.max_q = T;
-    first.n_split = r.prefix; first.split_keys = r.prefix_keys;
+    first.n_split = r.prefix.n; first.split_keys = r.prefix.keys;
     if ((st = launch_pieces(first, s))) return st;
   }
   p.phase = kOwn;
-  p.n_split = r.own; p.split_keys = r.own_keys;
-  p.part_first = r.prefix; p.prefix_keys = std::max(1, r.prefix_keys);
+  p.n_split = r.own.n; p.split_keys = r.own.keys;
+  p.part_first = r.prefix.n; p.prefix_keys = std::max(1, r.prefix.keys);
   return launch_attn(p, s);
 }

@@ -39,6 +39,7 @@ struct AttnParams {
   bool gen, tc;              // tc: the tensor-core kernel
   int window, sinks;         // a row sees its last `window` keys and the first `sinks`
   int gran;                  // keys of a piece are looked up in runs of this many, aligned where there are pages
+  int sinks_pad;             // the first keys' runs
   int piece_toks;            // new tokens of a piece of the tensor-core kernel at most
   int phase;
   int part_first, prefix_keys;  // kOwn: the prefix has part_first splits at most, of prefix_keys keys
@@ -138,29 +139,28 @@ __device__ __forceinline__ int attn_low(const AttnParams& p, const AttnSeq& s, i
 
 // The keys of a piece whose rows have limits from `first` to `last`, counted
 // without the gap between the first keys and the window: place v is key v below
-// sinks16 and key v + delta from there on.  Keys [low, ..) and [0, sinks) count, the
+// sinks_pad and key v + delta from there on.  Keys [low, ..) and [0, sinks) count, the
 // other places up to n are there for the alignment.  With a gap (delta > 0), every row
 // of the piece sees all of the first keys.
 struct AttnSpan {
   int low, delta, n;
 };
-__device__ __forceinline__ int attn_sinks16(const AttnParams& p) { return (p.sinks + 15) & ~15; }
 __device__ __forceinline__ AttnSpan attn_span(const AttnParams& p, const AttnSeq& s, int first, int last) {
   AttnSpan a;
   a.low = attn_low(p, s, first);
-  const int before = a.low - attn_sinks16(p);
+  const int before = a.low - p.sinks_pad;
   a.delta = before > 0 ? before & -p.gran : 0;
   a.n = max(0, last - a.delta);
   return a;
 }
-__device__ __forceinline__ int attn_key(int v, int sinks16, int delta) { return v < sinks16 ? v : v + delta; }
+__device__ __forceinline__ int attn_key(int v, int sinks_pad, int delta) { return v < sinks_pad ? v : v + delta; }
 // Splits that the keys of a sequence have in this launch (of one that has rows).  Of the
 // tensor-core kernel's pieces this is a bound: those beyond a piece's keys are empty.
 __device__ __forceinline__ int attn_splits(const AttnParams& p, const AttnSeq& s) {
   if (p.n_split == 1) return 1;
   int n;
   if (p.tc) {
-    const int64_t most = (int64_t)p.window + p.piece_toks + attn_sinks16(p) + p.gran;
+    const int64_t most = (int64_t)p.window + p.piece_toks + p.sinks_pad + p.gran;
     n = (int)min((int64_t)(s.len - (s.lo & -p.gran)), most);
   } else {
     n = attn_span(p, s, attn_limit<true>(p, s, 0), attn_limit<true>(p, s, s.n_q - 1)).n;

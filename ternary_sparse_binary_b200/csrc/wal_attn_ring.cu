@@ -32,18 +32,22 @@ struct RingCfg {
   static constexpr int keys = 16 * MT;
   static constexpr int scales = codes ? 2 * keys * 4 : 0;
   static constexpr int step = 2 * keys * row + scales;       // K, V, their scales
-  static constexpr int stages = row == 64 ? 4 : row == 128 ? (codes ? 2 : 4) : 2;
+  static constexpr int stages = D == 64 ? 3 : 2;
   static constexpr int ring = stages * step;                 // of a warp
   static constexpr int join = 8 * NT * (D + 4) * 4;          // a warp's sums, over its ring at the end
   static constexpr int warp = ring > join ? ring : join;
   static constexpr int smem = kDecWarps * warp;
-  static constexpr int ctas = NT == 1 ? 3 : 2;
+  static constexpr int ctas = NT > 1 ? 2 : D == 64 ? 4 : 3;  // of an SM; the split of the keys counts on it
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Zeros where the source is not there.
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+__device__ __forceinline__ void copy4_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
@@ -69,8 +73,8 @@ __device__ __forceinline__ void attn_ring(const AttnParams& p, uint8_t* smem) {
   constexpr int NW = D * (CODES ? 1 : 2) / 32;  // words of V per lane and key (of 8 lanes)
   constexpr int DT = D / 16;
   __shared__ float2 s_ml[kDecWarps][8 * NT];
-  const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const AttnSeq s = attn_seq<true>(p, b);
   if (p.clear) {
@@ -83,39 +87,55 @@ __device__ __forceinline__ void attn_ring(const AttnParams& p, uint8_t* smem) {
   if (rows == 0) return;
   const int first = attn_limit<true>(p, s, 0), last = attn_limit<true>(p, s, s.n_q - 1);
   const AttnSpan span = attn_span(p, s, first, last);
-  const int sinks16 = attn_sinks16(p);
   const int k0 = split * p.split_keys, k1 = min(span.n, k0 + p.split_keys);
+  const int whole_from = span.low - span.delta;  // some row sees every place from here on
   if (k0 >= k1 && split > 0) return;  // split 0 also answers for a sequence without keys
 
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * C::warp;
-  // The cache rows of a step's tiles, each of which lies in one page; a step ahead of
-  // its copies, which would wait for the table otherwise.
+  // The cache rows of a step's tiles, each of which lies in one page (with runs of 32
+  // keys or more, each pair of them); a step ahead of its copies, which would wait for
+  // the table otherwise.
   int64_t base[MT];
   auto find = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < MT; ++u)
-      base[u] = j0 + 16 * u < k1 ? attn_page_row(p, s.tab, h, attn_key(j0 + 16 * u, sinks16, span.delta)) : 0;
+      if ((u & 1) && p.gran >= 32)
+        base[u] = base[u - (u & 1)] + 16;
+      else
+        base[u] = j0 + 16 * u < k1 ? attn_page_row(p, s.tab, h, attn_key(j0 + 16 * u, p.sinks_pad, span.delta)) : 0;
   };
+  // A lane copies the chunk `ch` of rows r0, r0 + kRows, ...; r0 has no bit of kRows' multiples.
+  constexpr int kRows = 32 / CH, kCopies = 16 / kRows;
+  const int r0 = lane / CH, ch = lane % CH, from = r0 * ROW + 16 * ch;
   auto issue = [&](int j0, int slot) {
     const uint32_t dst = ring + (uint32_t)slot * C::step;
+    const bool whole = j0 + STEP <= k1 && j0 >= whole_from;  // some row sees every key of it
     if (j0 < k1) {
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
-        const int v0 = j0 + 16 * u, key0 = attn_key(v0, sinks16, span.delta);
-        auto seen = [&](int r) { return v0 + r < k1 && (key0 + r >= span.low || key0 + r < p.sinks); };
+        const int64_t at = base[u] * ROW + from;
+        const char *ks = static_cast<const char*>(p.k) + at, *vs = static_cast<const char*>(p.v) + at;
+        const uint32_t to = dst + (uint32_t)(16 * u) * ROW;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < 16 * CH / 32; ++i) {
-          const int r = (lane + 32 * i) / CH, ch = (lane + 32 * i) % CH;
-          const bool there = seen(r);
-          const int64_t at = there ? (base[u] + r) * ROW + 16 * ch : 0;
-          const uint32_t to = dst + (uint32_t)(16 * u) * ROW + place<ROW>(r, ch);
-          copy16(to, static_cast<const char*>(p.k) + at, there);
-          copy16(to + STEP * ROW, static_cast<const char*>(p.v) + at, there);
+          for (int i = 0; i < kCopies; ++i) {
+            copy16(to + place<ROW>(r0 | (i * kRows), ch), ks + i * kRows * ROW);
+            copy16(to + STEP * ROW + place<ROW>(r0 | (i * kRows), ch), vs + i * kRows * ROW);
+          }
+        } else {  // zeros for the others, whose slots lie in the same page
+          const int v0 = j0 + 16 * u, key0 = attn_key(v0, p.sinks_pad, span.delta);
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i) {
+            const int r = r0 | (i * kRows);
+            const bool there = v0 + r < k1 && (key0 + r >= span.low || key0 + r < p.sinks);
+            copy16_if(to + place<ROW>(r, ch), ks + i * kRows * ROW, there);
+            copy16_if(to + STEP * ROW + place<ROW>(r, ch), vs + i * kRows * ROW, there);
+          }
         }
         if (CODES) {  // K's scales, then V's
-          const int r = lane & 15;
-          const bool there = seen(r);
-          copy4(dst + 2 * STEP * ROW + (uint32_t)((lane >> 4) * STEP + 16 * u + r) * 4, (lane >> 4 ? p.vs : p.ks) + (there ? base[u] + r : 0), there);
+          const int r = lane & 15, v0 = j0 + 16 * u, key = attn_key(v0, p.sinks_pad, span.delta) + r;
+          copy4_if(dst + 2 * STEP * ROW + (uint32_t)((lane >> 4) * STEP + 16 * u + r) * 4, (lane >> 4 ? p.vs : p.ks) + base[u] + r,
+                   v0 + r < k1 && (key >= span.low || key < p.sinks));
         }
       }
     }
@@ -236,18 +256,18 @@ __device__ __forceinline__ void attn_ring(const AttnParams& p, uint8_t* smem) {
         vs[u][r] = CODES ? __uint_as_float(ptx::lds32(at + STEP * 4)) : 1.f;
         lv[u][r] = CODES ? lg2(fabsf(vs[u][r])) : 0.f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = sc[u][t][e + 2 * r];
-            x *= mult[t][e];
-            if (CODES) x *= ks;
-          }
+        for (int t = 0; t < NT; ++t) {
+          float2 f = make_float2(mult[t][0], mult[t][1]);
+          if (CODES) f = ptx::mul2(f, make_float2(ks, ks));
+          const float2 x = ptx::mul2(make_float2(sc[u][t][2 * r], sc[u][t][2 * r + 1]), f);
+          sc[u][t][2 * r] = x.x;
+          sc[u][t][2 * r + 1] = x.y;
+        }
       }
     if (j0 + STEP > lim_min || j0 < low_max) {  // keys a row does not see get -inf
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
-        const int v0 = j0 + 16 * u + gk, key0 = attn_key(j0 + 16 * u, sinks16, span.delta) + gk;
+        const int v0 = j0 + 16 * u + gk, key0 = attn_key(j0 + 16 * u, p.sinks_pad, span.delta) + gk;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll

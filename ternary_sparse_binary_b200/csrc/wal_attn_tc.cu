@@ -367,7 +367,7 @@ __device__ __forceinline__ void load_tiles(const AttnParams& p, int most, const 
       if (GEN) {  // boxes of p.gran places (a whole tile of a prompt without first keys), each a run of keys in one page
         box_rows = p.table || p.sinks ? p.gran : kTile;
         boxes = (cnt + box_rows - 1) / box_rows;
-        const int j0 = attn_key(kb + lane * box_rows, attn_sinks16(p), w.delta);
+        const int j0 = attn_key(kb + lane * box_rows, p.sinks_pad, w.delta);
         if (p.table && lane < boxes) page = attn_page(p, s.tab, j0);
         y0 = p.table ? j0 & ((1 << p.shift) - 1) : s.q0 + j0;
         hidden |= w.low - w.delta > p.sinks && kb < w.low - w.delta && kb + kTile > p.sinks;
@@ -1059,10 +1059,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   const float sl = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs + (GEN && C::codes ? 16 : 0)));
     softmax_rows<D, TYPE, GEN>(p, most, warp >> 2, sl, base, tmem, bars);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs - (GEN && C::codes ? 16 : 0)));
     if (warp == 8) {
       issue_mmas<D, TYPE, GEN>(p, most, base, tmem, bars);
     } else if (warp == 9) {
