@@ -532,7 +532,7 @@ void launch_decode(const AttnParams& p, const dim3& grid, cudaStream_t s) {
 template <bool GEN>
 int launch_combine(const AttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const bool shared = p.n_split + p.part_first > 6;
+  const bool shared = p.n_split + p.part_first > 6 && (!GEN || (int64_t)p.T * p.n_heads <= 1024);  // many rows keep the SMs busy alone
   const int rows = shared ? 1 : kRowWarps;  // of a CTA
   cfg.gridDim = dim3((unsigned)(((int64_t)p.max_q * p.n_heads + rows - 1) / rows), 1, (unsigned)p.B);
   cfg.blockDim = dim3(32 * kRowWarps);
@@ -814,12 +814,12 @@ int attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_h
 // The tensor-core kernel's CTAs take an SM each, and the other launch has what is left,
 // so a prefix is not spread over all of them: the split is the one with which the longer
 // of both is shortest, the prefix's own pieces (2.7 us a step of 128 8-bit keys, 1.9 of
-// bf16, three steps more a piece) and the sum of all work over the SMs, the other launch's
+// bf16, three steps more a piece, a third more beside other work) and the sum of all work over the SMs, the other launch's
 // at 6 TB/s of half its bounds.  More CTAs than half of the SMs, where two of them share
-// a pair of SMs, count a fifth more beside other work.  64 slots with up to 2048 tokens of
+// a pair of SMs, count a third more beside other work.  64 slots with up to 2048 tokens of
 // their own, 32 q heads of 128 on 8, behind 16384 shared int8 keys: in six, eight, nine
 // (which it takes), ten and sixteen splits 89, 74, 76, 85 and 87 us; over bf16 pages in
-// six, eight (nine), ten and twelve 81, 78, 80 and 83.
+// six, eight (seven), ten and twelve 81, 78, 80 and 83.
 struct SharedPlan {
   Split prefix, own;  // prefix.n is 0 where there is none
 };
@@ -840,8 +840,8 @@ SharedPlan plan_shared(const wal_kv_cache& c, int n_heads, int T, int B, int G, 
     double best = 0;
     for (int64_t s = 1; s <= tiles && s <= 128; ++s) {
       const double rounds = (double)((pieces * s + kPlanSms - 1) / kPlanSms), each = ((double)((tiles + s - 1) / s) + 3) * step;
-      double cost = std::max(rounds * each, (pieces * s * each + own) / kPlanSms) + (double)T * n_heads * c.head_dim * 4 * s * 2 / 5.7e6;
-      if (pieces * s > kPlanSms / 2 && own > 0.3 * cost * kPlanSms) cost *= 1.2;
+      double cost = std::max(1.3 * rounds * each, (pieces * s * each + own) / kPlanSms) + (double)T * n_heads * c.head_dim * 4 * s * 2 / 5.7e6;
+      if (pieces * s > kPlanSms / 2 && own > 0.3 * cost * kPlanSms) cost *= 1.3;
       if (s == 1 || cost < best) {
         n = s;
         best = cost;
