@@ -63,14 +63,51 @@ __device__ __forceinline__ float row_norm(const float (&v)[16], int lanes, float
   return r;
 }
 
+// Cosines and sines of a token, and the norms' weights, as the items take them: chunk j
+// of item `it` at [j][it], so that the lanes of a row read neighbouring chunks.  Angles:
+// {cos, cos, sin, sin} of two pairs.
+struct Angles {
+  float4 v[4][kMaxPairs / 8];
+};
+struct Weights {
+  float4 v[4][kMaxPairs / 8];
+};
+// rotate16 over them, its products contracted as they are there: the same bits.
+__device__ __forceinline__ void turn(float (&v)[16], int layout, const Angles& a, int it) {
+  if (layout == WAL_ROPE_HALF) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 t = a.v[j][it];
+      const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), minus = make_float2(-t.z, -t.w);
+      const float2 x = make_float2(v[2 * j], v[2 * j + 1]), y = make_float2(v[8 + 2 * j], v[9 + 2 * j]);
+      const float2 p = ptx::fma2(x, c, ptx::mul2(y, minus)), q = ptx::fma2(x, s, ptx::mul2(y, c));
+      v[2 * j] = p.x;
+      v[2 * j + 1] = p.y;
+      v[8 + 2 * j] = q.x;
+      v[9 + 2 * j] = q.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 t = a.v[j][it];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float c = e ? t.y : t.x, s = e ? t.w : t.z, x = v[4 * j + 2 * e], y = v[4 * j + 2 * e + 1];
+        v[4 * j + 2 * e] = x * c - y * s;
+        v[4 * j + 2 * e + 1] = y * c + x * s;
+      }
+    }
+  }
+}
+
 // Bound by bytes.  A CTA takes kTokens tokens (one where there are few: latency), a
 // thread the same item of each of them; all of them are loaded before the first
-// token's angles are worked out.
+// token's angles are worked out, and a round's loads before the round before is done.
 template <int XT, int TYPE, int kTokens>
 __global__ void __launch_bounds__(512) qkv_kernel(const __grid_constant__ QkvParams p) {
   constexpr int S = XT == WAL_F32 ? 4 : 2;
-  __shared__ float2 cs[kTokens * kMaxPairs];
-  __shared__ float weight[2][2 * kMaxPairs];
+  __shared__ Angles angle[kTokens];
+  __shared__ Weights weight[2];
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
   const int n = min(kTokens, (int)(p.T - t0));
   int slots[kTokens];
@@ -90,83 +127,107 @@ __global__ void __launch_bounds__(512) qkv_kernel(const __grid_constant__ QkvPar
   const int lanes = 1 << p.lanes_log2, rows = p.n_heads + p.n_kv_heads * (TYPE == kRows ? 1 : 2), per = rows << p.lanes_log2;
   const float inv_dim = 1.f / (float)p.head_dim;
   const bool norm = p.weight[0] != nullptr;
-  bool first = true;
-  for (int i = threadIdx.x; first || i - (int)threadIdx.x < per; i += blockDim.x) {
-    // whole warps go along for the shuffles
-    const int row = min(i >> p.lanes_log2, rows - 1), lane = i & (lanes - 1);
-    const int which = TYPE != kRows && row >= p.n_heads + p.n_kv_heads ? 2 : row >= p.n_heads;
-    const int h = row - (which == 0 ? 0 : which == 1 ? p.n_heads : p.n_heads + p.n_kv_heads);
-    const bool there = lane < p.items, live = there && i < per;
-    const int it = there ? lane : 0;
-    Rope r = p.rope;
-    if (which == 2) r.pairs = 0;
-    const ItemCols c = item_cols(r, it);
-    const char* x = static_cast<const char*>(which == 0 ? p.x[0] : which == 1 ? p.x[1] : p.x[2]);
-    const int64_t ld = which == 0 ? p.ld[0] : which == 1 ? p.ld[1] : p.ld[2];
-    Raw16<XT> raw[kTokens];
+  // a thread's item is the same in all of its rows
+  const int lane = threadIdx.x & (lanes - 1);
+  const bool there = lane < p.items;
+  const int it = there ? lane : 0;
+  Rope rope = p.rope, none = p.rope;
+  none.pairs = 0;
+  const ItemCols turned = item_cols(rope, it), plain = item_cols(none, it);
+  struct Place {
+    int which, h;
+    ItemCols c;
+  };
+  auto place = [&](int i) {
+    const int row = min(i >> p.lanes_log2, rows - 1);
+    Place x;
+    x.which = TYPE != kRows && row >= p.n_heads + p.n_kv_heads ? 2 : row >= p.n_heads;
+    x.h = row - (x.which == 0 ? 0 : x.which == 1 ? p.n_heads : p.n_heads + p.n_kv_heads);
+    x.c = x.which == 2 ? plain : turned;
+    return x;
+  };
+  Raw16<XT> raw[kTokens];
+  auto load = [&](const Place& x) {
+    const char* from = static_cast<const char*>(x.which == 0 ? p.x[0] : x.which == 1 ? p.x[1] : p.x[2]);
+    const int64_t ld = x.which == 0 ? p.ld[0] : x.which == 1 ? p.ld[1] : p.ld[2];
 #pragma unroll
     for (int t = 0; t < kTokens; ++t)
-      load16<XT>(x + (t0 + min(t, n - 1)) * ld * S, h * p.head_dim + c.a, h * p.head_dim + c.b, raw[t]);
-    if (first) {
-      first = false;
-      if (norm)
-        for (int j = threadIdx.x; j < 2 * p.head_dim; j += blockDim.x) {
-          const int k = j >= p.head_dim, col = j - (k ? p.head_dim : 0);
-          const void* w = k ? p.weight[1] : p.weight[0];
-          weight[k][col] = p.weight_type == WAL_F32 ? __ldg(static_cast<const float*>(w) + col)
-                                                    : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(w) + col) << 16);
-        }
-      if (p.rope.pairs) angles(p.rope, p.positions, t0, n, cs);
-      __syncthreads();
+      load16<XT>(from + ((t0 + min(t, n - 1)) * ld + x.h * p.head_dim) * S, x.c.a, x.c.b, raw[t]);
+  };
+  load(place(threadIdx.x));
+  if (norm)
+    for (int j = threadIdx.x; j < 32 * p.items; j += blockDim.x) {
+      const int k = j >= 16 * p.items, e = j - (k ? 16 * p.items : 0), item = e >> 4;
+      const ItemCols c = item_cols(rope, item);
+      const int col = (e & 8) ? c.b + (e & 7) : c.a + (e & 7);
+      const void* w = k ? p.weight[1] : p.weight[0];
+      reinterpret_cast<float*>(&weight[k].v[(e & 15) >> 2][item])[e & 3] =
+          p.weight_type == WAL_F32 ? __ldg(static_cast<const float*>(w) + col)
+                                   : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(w) + col) << 16);
     }
+  for (int q = threadIdx.x; q < n * rope.pairs; q += blockDim.x) {
+    const int t = q / rope.pairs, i = q - t * rope.pairs;
+    const float2 cs = rope_angle(rope, __ldg(p.positions + t0 + t), i);
+    float* f = reinterpret_cast<float*>(&angle[t].v[(i & 7) >> 1][i >> 3]) + (i & 1);
+    f[0] = cs.x;
+    f[2] = cs.y;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i - (int)threadIdx.x < per; i += blockDim.x) {  // whole warps go along for the shuffles
+    const Place x = place(i);
+    const bool live = there && i < per;
+    float v[kTokens][16];
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t) unpack16<XT>(raw[t], v[t]);
+    if (i - (int)threadIdx.x + (int)blockDim.x < per) load(place(i + blockDim.x));
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) {
-      float v[16];
-      unpack16<XT>(raw[t], v);
       if (!there)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        for (int e = 0; e < 16; ++e) v[t][e] = 0.f;
       if (norm) {
-        const float rn = row_norm(v, lanes, inv_dim, p.eps);
-        if (which < 2) {
-          const float4* wa = reinterpret_cast<const float4*>(weight[which] + c.a);
-          const float4* wb = reinterpret_cast<const float4*>(weight[which] + c.b);
+        const float rn = row_norm(v[t], lanes, inv_dim, p.eps);
+        if (x.which < 2) {
+          const float2 r2 = make_float2(rn, rn);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 w = e < 2 ? wa[e] : wb[e - 2];
-            v[4 * e] = v[4 * e] * rn * w.x;
-            v[4 * e + 1] = v[4 * e + 1] * rn * w.y;
-            v[4 * e + 2] = v[4 * e + 2] * rn * w.z;
-            v[4 * e + 3] = v[4 * e + 3] * rn * w.w;
+          for (int j = 0; j < 4; ++j) {
+            const float4 w = weight[x.which].v[j][it];
+            const float2 y = ptx::mul2(ptx::mul2(make_float2(v[t][4 * j], v[t][4 * j + 1]), r2), make_float2(w.x, w.y));
+            const float2 z = ptx::mul2(ptx::mul2(make_float2(v[t][4 * j + 2], v[t][4 * j + 3]), r2), make_float2(w.z, w.w));
+            v[t][4 * j] = y.x;
+            v[t][4 * j + 1] = y.y;
+            v[t][4 * j + 2] = z.x;
+            v[t][4 * j + 3] = z.y;
           }
         }
       }
-      if (c.rot) rotate16(v, r, it, cs + t * kMaxPairs);
-      if (TYPE == kRows || which == 0) {
+      if (x.c.rot) turn(v[t], rope.layout, angle[t], it);
+      if (TYPE == kRows || x.which == 0) {
         if (live && t < n) {
-          uint16_t* y = (which == 0 ? p.out[0] : p.out[1]) + (t0 + t) * (which == 0 ? p.ldo[0] : p.ldo[1]) + h * p.head_dim;
-          *reinterpret_cast<uint4*>(y + c.a) = pack8(v);
-          *reinterpret_cast<uint4*>(y + c.b) = pack8(v + 8);
+          uint16_t* y = (x.which == 0 ? p.out[0] : p.out[1]) + (t0 + t) * (x.which == 0 ? p.ldo[0] : p.ldo[1]) + x.h * p.head_dim;
+          *reinterpret_cast<uint4*>(y + x.c.a) = pack8(v[t]);
+          *reinterpret_cast<uint4*>(y + x.c.b) = pack8(v[t] + 8);
         }
       }
       if (TYPE == kRows) continue;
       const int slot = slots[t];
-      const bool store = live && which > 0 && (uint32_t)slot < p.n_slots;
-      char* cache = static_cast<char*>(which == 2 ? p.cache[1] : p.cache[0]);
-      const int64_t crow = (((int64_t)(slot >> p.shift) * p.n_kv_heads + h) << p.shift) + (slot & ((1 << p.shift) - 1));
+      const bool store = live && x.which > 0 && (uint32_t)slot < p.n_slots;
+      char* cache = static_cast<char*>(x.which == 2 ? p.cache[1] : p.cache[0]);
+      const int64_t crow = (((int64_t)(slot >> p.shift) * p.n_kv_heads + x.h) << p.shift) + (slot & ((1 << p.shift) - 1));
       if (TYPE == WAL_KV_BF16) {
         if (store) {
           uint16_t* d = reinterpret_cast<uint16_t*>(cache) + crow * p.head_dim;
-          *reinterpret_cast<uint4*>(d + c.a) = pack8(v);
-          *reinterpret_cast<uint4*>(d + c.b) = pack8(v + 8);
+          *reinterpret_cast<uint4*>(d + x.c.a) = pack8(v[t]);
+          *reinterpret_cast<uint4*>(d + x.c.b) = pack8(v[t] + 8);
         }
         continue;
       }
-      if (__all_sync(0xffffffffu, which == 0)) continue;
+      if (__all_sync(0xffffffffu, x.which == 0)) continue;
       // the largest magnitude as bits: infinities and NaN come out on top
       uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(v[t][e]) & 0x7FFFFFFFu);
       for (int o = lanes >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const bool bad = top >= 0x7F800000u;
       const float scale = fmaxf(__fdiv_rn(__uint_as_float(bad ? 0u : top), TYPE == WAL_KV_INT8 ? 127.f : 448.f), 1.1754943508222875e-38f);
@@ -175,43 +236,49 @@ __global__ void __launch_bounds__(512) qkv_kernel(const __grid_constant__ QkvPar
       const float inv = __frcp_rn(scale);
       if (scale < 0x1p-100f) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __fdiv_rn(v[e], scale);
+        for (int e = 0; e < 16; ++e) v[t][e] = __fdiv_rn(v[t][e], scale);
       } else {
         const float2 inv2 = make_float2(inv, inv), minus = make_float2(-scale, -scale);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 x = make_float2(v[2 * e], v[2 * e + 1]);
-          const float2 y = ptx::mul2(x, inv2), z = ptx::fma2(ptx::fma2(y, minus, x), inv2, y);
-          v[2 * e] = z.x;
-          v[2 * e + 1] = z.y;
+          const float2 u = make_float2(v[t][2 * e], v[t][2 * e + 1]);
+          const float2 y = ptx::mul2(u, inv2), z = ptx::fma2(ptx::fma2(y, minus, u), inv2, y);
+          v[t][2 * e] = z.x;
+          v[t][2 * e + 1] = z.y;
         }
       }
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = codes2<TYPE>(v[4 * e], v[4 * e + 1]) | (codes2<TYPE>(v[4 * e + 2], v[4 * e + 3]) << 16);
+      for (int e = 0; e < 4; ++e) w[e] = codes2<TYPE>(v[t][4 * e], v[t][4 * e + 1]) | (codes2<TYPE>(v[t][4 * e + 2], v[t][4 * e + 3]) << 16);
       if (bad) w[0] = w[1] = w[2] = w[3] = 0;
       if (store) {
         uint8_t* d = reinterpret_cast<uint8_t*>(cache) + crow * p.head_dim;
-        *reinterpret_cast<uint2*>(d + c.a) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(d + c.b) = make_uint2(w[2], w[3]);
-        if (it == 0) (which == 2 ? p.scale[1] : p.scale[0])[crow] = bad ? __int_as_float(0x7FC00000) : scale;
+        *reinterpret_cast<uint2*>(d + x.c.a) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(d + x.c.b) = make_uint2(w[2], w[3]);
+        if (it == 0) (x.which == 2 ? p.scale[1] : p.scale[0])[crow] = bad ? __int_as_float(0x7FC00000) : scale;
       }
     }
   }
 }
 
-constexpr int kManyTokens = 2, kFewTokens = 148 * 4;
+// Up to kFewTokens tokens leave SMs idle: one CTA a token, wide, for latency.  More of
+// them: CTAs of 128 threads (16381 tokens of 32 + 16 fp32 heads into e4m3: 107 us; 192
+// threads 138, 256 the same, 96 108).  Two tokens a CTA halve the weights' loads but
+// double the registers: bf16 rows gain (8191 tokens of 80 heads: 57 us, 61 with one), fp32
+// rows lose (the former 94 us with one).
+constexpr int kFewTokens = 148 * 4;
 
 template <int XT, int TYPE>
 void launch_qkv(const QkvParams& p, cudaStream_t s) {
   const int per = (p.n_heads + p.n_kv_heads * (TYPE == kRows ? 1 : 2)) << p.lanes_log2;
   const bool few = p.T <= kFewTokens;
-  const int most = few ? 512 : 256, rounds = (per + most - 1) / most;
+  constexpr int kMany = XT == WAL_F32 ? 1 : 2;
+  const int most = few ? 512 : 128, rounds = (per + most - 1) / most;
   const int threads = ((per + rounds - 1) / rounds + 31) / 32 * 32;  // whole warps, in equal rounds
   if (few)
     qkv_kernel<XT, TYPE, 1><<<p.T, threads, 0, s>>>(p);
   else
-    qkv_kernel<XT, TYPE, kManyTokens><<<(p.T + kManyTokens - 1) / kManyTokens, threads, 0, s>>>(p);
+    qkv_kernel<XT, TYPE, kMany><<<(p.T + kMany - 1) / kMany, threads, 0, s>>>(p);
 }
 
 int check_norm(const wal_head_norm* n, int head_dim) {
