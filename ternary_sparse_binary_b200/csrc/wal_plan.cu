@@ -3,10 +3,12 @@
 //
 // Sequences take pages and rows in order, so everything is a prefix sum over them.
 // It moves a few bytes for each sequence and row and is bound by the chain of its
-// loads and barriers.  One CTA does a small step, a cluster of eight a large one:
-// each CTA sums its share of the sequences, the totals go round over distributed
-// shared memory, and then pages and rows are dealt out evenly, each finding its
-// sequence by bisection of the sums.
+// loads and barriers: 2.9 us of a graph for 25 sequences of a token each, 15.4 for 1500
+// with 70000 rows and 8000 pages taken or given back.  One CTA does a small step, a
+// cluster of eight a large one (of sixteen: 13.6 us, but not every device has it): each
+// CTA sums its share of the sequences, the totals go round over distributed shared
+// memory, and then pages and rows are dealt out evenly to warps, which find their
+// sequences in the sums.
 #include "wal_kv.h"
 
 #include <algorithm>
@@ -37,7 +39,8 @@ struct PlanParams {
   int64_t ld_table;
   int B, T, shift, n_pages, max_kv;
   int per;         // sequences of a CTA
-  bool starts;     // q_start fits in shared memory
+  bool starts;     // every sequence's place fits in shared memory
+  bool wide;       // positions and slots are 16-byte aligned
 };
 
 // What a sequence asks for: rows, pages to take, pages to give back.  One whose
@@ -70,25 +73,62 @@ struct Sums {
 };
 __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return min(a + b, kMost); }
 
-// The last place i of sums[0 .. n) (not falling, the first is 0) with sums[i] <= v.
-__device__ __forceinline__ int find(const uint32_t* sums, int n, uint32_t v) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sums[mid] <= v)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
+// The sums up to and with each lane's.
+__device__ __forceinline__ Sums warp_sums(Sums s, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, s.v[k], o);
+      if (lane >= o) s.v[k] = add(s.v[k], up);
+    }
+  return s;
 }
+
+// For each of a lane's four values the last place i of [0, n) with at(i) <= v[e]; at does
+// not fall, and at(0) is 0.  The warp's values lie between `first` and `last`: it looks
+// for the places of these two with a probe a lane, then each lane bisects between them,
+// all in the same steps.  No load is behind a branch: a step is one latency.
+constexpr int kDeal = 4;
+template <typename At>
+__device__ __forceinline__ void find(int n, uint32_t first, uint32_t last, int lane, const uint32_t (&v)[kDeal], int (&place)[kDeal], At at) {
+  int lo = 0, hi = 0;
+  for (int size = n; size > 1;) {
+    const int step = (size + 31) >> 5, i = lo + lane * step, j = hi + lane * step;
+    const uint32_t ai = at(min(i, n - 1)), aj = at(min(j, n - 1));
+    lo += (__popc(__ballot_sync(0xffffffffu, lane * step < size && i < n && ai <= first)) - 1) * step;
+    hi += (__popc(__ballot_sync(0xffffffffu, lane * step < size && j < n && aj <= last)) - 1) * step;
+    size = step;
+  }
+  int w = lo, x = lo, y = lo, z = lo;
+#pragma unroll 1
+  for (int step = hi > lo ? 1 << (31 - __clz(hi - lo)) : 0; step > 0; step >>= 1) {
+    const uint32_t aw = at(min(w + step, hi)), ax = at(min(x + step, hi)), ay = at(min(y + step, hi)), az = at(min(z + step, hi));
+    if (w + step <= hi && aw <= v[0]) w += step;
+    if (x + step <= hi && ax <= v[1]) x += step;
+    if (y + step <= hi && ay <= v[2]) y += step;
+    if (z + step <= hi && az <= v[3]) z += step;
+  }
+  place[0] = w;
+  place[1] = x;
+  place[2] = y;
+  place[3] = z;
+}
+
+// Where a sequence's rows begin, and what makes a row's number its position.
+struct Place {
+  uint32_t start;
+  int to_position;
+};
 
 template <int C>
 __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const __grid_constant__ PlanParams p) {
-  extern __shared__ uint32_t dyn[];
-  __shared__ Sums s_warp[32], s_total, s_in;
+  extern __shared__ __align__(8) uint32_t dyn[];
+  __shared__ Sums s_warp[32], s_total[C], s_in;
   __shared__ int s_bad;
-  uint32_t *s_rows = dyn, *s_take = dyn + p.per, *s_give = dyn + 2 * p.per, *s_len = dyn + 3 * p.per, *s_start = dyn + 4 * p.per;
+  Place* s_place = reinterpret_cast<Place*>(dyn);  // of every sequence
+  uint32_t* s_rows = dyn + (p.starts ? 2 * p.B : 0);  // of this CTA's
+  uint32_t *s_take = s_rows + p.per, *s_give = s_take + p.per, *s_len = s_give + p.per, *s_new = s_len + p.per;
   const cg::cluster_group cluster = cg::this_cluster();
   auto barrier = [&] {
     if (C > 1)
@@ -104,6 +144,7 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const __grid_constant
     s_bad = 0;
     s_in = {};
   }
+  if (C > 1) cluster.barrier_arrive();
   const int n_free = *p.n_free;
   bool bad = false;
 
@@ -116,49 +157,38 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const __grid_constant
       a = ask(p, lo + i);
       bad |= a.bad;
     }
-    const Sums own = {{a.rows, a.take, a.give}};
-    Sums sum = own;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint32_t up = __shfl_up_sync(0xffffffffu, sum.v[k], o);
-        if (lane >= o) sum.v[k] = add(sum.v[k], up);
-      }
+    const Sums sum = warp_sums({{a.rows, a.take, a.give}}, lane);
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    Sums before = carry, all = carry;
-    for (int w = 0; w < n_warps; ++w)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (w == warp) before.v[k] = all.v[k];
-        all.v[k] = add(all.v[k], s_warp[w].v[k]);
-      }
-    carry = all;
-    // what comes before is the inclusive sum of the lane below
+    const Sums warps = warp_sums(lane < n_warps ? s_warp[lane] : Sums{}, lane);
+    // what comes before: the chunks before, the warps below, the lanes below
+    Sums before;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const uint32_t up = __shfl_up_sync(0xffffffffu, sum.v[k], 1);
-      before.v[k] = add(before.v[k], lane ? up : 0);
+      const uint32_t below = __shfl_sync(0xffffffffu, warps.v[k], (warp - 1) & 31), up = __shfl_up_sync(0xffffffffu, sum.v[k], 1);
+      before.v[k] = add(add(carry.v[k], warp ? below : 0), lane ? up : 0);
+      carry.v[k] = add(carry.v[k], __shfl_sync(0xffffffffu, warps.v[k], 31));
     }
     if (i < mine) {
       s_rows[i] = before.v[0];
       s_take[i] = before.v[1];
       s_give[i] = before.v[2];
       s_len[i] = (uint32_t)a.len;
+      s_new[i] = (uint32_t)a.n_new;
     }
     __syncthreads();
   }
-  if (tid == 0) s_total = carry;
-  barrier();
-  Sums base = {}, total = {};
-#pragma unroll
-  for (int r = 0; r < C; ++r) {
-    const Sums t = *of(&s_total, r);
+  Sums base = {}, total = carry;
+  if (C > 1) {  // the CTAs' totals go round
+    cluster.barrier_wait();
+    if (tid < C) *of(s_total + rank, tid) = carry;
+    barrier();
+    const Sums sum = warp_sums(lane < C ? s_total[lane] : Sums{}, lane);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      if (r == rank) base.v[k] = total.v[k];
-      total.v[k] = add(total.v[k], t.v[k]);
+      const uint32_t below = __shfl_sync(0xffffffffu, sum.v[k], (rank - 1) & 31);
+      base.v[k] = rank ? below : 0;
+      total.v[k] = __shfl_sync(0xffffffffu, sum.v[k], 31);
     }
   }
   // who goes in: all, or the sequences before the first that finds too little
@@ -192,65 +222,93 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const __grid_constant
   const uint32_t give = sound ? carry.v[2] : 0;
   for (int i = tid; i < mine; i += blockDim.x) {
     const uint32_t start = add(base.v[0], s_rows[i]);
-    const int b = lo + i, m = p.n_new[b];
-    const uint32_t want = i + 1 < mine ? s_rows[i + 1] - s_rows[i] : carry.v[0] - s_rows[i];
-    const bool trim = m < 0 && sound && (int64_t)s_len[i] + m >= 0 && (int)s_len[i] >= 0 && (int)s_len[i] <= p.max_kv;
-    const int len = (int)s_len[i];
-    int after = trim ? len + m : len;
-    if (want && start < rows && want <= rows - start) after = len + (int)want;
+    const int b = lo + i, len = (int)s_len[i], m = (int)s_new[i];  // 0 new tokens where a value is out of range
+    int after = m < 0 && sound ? len + m : len;
+    if (m > 0 && start < rows && (uint32_t)m <= rows - start) after = len + m;
     p.kv_len_out[b] = after;
     const uint32_t s = min(start, rows);
     p.q_start[b] = (int)s;
-    if (p.starts) for (int r = 0; r < C; ++r) of(s_start, r)[b] = s;
+    if (p.starts) {
+      const Place place = {s, len - (int)s};
+      for (int r = 0; r < C; ++r) of(s_place, r)[b] = place;
+    }
   }
   if (rank == C - 1 && tid == 0) p.q_start[p.B] = (int)rows;
-  for (uint32_t k = tid; k < give; k += blockDim.x) {
-    const int i = find(s_give, mine, k);
-    const uint32_t end = i + 1 < mine ? s_give[i + 1] : carry.v[2];
-    const uint32_t at = pages_of((int)s_len[i], p.shift) - (end - k);
-    const int page = p.table[(lo + i) * p.ld_table + at];
-    bad |= (uint32_t)page >= (uint32_t)p.n_pages;
-    p.free_pages[(uint32_t)n_free + base.v[2] + k] = page;
-  }
-  if (total.v[2]) barrier();
-  // taken pages, from the top of the list
-  const uint32_t taken = take > base.v[1] ? min(take - base.v[1], carry.v[1]) : 0;
-  for (uint32_t k = tid; k < taken; k += blockDim.x) {
-    const int i = find(s_take, mine, k);
-    const int page = __ldcg(p.free_pages + (held - 1 - base.v[1] - k));
-    bad |= (uint32_t)page >= (uint32_t)p.n_pages;
-    p.table[(lo + i) * p.ld_table + pages_of((int)s_len[i], p.shift) + (k - s_take[i])] = page;
-  }
-  barrier();
-  // rows
-  for (int t = rank * blockDim.x + tid; t < p.T; t += C * blockDim.x) {
-    int pos = 0, slot = -1;
-    if ((uint32_t)t < rows) {
-      int b;
-      uint32_t start, end;
-      if (p.starts) {
-        b = find(s_start, p.B, (uint32_t)t);
-        start = s_start[b];
-        end = b + 1 < p.B ? s_start[b + 1] : rows;
-      } else {
-        int l = 0, h = p.B;
-        while (h - l > 1) {
-          const int mid = (l + h) >> 1;
-          if (__ldcg(p.q_start + mid) <= t) l = mid; else h = mid;
-        }
-        b = l;
-        start = (uint32_t)__ldcg(p.q_start + b);
-        end = (uint32_t)__ldcg(p.q_start + b + 1);
+  // Pages of this CTA's sequences, a run of 32 * kDeal a warp
+  auto deal = [&](const uint32_t* sums, uint32_t n, auto load, auto store) {
+    for (uint32_t k0 = warp * 32 * kDeal; k0 < n; k0 += n_warps * 32 * kDeal) {
+      uint32_t k[kDeal];
+      int i[kDeal], page[kDeal];
+#pragma unroll
+      for (int e = 0; e < kDeal; ++e) k[e] = min(k0 + 32 * e + lane, n - 1);
+      find(mine, k0, min(k0 + 32 * kDeal, n) - 1, lane, k, i, [&](int j) { return sums[j]; });
+#pragma unroll
+      for (int e = 0; e < kDeal; ++e) page[e] = load(k[e], i[e], k[e] - sums[i[e]]);
+#pragma unroll
+      for (int e = 0; e < kDeal; ++e) {
+        if (k0 + 32 * e + lane >= n) continue;
+        bad |= (uint32_t)page[e] >= (uint32_t)p.n_pages;
+        store(k[e], i[e], k[e] - sums[i[e]], page[e]);
       }
-      pos = __ldcg(p.kv_len_out + b) - (int)(end - start) + (t - (int)start);
-      const int page = __ldcg(p.table + b * p.ld_table + (pos >> p.shift));
-      if ((uint32_t)page < (uint32_t)p.n_pages)
-        slot = (page << p.shift) + (pos & ((1 << p.shift) - 1));
-      else
-        bad = true;
     }
-    p.positions[t] = pos;
-    p.slots[t] = slot;
+  };
+  // a sequence's entry of the table: `nth` of those behind its pages after (given) or before (taken)
+  auto entry = [&](int i, int len, uint32_t nth) { return p.table + (lo + i) * p.ld_table + (pages_of(len, p.shift) + nth); };
+  deal(s_give, give, [&](uint32_t, int i, uint32_t nth) { return *entry(i, (int)(s_len[i] + s_new[i]), nth); },
+       [&](uint32_t k, int, uint32_t, int page) { p.free_pages[(uint32_t)n_free + base.v[2] + k] = page; });
+  if (total.v[2]) barrier();
+  // taken from the top of the list
+  const uint32_t taken = take > base.v[1] ? min(take - base.v[1], carry.v[1]) : 0;
+  deal(s_take, taken, [&](uint32_t k, int, uint32_t) { return __ldcg(p.free_pages + (held - 1 - base.v[1] - k)); },
+       [&](uint32_t, int i, uint32_t nth, int page) { *entry(i, (int)s_len[i], nth) = page; });
+  barrier();
+  // rows, likewise over all CTAs, four neighbours a lane
+  for (int64_t t0 = (int64_t)(rank * n_warps + warp) * 32 * kDeal; t0 < p.T; t0 += C * n_warps * 32 * kDeal) {
+    const int64_t t = t0 + kDeal * lane;
+    int pos[kDeal], slot[kDeal], b[kDeal];
+    uint32_t v[kDeal];
+#pragma unroll
+    for (int e = 0; e < kDeal; ++e) {
+      v[e] = min((uint32_t)t + e, rows - 1);
+      pos[e] = 0;
+      slot[e] = -1;
+    }
+    if (t0 < rows) {
+      const uint32_t last = min((uint32_t)t0 + 32 * kDeal, rows) - 1;
+      if (p.starts)
+        find(p.B, (uint32_t)t0, last, lane, v, b, [&](int j) { return s_place[j].start; });
+      else
+        find(p.B, (uint32_t)t0, last, lane, v, b, [&](int j) { return (uint32_t)__ldcg(p.q_start + j); });
+#pragma unroll
+      for (int e = 0; e < kDeal; ++e) {
+        const int at = (int)v[e] + (p.starts ? s_place[b[e]].to_position : __ldcg(p.kv_len_out + b[e]) - __ldcg(p.q_start + b[e] + 1));
+        const int page = __ldcg(p.table + b[e] * p.ld_table + (at >> p.shift));
+        const bool there = (uint32_t)t + e < rows;
+        pos[e] = there ? at : 0;
+        slot[e] = there ? page : -1;
+      }
+#pragma unroll
+      for (int e = 0; e < kDeal; ++e) {
+        if ((uint32_t)t + e >= rows) continue;
+        if ((uint32_t)slot[e] < (uint32_t)p.n_pages) {
+          slot[e] = (slot[e] << p.shift) + (pos[e] & ((1 << p.shift) - 1));
+        } else {
+          slot[e] = -1;
+          bad = true;
+        }
+      }
+    }
+    if (p.wide && t + kDeal <= p.T) {
+      *reinterpret_cast<int4*>(p.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(p.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kDeal; ++e)
+        if (t + e < p.T) {
+          p.positions[t + e] = pos[e];
+          p.slots[t + e] = slot[e];
+        }
+    }
   }
   if (bad) atomicOr(of(&s_bad, 0), 1);
   barrier();
@@ -260,9 +318,12 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const __grid_constant
   }
 }
 
-constexpr int kSmall = 1024;    // sequences, and
-constexpr int kSmallRows = 8192;  // rows of a step that one CTA does
-constexpr int kStarts = 24576;  // sequences whose starts fit in shared memory beside the sums
+// A step that one CTA does: 256 sequences and 3439 rows 8.3 us against 9.9 of the
+// cluster, 100 and 6359 8.2 against 9.3; 1000 and 3781 rows, with many pages given back,
+// 15.6 against 12.7.
+constexpr int kSmall = 512;       // sequences
+constexpr int kSmallRows = 8192;  // rows
+constexpr int kStarts = 16384;  // sequences whose places fit in shared memory beside the sums
 
 }  // namespace
 }  // namespace wal
@@ -297,13 +358,14 @@ extern "C" int wal_kv_plan(const wal_kv_cache* cache, const int32_t* n_new, cons
   p.B = B; p.T = T; p.max_kv = max_kv;
   p.shift = log2_of(cache->page_size); p.n_pages = cache->n_pages;
   p.starts = B <= kStarts;
+  p.wide = !misaligned(positions, 16) && !misaligned(slots, 16);
   const bool small = B <= kSmall && T <= kSmallRows;
   p.per = small ? B : (B + kCluster - 1) / kCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(small ? 1 : kCluster);
   const int most = std::min(kMaxThreads, (std::max(B, T) + 31) / 32 * 32);
   cfg.blockDim = dim3(small ? most : kMaxThreads);
-  cfg.dynamicSmemBytes = (size_t)4 * (4 * p.per + (p.starts ? B : 0));
+  cfg.dynamicSmemBytes = (size_t)4 * (5 * p.per + (p.starts ? 2 * B : 0));
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
