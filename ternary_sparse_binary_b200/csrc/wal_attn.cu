@@ -405,17 +405,17 @@ __global__ void __launch_bounds__(32 * kDecWarps, TYPE == WAL_KV_BF16 && NT == 1
 // Add the splits of a row, and report index values out of range.  PER warps of
 // the CTA share a row, each its splits in order, joined in order: one where
 // there are few splits, four where a warp alone would wait for one load after
-// the other.
+// the other.  The index arrays are older than the first kernel: they are read
+// while it still runs.
 template <int D, int PER, bool GEN>
 __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __grid_constant__ AttnParams p) {
   constexpr int VPL = D / 32;
   __shared__ float s_o[PER > 1 ? kRowWarps : 1][D];
   __shared__ float s_l[PER > 1 ? kRowWarps : 1];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const AttnSeq s = attn_seq<GEN>(p, b);
+  const AttnSeq s = attn_seq<GEN, true>(p, b);
+  bool bad = s.bad;
   if (blockIdx.x == 0) {  // the first kernel cleared the status word; what it skipped is reported here
-    bool bad = s.bad;
     const int pages = (s.len + (1 << p.shift) - 1) >> p.shift;
     auto look = [&](int row, int from, int to) {
       for (int i = from + threadIdx.x; i < to; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + row * p.ld_table + i) >= (uint32_t)p.n_pages;
@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
       look(s.head, 0, (first + (1 << p.shift) - 1) >> p.shift);
       look(b, low >> p.shift, pages);
     }
-    if (bad) attn_report(p.status);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && bad) attn_report(p.status);
   const int row = blockIdx.x * (kRowWarps / PER) + warp / PER;  // (token, head)
   if (s.bad || row >= s.n_q * p.n_heads) return;                // PER > 1: the whole CTA
   const int tok = row / p.n_heads, head = row - tok * p.n_heads;
@@ -441,6 +442,26 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
   }
   const int64_t pr = attn_part_row(p, s, tok, head), stride = (int64_t)p.T * p.n_heads;
   auto part = [&](int i) { return pr + (GEN && i >= prefix ? i + gap : i) * stride; };
+  // the first sums are loaded before the largest maximum is known
+  constexpr int kAhead = 4;
+  float2 ml[kAhead];
+  float v[kAhead][VPL];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t at = part(min(i0 + u * PER, n - 1));
+      ml[u] = p.part_ml[at];
+      const float* src = p.part_o + at * D + lane * VPL;
+      if (VPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[u][0] = x.x; v[u][1] = x.y; v[u][VPL - 2] = x.z; v[u][VPL - 1] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[u][0] = x.x; v[u][1] = x.y;
+      }
+    }
+  };
+  load(warp % PER);
   float mm = -INFINITY;
   for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[part(i)].x);
 #pragma unroll
@@ -449,18 +470,17 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
   float acc[VPL], ll = 0.f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int i = warp % PER; i < n; i += PER) {
-    const float2 ml = p.part_ml[part(i)];
-    const float* src = p.part_o + part(i) * D + lane * VPL;
-    float v[VPL];
+#pragma unroll 1
+  for (int i = warp % PER; i < n; i += kAhead * PER) {
+    if (i >= PER) load(i);
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) v[k] = src[k];
-    const bool none = ml.x == -INFINITY && ml.y == 0.f;  // the row sees nothing of this split
-    const float f = exp2f(ml.x - ref);
-    ll += none ? 0.f : f * ml.y;
+    for (int u = 0; u < kAhead; ++u) {
+      const bool none = i + u * PER >= n || (ml[u].x == -INFINITY && ml[u].y == 0.f);  // the row sees nothing of this split
+      const float f = exp2f(ml[u].x - ref);
+      ll += none ? 0.f : f * ml[u].y;
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) acc[k] += none ? 0.f : f * v[k];
+      for (int k = 0; k < VPL; ++k) acc[k] += none ? 0.f : f * v[u][k];
+    }
   }
   if (PER > 1) {
 #pragma unroll

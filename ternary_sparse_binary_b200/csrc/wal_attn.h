@@ -79,7 +79,10 @@ __device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup
   r.q1 = p.q_start[r.last];
   return r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.T;
 }
-template <bool GEN = false>
+// WARP: the lanes of a warp ask for one sequence and look for its group together.  Loads
+// come before the checks of what others gave, so that they wait for one another as little
+// as they can.
+template <bool GEN = false, bool WARP = false>
 __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
   AttnSeq s = {0, 0, 0, true};
   if (GEN) {
@@ -97,18 +100,36 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
     }
   }
   const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > p.T || q1 - q0 > p.max_q) return s;
-  const int len = p.kv_len ? p.kv_len[b] : q1 - q0;
-  if (len < 0 || len > p.max_kv) return s;
-  if (GEN && p.phase == kOwn) {
-    int g = 0, end = p.n_groups;  // the last group that starts at b or before
-    while (end - g > 1) {
-      const int mid = (g + end) >> 1;
-      if (p.group_start[mid] <= b) g = mid; else end = mid;
+  int len = p.kv_len ? p.kv_len[b] : 0;
+  int g = 0;
+  if (GEN && p.phase == kOwn) {  // the last group that starts at b or before
+    int end = p.n_groups;
+    if (WARP) {
+      const int lane = threadIdx.x & 31;
+      for (int size = end; size > 1;) {
+        const int step = (size + 31) >> 5, i = g + lane * step;
+        const int at = p.group_start[min(i, p.n_groups - 1)];
+        // the first probe is taken for granted; what is out of order is found out below
+        const uint32_t below = __ballot_sync(0xffffffffu, lane * step < size && i < p.n_groups && at <= b) | 1u;
+        g += (31 - __clz(below)) * step;
+        size = step;
+      }
+    } else {
+      while (end - g > 1) {
+        const int mid = (g + end) >> 1;
+        if (p.group_start[mid] <= b) g = mid; else end = mid;
+      }
     }
+  }
+  if (!p.kv_len) len = q1 - q0;
+  const bool fits = q0 >= 0 && q1 >= q0 && q1 <= p.T && q1 - q0 <= p.max_q && len >= 0 && len <= p.max_kv;
+  if (GEN && p.phase == kOwn) {
     AttnGroup r;
-    if (p.group_start[g] <= b) {
-      if (!attn_group(p, g, r)) return s;
+    const int first = p.group_start[g];
+    const bool sound = attn_group(p, g, r);
+    if (!fits) return s;
+    if (first <= b) {
+      if (!sound) return s;
       if (b < r.last) {
         if (q0 < r.q0 || q1 > r.q1) return s;
         s.lo = r.keys;
@@ -122,6 +143,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
       return s;
     }
   }
+  if (!fits) return s;
   s.q0 = q0;
   s.n_q = q1 - q0;
   s.len = len;

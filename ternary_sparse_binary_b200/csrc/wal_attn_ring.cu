@@ -76,7 +76,7 @@ __device__ __forceinline__ void attn_ring(const AttnParams& p, uint8_t* smem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const AttnSeq s = attn_seq<true>(p, b);
+  const AttnSeq s = attn_seq<true, true>(p, b);
   if (p.clear) {
     if (split == 0 && h == 0 && b == 0 && threadIdx.x == 0 && !p.part_first) *p.status = 0;
   } else if (s.bad && h == 0 && threadIdx.x == 0 && p.status) {
