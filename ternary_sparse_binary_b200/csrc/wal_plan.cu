@@ -324,6 +324,11 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const __grid_constant
 constexpr int kSmall = 512;       // sequences
 constexpr int kSmallRows = 8192;  // rows
 constexpr int kStarts = 16384;  // sequences whose places fit in shared memory beside the sums
+constexpr int kMostSeqs = 65535;
+constexpr int plan_smem(int B, int per) { return 4 * (5 * per + (B <= kStarts ? 2 * B : 0)); }
+// The limit that is set is the same for every call: two threads may set it at once.
+constexpr int kPlanSmem = std::max(plan_smem(kStarts, kStarts / kCluster), plan_smem(kMostSeqs, (kMostSeqs + kCluster - 1) / kCluster));
+static_assert(kPlanSmem <= 230000 && plan_smem(kSmall, kSmall) <= 48 << 10, "above the shared memory of an SM, or of a launch without the attribute");
 
 }  // namespace
 }  // namespace wal
@@ -335,7 +340,7 @@ extern "C" int wal_kv_plan(const wal_kv_cache* cache, const int32_t* n_new, cons
                            int32_t* slots, int32_t* kv_len_out, int32_t* n_free_out, void* ws, size_t ws_bytes, wal_stream_t stream) {
   int st = check_cache(cache);
   if (st) return st;
-  if (B < 1 || B > 65535 || T < 0 || max_kv < 1) return fail(WAL_ERR_SHAPE, "1 <= B <= 65535, T >= 0 and max_kv >= 1");
+  if (B < 1 || B > kMostSeqs || T < 0 || max_kv < 1) return fail(WAL_ERR_SHAPE, "1 <= B <= 65535, T >= 0 and max_kv >= 1");
   if (T == 0x7FFFFFFF) return fail(WAL_ERR_UNSUPPORTED, "T must be below 2^31 - 1");
   if (max_kv > 1 << 30) return fail(WAL_ERR_UNSUPPORTED, "at most 2^30 tokens a sequence");
   for (const void* a : {(const void*)n_new, (const void*)kv_len, (const void*)table, (const void*)free_pages, (const void*)n_free,
@@ -365,7 +370,7 @@ extern "C" int wal_kv_plan(const wal_kv_cache* cache, const int32_t* n_new, cons
   cfg.gridDim = dim3(small ? 1 : kCluster);
   const int most = std::min(kMaxThreads, (std::max(B, T) + 31) / 32 * 32);
   cfg.blockDim = dim3(small ? most : kMaxThreads);
-  cfg.dynamicSmemBytes = (size_t)4 * (5 * p.per + (p.starts ? 2 * B : 0));
+  cfg.dynamicSmemBytes = (size_t)plan_smem(B, p.per);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -376,7 +381,7 @@ extern "C" int wal_kv_plan(const wal_kv_cache* cache, const int32_t* n_new, cons
   } else {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaFuncSetAttribute(plan_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    e = cudaFuncSetAttribute(plan_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, plan_kernel<kCluster>, p);
   }
   if (e != cudaSuccess) return fail(WAL_ERR_CUDA, std::string("plan_kernel launch: ") + cudaGetErrorString(e));

@@ -201,7 +201,7 @@ def test_plan_arrays_of_any_alignment():
             assert need.max() <= 4
 
 
-@pytest.mark.parametrize("B", [31, 32, 33, 511, 512, 513, 1024, 1025])
+@pytest.mark.parametrize("B", [31, 32, 33, 511, 512, 513, 1024, 1025, 16384, 16385])
 def test_plan_sizes_of_a_warp_and_a_cta(B):
     """Sequences around what a warp's probes, a CTA and a cluster take; most of them want nothing."""
     w = wal()
