@@ -125,7 +125,6 @@ class Rope:
             _abi.wal_rope(self.desc, x.data_ptr(), xt, T, width // self.head_dim, ldx,
                           _index(positions, "positions", T), out.data_ptr(), ldo, s)
 
-
     def apply_qk(self, q, k, positions, q_out, k_out, norm=None, stream=None):
         """q_out and k_out (bf16) = q and k (fp32 or bf16), each head normalised by `norm` (a HeadNorm) and
         rotated, [tokens, heads * head_dim]; a bf16 input may be its own output."""

@@ -638,7 +638,9 @@ void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int
 // and 4096 (one) 58.3, 63.5, 67.7, 63.6; heads of 64 (two) 39.5, 31.9, 30.7, 36.7.
 // Where they are ragged, so many that twice the CTAs at a time have keys: the same slots
 // with a window beyond their up to 32768 tokens take 248 us in two splits, 172, 154, 145
-// and 150 in three, four, eight (it takes seven) and sixteen.
+// and 150 in three, four, eight (it takes seven) and sixteen.  But not into pieces below
+// 512 keys beyond what fills the SMs once: 30 sequences of up to 1000 e4m3 keys, 16 heads
+// of 64, take 20.4, 19.6 and 21.9 us in one, two (it takes these) and four splits.
 struct Split {
   int n, keys;
 };
@@ -652,6 +654,7 @@ Split plan_general(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, 
   }
   const int64_t pieces = (int64_t)B * c.n_heads, tiles = ((int64_t)max_kv + 127) / 128, slots = kPlanSms * ring_ctas(c.head_dim, rows);
   int64_t n = std::min(tiles, std::max<int64_t>(1, slots * 7 / (2 * pieces)));
+  n = std::min(n, std::max((slots + pieces - 1) / pieces, tiles / 4));
   if (even) {
     const bool codes = c.type != WAL_KV_BF16;
     const double bytes = (double)pieces * max_kv * (2 * c.head_dim * (codes ? 1 : 2) + (codes ? 8 : 0)) / 6e6;
