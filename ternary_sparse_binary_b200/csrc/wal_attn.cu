@@ -634,11 +634,11 @@ void plan_split(const wal_kv_cache& c, int n_heads, int T, int B, int max_q, int
 // the least estimate: the keys' bytes at 6 TB/s, or rounds of CTAs of 4 us and a time a
 // key, whichever is longer, and 7 us for the second kernel.  25 slots, int8 pages, 32 q
 // heads of 128 on 8, in one, two, three and four splits: window of 4096 (it takes two)
-// 52.6, 46.5, 53.3 and 50.1 us; window of 1024 (one) 17.6, 19.1, 21.1, 21.0; bf16 pages
-// and 4096 (one) 58.3, 63.5, 67.7, 63.6; heads of 64 (two) 39.5, 31.9, 30.7, 36.7.
+// 53.1, 44.3, 50.3 and 48.3 us; window of 1024 (one) 17.4, 17.9, 19.3, 19.3; bf16 pages
+// and 4096 (one) 63.1, 68.1, 68.7, 67.5; heads of 64 (two) 40.2, 31.1, 29.3, 35.7.
 // Where they are ragged, so many that twice the CTAs at a time have keys: the same slots
-// with a window beyond their up to 32768 tokens take 248 us in two splits, 172, 154, 145
-// and 150 in three, four, eight (it takes seven) and sixteen.  But not into pieces below
+// with a window beyond their up to 32768 tokens take 246 us in two splits, 170, 150, 142
+// and 146 in three, four, eight (it takes seven: 148) and sixteen.  But not into pieces below
 // 512 keys beyond what fills the SMs once: 30 sequences of up to 1000 e4m3 keys, 16 heads
 // of 64, take 20.4, 19.6 and 21.9 us in one, two (it takes these) and four splits.
 struct Split {
@@ -841,8 +841,8 @@ int attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_h
 // at 6 TB/s of half its bounds.  More CTAs than half of the SMs, where two of them share
 // a pair of SMs, count a third more beside other work.  64 slots with up to 2048 tokens of
 // their own, 32 q heads of 128 on 8, behind 16384 shared int8 keys: in six, eight, nine
-// (which it takes), ten and sixteen splits 89, 74, 76, 85 and 87 us; over bf16 pages in
-// six, eight (seven), ten and twelve 81, 78, 80 and 83.
+// (which it takes), ten and sixteen splits 92, 76, 73, 87 and 90 us; over bf16 pages in
+// six, seven (it takes these), eight, ten and twelve 77, 72, 74, 77 and 82.
 struct SharedPlan {
   Split prefix, own;  // prefix.n is 0 where there is none
 };
