@@ -22,9 +22,9 @@ constexpr int kRowWarps = 4;
 // few query rows: keys split over CTAs, mma.sync
 // ---------------------------------------------------------------------------
 // Bound by bytes over bf16 (25 sequences of up to 16384 keys, 8 heads of 128: 133 us,
-// 0.93 of the copy rate) and by latency over codes (up to 32768 int8 keys: 179 us,
+// 0.93 of the copy rate) and by latency over codes (up to 32768 int8 keys: 177 us,
 // 0.71; registers allow 8 warps an SM, which use 41 % of the issue slots); one
-// sequence of 2048 keys takes 8.9 us of a graph, both kernels.
+// sequence of 2048 keys takes 7.4 us of a graph, both kernels.
 // A CTA takes one (sequence, K/V head, split of the keys) and its 8 * NT query
 // rows at most; its four warps take steps of 16 * MT keys in turn.  The keys
 // are the M side of both products, so the few query rows waste little:
