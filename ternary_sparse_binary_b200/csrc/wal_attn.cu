@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
     }
   };
   load(warp % PER);
+  const int fall = GEN && p.phase == kOwn ? __ldcg(p.status + kGroupsFall) : 0;
   float mm = -INFINITY;
   for (int i = lane; i < n; i += 32) mm = fmaxf(mm, p.part_ml[part(i)].x);
 #pragma unroll
@@ -498,6 +499,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
       for (int k = 0; k < VPL; ++k) acc[k] += s_o[i][lane * VPL + k];
     }
   }
+  if (GEN && fall) return;
   finish_row<D, GEN>(p, s, b, head, tok, acc, ll);
 }
 

@@ -134,8 +134,6 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
         if (q0 < r.q0 || q1 > r.q1) return s;
         s.lo = r.keys;
         s.head = r.first;
-      } else if (g != p.n_groups - 1) {
-        return s;
       }
     }
     if (len - (q1 - q0) < s.lo || len - s.lo > p.max_own) {
@@ -149,6 +147,23 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
   s.len = len;
   s.bad = false;
   return s;
+}
+// Where the starts of a shared call's groups fall, it is open whose a sequence is: all of
+// them are left out then.  The two launches may take a sequence for any group's, within
+// all bounds, and leave partial results of two groups in one row; nobody reads them, as the
+// joining kernel finds this word, which the second launch's first CTA leaves at its end
+// (one warp does: the first launch, which cleared the status word, is waited for).
+constexpr int kGroupsFall = 32;  // place of the word behind the status word
+__device__ __forceinline__ void attn_groups_end(const AttnParams& p) {
+  const int lane = threadIdx.x & 31;
+  int fall = 0;
+#pragma unroll 4
+  for (int g = lane; g < p.n_groups; g += 32) fall |= p.group_start[g + 1] < p.group_start[g];
+  fall = __any_sync(0xffffffffu, fall);
+  if (p.part_first) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (lane) return;
+  p.status[kGroupsFall] = fall;
+  if (fall) attn_report(p.status);
 }
 // Keys that new token i sees: the first attn_limit(s, i) of the sequence.
 __device__ __forceinline__ int attn_limit(const AttnSeq& s, int i) { return max(0, s.len - s.n_q + i + 1); }

@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, RingCfg<D, TYPE, NT>::ctas) at
   attn_ring<D, TYPE, NT>(p, ring_smem);
   // The second launch of a shared call starts beside the first.  Its first CTA waits for
   // that, so that what comes after the second comes after both.
-  if (p.part_first && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.phase == kOwn && threadIdx.x < 32 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) attn_groups_end(p);
 }
 
 template <int D, int TYPE, int NT>

@@ -1078,7 +1078,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
   // The second launch of a shared call starts beside the first; what comes after it must come after both.
-  if (GEN && p.part_first && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (GEN && p.phase == kOwn && warp == 0 && blockIdx.x == 0) attn_groups_end(p);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,37 @@
+"""A serving step's operators at the edges of what their header allows (needs a B200)."""
+import pytest
+import torch
+
+from gpu_util import needs_gpu, wal
+from test_gpu_attention import i32
+from test_gpu_shared import Batch
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+
+def recorded(b, skip=(), ws=None, **change):
+    """A call that records WAL_ERR_ARG, leaves the sequences of `skip` unwritten and answers the others; the next
+    one with the same workspace is clean."""
+    w = wal()
+    ws = b.ws() if ws is None else ws
+    O = b.call(ws, **change)
+    with pytest.raises(w.WalError) as e:
+        w.attention.status(ws)
+    assert e.value.status == w.WAL_ERR_ARG
+    b.check(O, skip=skip)
+    b.check(b.call(ws))
+    w.attention.status(ws)
+
+
+# ---- shared calls: malformed groups ----------------------------------------------------
+
+@pytest.mark.parametrize("typ", ["bf16", "int8"])
+@pytest.mark.parametrize("n", [1, 30])
+@pytest.mark.parametrize("starts", [[0, 5, 3, 8], [0, 5, 5, 3, 8], [0, 8, 0, 8], [4, 3, 8, 8], [0, 4, 8, 7], [0, 8, 8, 8, 5, 8, 8], [3, 8, 8, 0]])
+def test_group_starts_that_fall(starts, n, typ):
+    """Nobody knows whose the sequences between are, so all are left out, by every kernel: at 4 and at more than 16
+    query rows a head, with neighbouring groups of different prefixes."""
+    b = Batch([(500, [(n, n + 3), (n, n + 50), (1, 200)]), (96, [(1, 9), (1, 20), (n, n + 300), (n, n), (1, 700)])], D=64, typ=typ, seed=n)
+    prefix = [500, 96, 32, 500, 0, 64][:len(starts) - 1]
+    recorded(b, range(8), group_start=i32(starts), prefix_len=i32(prefix), max_own=b.bounds["max_kv"],
+             ws=torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda"))
