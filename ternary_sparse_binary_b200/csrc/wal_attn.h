@@ -109,7 +109,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
       for (int size = end; size > 1;) {
         const int step = (size + 31) >> 5, i = g + lane * step;
         const int at = p.group_start[min(i, p.n_groups - 1)];
-        // the first probe is taken for granted; what is out of order is found out below
+        // the first probe is taken for granted: `first` tells below
         const uint32_t below = __ballot_sync(0xffffffffu, lane * step < size && i < p.n_groups && at <= b) | 1u;
         g += (31 - __clz(below)) * step;
         size = step;
@@ -128,13 +128,10 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
     const int first = p.group_start[g];
     const bool sound = attn_group(p, g, r);
     if (!fits) return s;
-    if (first <= b) {
-      if (!sound) return s;
-      if (b < r.last) {
-        if (q0 < r.q0 || q1 > r.q1) return s;
-        s.lo = r.keys;
-        s.head = r.first;
-      }
+    if (first <= b && b < r.last) {  // behind the last group, a sequence shares nothing whatever that group holds
+      if (!sound || q0 < r.q0 || q1 > r.q1) return s;
+      s.lo = r.keys;
+      s.head = r.first;
     }
     if (len - (q1 - q0) < s.lo || len - s.lo > p.max_own) {
       s.lo = 0;

@@ -35,3 +35,15 @@ def test_group_starts_that_fall(starts, n, typ):
     prefix = [500, 96, 32, 500, 0, 64][:len(starts) - 1]
     recorded(b, range(8), group_start=i32(starts), prefix_len=i32(prefix), max_own=b.bounds["max_kv"],
              ws=torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_sequences_behind_a_malformed_last_group(n):
+    """They are in no group, whatever that one holds."""
+    b = Batch([(100, [(n, n + 3), (n, n + 50)]), (64, [(1, 9), (n, n)])], alone=[(1, 40)], after=[(n, n + 33), (1, 1)], D=64)
+    for bad in (-1, b.bounds["max_prefix"] + 1):
+        recorded(b, [3, 4], prefix_len=i32([100, bad]))
+    # one group, from -1 to 3: the sequences from 3 on share nothing, but what they hold behind a prefix of others is
+    # not in their rows of the table
+    b = Batch([(0, [(n, n + 3), (1, 50), (n, n)])], after=[(n, n + 33), (1, 1)], D=64)
+    recorded(b, [0, 1, 2], group_start=i32([-1, 3]))
