@@ -628,8 +628,8 @@ int wal_attn_prompt_window(const uint16_t* Q, const uint16_t* K, const uint16_t*
  * or whose rows do not lie within its group's, is left out like one of wal_attn_paged;
  * so are all of a group whose start values leave [0, B] or whose prefix_len is outside
  * [0, max_prefix], and all sequences of the call if the start values fall anywhere.
- * Rows of a group's sequences follow one another in Q.  The workspace is required when
- * T > 0. */
+ * Such groups are recorded without sequences too.  Rows of a group's sequences follow one
+ * another in Q.  The workspace is required when T > 0. */
 size_t wal_attn_paged_shared_workspace_bytes(const wal_kv_cache* cache, int n_heads, int T, int B, int G, int max_q,
                                              int max_prefix, int max_own);
 int wal_attn_paged_shared(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,

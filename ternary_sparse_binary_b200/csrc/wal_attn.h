@@ -149,18 +149,24 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
 // them are left out then.  The two launches may take a sequence for any group's, within
 // all bounds, and leave partial results of two groups in one row; nobody reads them, as the
 // joining kernel finds this word, which the second launch's first CTA leaves at its end
-// (one warp does: the first launch, which cleared the status word, is waited for).
+// (one warp does: the first launch, which cleared the status word, is waited for).  It also
+// reports groups that are out of range, which may have no sequence to report them.
 constexpr int kGroupsFall = 32;  // place of the word behind the status word
 __device__ __forceinline__ void attn_groups_end(const AttnParams& p) {
   const int lane = threadIdx.x & 31;
-  int fall = 0;
-#pragma unroll 4
-  for (int g = lane; g < p.n_groups; g += 32) fall |= p.group_start[g + 1] < p.group_start[g];
+  int fall = 0, bad = 0;
+#pragma unroll 2
+  for (int i = lane; i < p.n_groups; i += 32) {
+    AttnGroup g;
+    bad |= !attn_group(p, i, g);
+    fall |= g.last < g.first;
+  }
   fall = __any_sync(0xffffffffu, fall);
+  bad = __any_sync(0xffffffffu, bad);
   if (p.part_first) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (lane) return;
   p.status[kGroupsFall] = fall;
-  if (fall) attn_report(p.status);
+  if (bad) attn_report(p.status);
 }
 // Keys that new token i sees: the first attn_limit(s, i) of the sequence.
 __device__ __forceinline__ int attn_limit(const AttnSeq& s, int i) { return max(0, s.len - s.n_q + i + 1); }

@@ -47,3 +47,15 @@ def test_sequences_behind_a_malformed_last_group(n):
     # not in their rows of the table
     b = Batch([(0, [(n, n + 3), (1, 50), (n, n)])], after=[(n, n + 33), (1, 1)], D=64)
     recorded(b, [0, 1, 2], group_start=i32([-1, 3]))
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_malformed_groups_without_sequences(n):
+    """Nothing is left out, and they are recorded."""
+    b = Batch([(100, [(n, n + 3), (n, n + 50)]), (64, []), (32, [(1, 9), (n, n)]), (10, [])], alone=[(1, 40)], after=[(n, n + 33)], D=64)
+    for at in (1, 3):
+        for bad in (-1, b.bounds["max_prefix"] + 1):
+            recorded(b, prefix_len=i32([100, 64, 32, 10][:at] + [bad] + [100, 64, 32, 10][at + 1:]))
+    b = Batch([(0, []), (100, [(n, n + 3), (n, n + 50)]), (50, [])], D=64)
+    recorded(b, group_start=i32([-1, 0, 2, 2]))
+    recorded(b, group_start=i32([0, 0, 2, 3]))
