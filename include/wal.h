@@ -624,8 +624,8 @@ int wal_attn_prompt_window(const uint16_t* Q, const uint16_t* K, const uint16_t*
  * group_start[0] or from group_start[G] on, share nothing.
  * Bounds: max_kv of kv_len, max_prefix >= 0 of prefix_len, max_own >= 1 of the tokens
  * behind the prefix; ceil(max_kv / page_size) <= ld_table; 1 <= G <= 65535.
- * A sequence whose new tokens are not all behind its group's prefix, that breaks a bound,
- * or whose rows do not lie within its group's, is left out like one of wal_attn_paged;
+ * A sequence that shares tokens and whose new ones are not all behind them, that breaks a
+ * bound, or whose rows do not lie within its group's, is left out like one of wal_attn_paged;
  * so are all of a group whose start values leave [0, B] or whose prefix_len is outside
  * [0, max_prefix], and all sequences of the call if the start values fall anywhere.
  * Such groups are recorded without sequences too.  Rows of a group's sequences follow one

@@ -133,7 +133,8 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
       s.lo = r.keys;
       s.head = r.first;
     }
-    if (len - (q1 - q0) < s.lo || len - s.lo > p.max_own) {
+    // without shared keys, tokens before the first key see nothing, as elsewhere
+    if ((s.lo && len - (q1 - q0) < s.lo) || len - s.lo > p.max_own) {
       s.lo = 0;
       return s;
     }

@@ -2,8 +2,9 @@
 import pytest
 import torch
 
+from attn_util import TYPES
 from gpu_util import needs_gpu, wal
-from test_gpu_attention import i32
+from test_gpu_attention import SENTINEL, i32
 from test_gpu_shared import Batch
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
@@ -59,3 +60,23 @@ def test_malformed_groups_without_sequences(n):
     b = Batch([(0, []), (100, [(n, n + 3), (n, n + 50)]), (50, [])], D=64)
     recorded(b, group_start=i32([-1, 0, 2, 2]))
     recorded(b, group_start=i32([0, 0, 2, 3]))
+
+
+# ---- shared calls: sequences that share nothing ---------------------------------------
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("n", [1, 30])
+def test_more_new_tokens_than_keys_without_a_prefix(n, typ):
+    """As attend() answers them: the tokens before the first key see nothing and get zeros."""
+    w = wal()
+    b = Batch([(0, [(n + 4, 2), (3, 0), (1, 5)]), (100, [(n, n + 3), (1, 20)])], alone=[(n + 2, 1), (2, 0)], after=[(n + 9, n)], D=64, typ=typ)
+    ws = b.ws()
+    O = b.call(ws)
+    w.attention.status(ws)
+    b.check(O)
+    ref = torch.full_like(O, SENTINEL)
+    few = dict(q_start=b.args["q_start"][:6].contiguous(), kv_len=b.args["kv_len"][:5].contiguous(), table=b.args["table"][:5])
+    b.cache.attend(b.Q[:, :512], out=ref[:, :512], max_q=b.bounds["max_q"], max_kv=b.bounds["max_kv"], **few)
+    for seq, rows in ((0, n + 1), (1, 2), (2, n + 2), (3, 3)):
+        at = slice(b.start[seq], b.start[seq] + rows)
+        assert torch.all(O[at, :512] == 0) and torch.all(ref[at, :512] == 0)
