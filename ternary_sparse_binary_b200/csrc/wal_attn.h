@@ -133,8 +133,9 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
       s.lo = r.keys;
       s.head = r.first;
     }
-    // without shared keys, tokens before the first key see nothing, as elsewhere
-    if ((s.lo && len - (q1 - q0) < s.lo) || len - s.lo > p.max_own) {
+    // Without shared keys, tokens before the first key see nothing, as elsewhere.  A
+    // sequence without new tokens may hold less than its group shares.
+    if ((s.lo && q1 > q0 && len - (q1 - q0) < s.lo) || len - s.lo > p.max_own) {
       s.lo = 0;
       return s;
     }

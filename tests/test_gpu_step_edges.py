@@ -80,3 +80,16 @@ def test_more_new_tokens_than_keys_without_a_prefix(n, typ):
     for seq, rows in ((0, n + 1), (1, 2), (2, n + 2), (3, 3)):
         at = slice(b.start[seq], b.start[seq] + rows)
         assert torch.all(O[at, :512] == 0) and torch.all(ref[at, :512] == 0)
+
+
+@pytest.mark.parametrize("n", [1, 30])
+@pytest.mark.parametrize("held", [0, 40, 100])
+def test_idle_sequences_of_a_group(held, n):
+    """A finished request that stays in its place, with less than the shared tokens or none: nothing to answer or record."""
+    w = wal()
+    b = Batch([(100, [(n, n + 3), (0, 7), (1, 50), (0, 0)]), (64, [(0, 20), (n, n)])], D=64)
+    lens = [held if q == 0 else v for q, v in zip(b.n_q, b.lens)]
+    ws = b.ws()
+    O = b.call(ws, kv_len=i32(lens))
+    w.attention.status(ws)
+    b.check(O)
