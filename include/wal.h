@@ -509,7 +509,8 @@ size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, in
  * A sequence whose starts decrease or leave [0, T], with more than max_q new
  * tokens, or with kv_len outside [0, max_kv] is left out, its rows unwritten;
  * a page id outside [0, n_pages) makes its sequence's rows unspecified; both
- * record WAL_ERR_ARG.  n_heads / n_kv_heads <= 128.  O must not overlap Q.
+ * record WAL_ERR_ARG.  The table row of a sequence without new tokens is not looked
+ * at.  n_heads / n_kv_heads <= 128.  O must not overlap Q.
  * Results do not depend on timing (no atomics on values).  Asynchronous. */
 int wal_attn_paged(const wal_kv_cache* cache, const uint16_t* Q, int n_heads, int T, int ldq,
                    const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int ld_table, int B,

@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) attn_combine_kernel(const __gr
     auto look = [&](int row, int from, int to) {
       for (int i = from + threadIdx.x; i < to; i += 32 * kRowWarps) bad |= (uint32_t)__ldg(p.table + row * p.ld_table + i) >= (uint32_t)p.n_pages;
     };
-    if (!GEN) {
+    if (!GEN && s.n_q > 0) {
       look(b, 0, pages);
     } else if (s.n_q > 0) {  // the pages of keys that some row sees
       const int low = attn_low(p, s, attn_limit(s, 0)), first = p.phase == kOwn ? s.lo : min(p.sinks, s.len);

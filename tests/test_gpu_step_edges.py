@@ -6,6 +6,7 @@ from attn_util import TYPES
 from gpu_util import needs_gpu, wal
 from test_gpu_attention import SENTINEL, i32
 from test_gpu_shared import Batch
+from test_gpu_window import run_paged
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
 
@@ -93,3 +94,14 @@ def test_idle_sequences_of_a_group(held, n):
     O = b.call(ws, kv_len=i32(lens))
     w.attention.status(ws)
     b.check(O)
+
+
+# ---- windows ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("window", [50, 4999, 5000, 100000])
+def test_pages_of_idle_sequences_may_be_gone(window, n, typ):
+    """A sequence without new tokens sees no page, with a window shorter than its context or not."""
+    run_paged([5000, 3000, 700], [n, 0, n], window, 0, typ=typ, seed=window)
+    run_paged([5000, 3000, 700], [n, 0, n], window, 5000, typ=typ, seed=window)
