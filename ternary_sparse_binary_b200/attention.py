@@ -253,6 +253,7 @@ class KvCache:
     def read(self, table, start, k_out, v_out, max_len, ws=None, stream=None):
         """Rows start[b] .. start[b + 1] - 1 of k_out and v_out (fp32 or bf16) = the first tokens of sequence b."""
         B = start.numel() - 1
+        _fits(max_len, "max_len")
         kt, ldk, T, width = _rows(k_out, "k_out")
         vt, ldv, *shape = _rows(v_out, "v_out")
         if vt != kt or shape != [T, width] or width != self.n_heads * self.head_dim:
@@ -289,7 +290,7 @@ class KvCache:
         `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence."""
         ldq, ldo, T, n_heads = self._tokens(q, out)
         B = kv_len.numel()
-        _fits(max_q, "max_q")
+        _fits(max(max_q, max_kv), "bounds")
         seen = () if window is None else _window(window, sinks)
         tp, ldt = _table(table, B, max_kv, self.page_size)
         guard, s = _enter(stream, self.k, q, q_start, kv_len, table, out)
@@ -313,7 +314,7 @@ class KvCache:
         pages of the first of them; max_own bounds the tokens behind."""
         ldq, ldo, T, n_heads = self._tokens(q, out)
         B, G = kv_len.numel(), prefix_len.numel()
-        _fits(max(max_q, max_prefix, max_own), "bounds")
+        _fits(max(max_q, max_kv, max_prefix, max_own), "bounds")
         tp, ldt = _table(table, B, max_kv, self.page_size)
         guard, s = _enter(stream, self.k, q, q_start, kv_len, table, group_start, prefix_len, out)
         if ws is None:
