@@ -88,9 +88,10 @@ def _scratch(n, like, stream):
 
 
 def _window(window, sinks):
-    if window < 1 or sinks < 0:
+    """A windowed call's arguments; none without a window, where the first keys are seen as all others are."""
+    if sinks < 0 or (window is not None and window < 1):
         raise ValueError("window must be at least 1 and sinks at least 0")
-    return min(window, _INT), min(sinks, _INT)  # beyond any sequence either way
+    return () if window is None else (min(window, _INT), min(sinks, _INT))  # beyond any sequence either way
 
 
 def status(ws, stream=None):
@@ -280,18 +281,19 @@ class KvCache:
     def attend_workspace_bytes(self, n_heads, T, B, max_q, max_kv, window=None, sinks=0):
         """Bytes of a `ws` for attend.  Not monotone: a smaller batch may need more (its keys are split
         further), so one `ws` for several shapes takes the largest of their sizes."""
-        if window is None:
-            return self._bytes(_abi.wal_attn_paged_workspace_bytes, n_heads, T, B, max_q, max_kv)
-        return self._bytes(_abi.wal_attn_paged_window_workspace_bytes, n_heads, T, B, max_q, max_kv, *_window(window, sinks))
+        seen = _window(window, sinks)
+        fn = _abi.wal_attn_paged_window_workspace_bytes if seen else _abi.wal_attn_paged_workspace_bytes
+        return self._bytes(fn, n_heads, T, B, max_q, max_kv, *seen)
 
     def attend(self, q, q_start, kv_len, table, out, max_q, max_kv, scale=None, ws=None, stream=None, window=None, sinks=0):
         """out (bf16) = attention of the new tokens' q (bf16) [tokens, n_heads * head_dim] over the cache;
         rows q_start[b] .. q_start[b + 1] - 1 are the last tokens of sequence b's kv_len[b].  With a
-        `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence."""
+        `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence; without
+        one it sees all, and `sinks` changes nothing."""
         ldq, ldo, T, n_heads = self._tokens(q, out)
         B = kv_len.numel()
         _fits(max(max_q, max_kv), "bounds")
-        seen = () if window is None else _window(window, sinks)
+        seen = _window(window, sinks)
         tp, ldt = _table(table, B, max_kv, self.page_size)
         guard, s = _enter(stream, self.k, q, q_start, kv_len, table, out)
         if ws is None:
@@ -339,7 +341,8 @@ class KvCache:
 def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, stream=None, window=None, sinks=0):
     """out (bf16) = causal attention over packed prompts; q and out [tokens, n_heads * head_dim],
     k and v [tokens, n_kv_heads * head_dim], sequence b in rows start[b] .. start[b + 1] - 1.  With a
-    `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence."""
+    `window`, a token sees that many keys up to its own, and the first `sinks` of its sequence; without one
+    it sees all, and `sinks` changes nothing."""
     _, ldq, T, width = _rows(q, "q", _BF16)
     _, ldk, *k_shape = _rows(k, "k", _BF16)
     _, ldv, *v_shape = _rows(v, "v", _BF16)
@@ -347,7 +350,7 @@ def attn_prompt(q, k, v, start, out, head_dim, max_len, scale=None, ws=None, str
     if shape != [T, width] or k_shape != v_shape or k_shape[0] != T or width % head_dim or k_shape[1] % head_dim:
         raise ValueError("q and out: [tokens, n_heads * head_dim]; k and v: [tokens, n_kv_heads * head_dim]")
     _fits(max_len, "max_len")
-    seen = () if window is None else _window(window, sinks)
+    seen = _window(window, sinks)
     guard, s = _enter(stream, q, k, v, start, out)
     wp, wn = _ws(ws, q)
     call = _abi.wal_attn_prompt if window is None else _abi.wal_attn_prompt_window

@@ -28,3 +28,12 @@ def test_bounds_past_32_bits(max_kv, ws):
     refused("fit", c.attend, **wide, window=9)
     refused("fit", c.attend_shared, **wide, group_start=i(2), prefix_len=i(1), max_prefix=16, max_own=48)
     refused("fit", c.read, table=WIDE, start=i(3), k_out=f(3, 128), v_out=f(3, 128), max_len=max_kv, ws=ws)
+
+
+def test_sinks_are_checked_without_a_window_too():
+    c = cache()
+    refused("sinks", c.attend, **ATTEND, sinks=-1)
+    refused("sinks", c.attend_workspace_bytes, n_heads=4, T=3, B=2, max_q=2, max_kv=64, sinks=-1)
+    refused("sinks", wal.attn_prompt, q=f(3, 256), k=f(3, 128), v=f(3, 128), start=i(2), out=f(3, 256), head_dim=64, max_len=3, sinks=-1)
+    # without a window every key is seen, the first ones among them: the size is that of the call without them
+    assert c.attend_workspace_bytes(4, 3, 2, 2, 64, sinks=4) == c.attend_workspace_bytes(4, 3, 2, 2, 64)
