@@ -96,6 +96,20 @@ def test_idle_sequences_of_a_group(held, n):
     b.check(O)
 
 
+def test_many_groups():
+    """More than a warp's probes squared; one out of range and one that falls among them."""
+    w = wal()
+    groups = [(3 + g % 40, [(1, 1 + g % 7)] * (g % 3)) for g in range(1500)]
+    b = Batch(groups, alone=[(1, 9)], after=[(1, 4)], heads=2, kv_heads=1, D=64, page=16)
+    ws = b.ws()
+    O = b.call(ws)
+    w.attention.status(ws)
+    b.check(O)
+    for g in (1023, 1499):
+        recorded(b, range(b.starts[g], b.starts[g + 1]), ws, prefix_len=i32(b.prefix[:g] + [-1] + b.prefix[g + 1:]))
+        recorded(b, range(len(b.lens)), ws, group_start=i32(b.starts[:g] + [b.starts[g + 1] + 1] + b.starts[g + 1:]))
+
+
 # ---- windows ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("typ", list(TYPES))
