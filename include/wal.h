@@ -500,8 +500,9 @@ size_t wal_attn_paged_workspace_bytes(const wal_kv_cache* cache, int n_heads, in
  * token i sees the keys j <= kv_len[b] - (q_start[b + 1] - q_start[b]) + i.
  *   O[t][h] = sum_j softmax_j(scale * Q[t][h] . K[j]) V[j]       (bf16 [T][ldo])
  * with the maximum, the sum and the accumulators in fp32, and each softmax
- * weight rounded to bf16 (or fp16) for its product with V.  A row that sees no key gets
- * zeros.  Keys a row does not see never reach it, whatever they hold.
+ * weight rounded to bf16 for its product with V (few tokens over 8-bit pages: times V's
+ * scale, to fp16, which keeps 2^-25 of the row's largest such product).  A row that sees
+ * no key gets zeros.  Keys a row does not see never reach it, whatever they hold.
  * 1 <= B <= 65535; max_q >= 1 and 1 <= max_kv <= 2^30 bound the lengths (they size the
  * grid and the workspace), ceil(max_kv / page_size) <= ld_table.  Rows of no sequence
  * (before q_start[0] or from q_start[B] on) are left as they are.  With T = 0
@@ -561,9 +562,13 @@ int wal_attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int
  * sequence that finds too little and all growing ones after it; dropped tokens and their
  * pages go through.  If n_free is outside [0, n_pages], or the list would become longer
  * than that, all are left out.  A page id outside [0, n_pages) moves as it is, and the
- * rows in that page get the slot -1.  All of these record WAL_ERR_ARG.  Pages that
- * several sequences hold are given back once for each: whoever shares pages drops tokens
- * down to the shared ones only.
+ * rows in that page get the slot -1.  All of these record WAL_ERR_ARG.
+ *   The plan knows a page by its entry alone: those that several sequences hold are given
+ * back once for each, and those that a window has left behind are given back although
+ * their caller may have put them on the list, or given them to others, long ago.  Whoever
+ * shares pages or takes them back early drops a request's tokens only down to the last
+ * such page, then puts back what it still holds in front of it and sets kv_len (between
+ * calls the caller may write every array).
  * 1 <= B <= 65535, T < 2^31 - 1, 1 <= max_kv <= 2^30, ceil(max_kv / page_size) <=
  * ld_table.  The cache's pages are not touched.  ws: NULL, or at least 512 bytes.
  * Asynchronous. */
@@ -623,8 +628,9 @@ int wal_attn_prompt_window(const uint16_t* Q, const uint16_t* K, const uint16_t*
  * the other rows only the pages from the prefix's end on are looked at (a prefix need not
  * end with a page).  kv_len counts the shared tokens too.  Sequences of no group, before
  * group_start[0] or from group_start[G] on, share nothing.
- * Bounds: max_kv of kv_len, max_prefix >= 0 of prefix_len, max_own >= 1 of the tokens
- * behind the prefix; ceil(max_kv / page_size) <= ld_table; 1 <= G <= 65535.
+ * Bounds: max_kv of kv_len, max_prefix of prefix_len (0 <= max_prefix <= max_kv, which
+ * the size below cannot check), max_own >= 1 of the tokens behind the prefix;
+ * ceil(max_kv / page_size) <= ld_table; 1 <= G <= 65535.
  * A sequence that shares tokens and whose new ones are not all behind them, that breaks a
  * bound, or whose rows do not lie within its group's, is left out like one of wal_attn_paged;
  * so are all of a group whose start values leave [0, B] or whose prefix_len is outside

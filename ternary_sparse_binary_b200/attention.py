@@ -237,7 +237,9 @@ class KvCache:
              max_kv=None, ws=None, stream=None):
         """The plan of a step in which sequence b gets n_new[b] tokens more (or loses -n_new[b]): its pages go from
         the list `free` [n_pages] of n_free[0] pages to its row of `table`, or back; q_start, and position and slot of
-        every row of the step, are written, and the new lengths (in place without kv_len_out and n_free_out)."""
+        every row of the step, are written, and the new lengths (in place without kv_len_out and n_free_out).  It
+        gives back every page of the tokens that a sequence loses: one that shares pages, or whose pages behind a
+        window were taken from it, drops its tokens only down to the last of those; the rest is the caller's."""
         B, T = n_new.numel(), slots.numel()
         most = table.shape[-1] * self.page_size if max_kv is None else _fits(max_kv, "max_kv")
         tp, ldt = _table(table, B, most, self.page_size)
@@ -312,8 +314,8 @@ class KvCache:
     def attend_shared(self, q, q_start, kv_len, table, group_start, prefix_len, out, max_q, max_kv, max_prefix, max_own,
                       scale=None, ws=None, stream=None):
         """attend() of sequences that share their first tokens: group g is the sequences group_start[g] ..
-        group_start[g + 1] - 1, whose first prefix_len[g] tokens (at most max_prefix) are read once, from the
-        pages of the first of them; max_own bounds the tokens behind."""
+        group_start[g + 1] - 1, whose first prefix_len[g] tokens (at most max_prefix, which is at most max_kv) are
+        read once, from the pages of the first of them; max_own bounds the tokens behind."""
         ldq, ldo, T, n_heads = self._tokens(q, out)
         B, G = kv_len.numel(), prefix_len.numel()
         _fits(max(max_q, max_kv, max_prefix, max_own), "bounds")

@@ -46,6 +46,9 @@ constexpr int kRowWarps = 4;
 // at most about 1 where they count.  bf16 caches stay bf16 (m2 = m).  Weights are
 // rounded for the second product (2^-8 or 2^-11 of a weight, averaged over the
 // keys); references, l, scores and O are fp32.
+// fp16 weights below 2^-14 of the largest (in units of weight and V scale) are subnormal
+// and keep 2^-25 of it: an output to which the heavy keys' codes give next to nothing
+// has a larger relative error there.
 // References are lazy: they follow the maximum when it has grown by more than
 // 2^4, which a vote finds; most steps have no reduction and leave O alone.
 template <int D, int TYPE, int NT, int MT>
@@ -844,7 +847,9 @@ int attn_prompt(const uint16_t* Q, const uint16_t* K, const uint16_t* V, int n_h
 // a pair of SMs, count a third more beside other work.  64 slots with up to 2048 tokens of
 // their own, 32 q heads of 128 on 8, behind 16384 shared int8 keys: in six, eight, nine
 // (which it takes), ten and sixteen splits 92, 76, 73, 87 and 90 us; over bf16 pages in
-// six, seven (it takes these), eight, ten and twelve 77, 72, 74, 77 and 82.
+// six, seven (it takes these), eight, ten and twelve 77, 72, 74, 77 and 82.  These two
+// types of one batch are all that was measured: the threes and the threshold of the last
+// term are theirs, and other batches, groups and heads of 64 are planned by them unseen.
 struct SharedPlan {
   Split prefix, own;  // prefix.n is 0 where there is none
 };

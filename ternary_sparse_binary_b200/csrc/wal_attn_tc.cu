@@ -37,11 +37,13 @@
 // for the second product (2^-8 of a weight, averaged over the keys), scores, m,
 // l and O are fp32.
 //
-// Keys past a row's limit get the score -inf.  V rows past the last key of the
-// CTA are zeroed, since 0 * NaN would spread what lies there; a key that only
-// some rows see may still do that to the others, and such a row, NaN at the
-// end though its sum of weights is not, is done again from its own keys if a V
-// behind its last key is to blame (attn_last_nonfinite, attend_row).
+// Keys past a row's limit, or (GEN) between the first keys and its window, get the
+// score -inf.  V rows of places that hold no key which some row of the piece sees
+// (past its last key; GEN: also in front of its window and behind the first keys) are
+// zeroed, since 0 * NaN would spread what lies there; a key that only some rows see
+// may still do that to the others, and such a row, NaN at the end though its sum of
+// weights is not, is done again from its own keys if a V behind its last key, or in
+// front of its window, is to blame (attn_last_nonfinite, attend_row).
 //
 // All waits are bounded; one that gives up records WAL_ERR_TIMEOUT, and its
 // role stops, waits for its copies or MMAs in flight and leaves.  What the others
@@ -68,7 +70,9 @@ constexpr int kGrid = 148;      // CTAs of a launch at most; they wait for nobod
 
 // Shared memory and registers.  Launched registers are shared out again by
 // setmaxnreg: 384 threads of 168 as 256 x 208 + 128 x 88, 512 threads of 128 as
-// 256 x 176 + 256 x 80.
+// 256 x 176 + 256 x 80, in the general forms (GEN) over codes 256 x 192 + 256 x 64.
+// These four spill all the same (98 to 102 bytes stored, 152 to 156 loaded a thread):
+// the walk, the span of the keys and the groups' lookup live in every role.
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool codes = TYPE != WAL_KV_BF16;
